@@ -346,6 +346,77 @@ mok_status mok_moe_backward(const mok_layer_desc* desc, const void* dy, const vo
                             void* dw13, void* dw2, float* dgates, void* ws, size_t ws_bytes,
                             void* stream);
 
+/* ------------------------------------------------------------------ optimizer step
+ * The step that consumes the layer's gradients (the pages end with the backward pass; the update
+ * is plain AdamW, I. Loshchilov and F. Hutter, "Decoupled Weight Decay Regularization").  Tensors
+ * are given as a host array that is read before the call returns; nothing of it is kept. */
+typedef enum { MOK_ELEM_F32 = 0, MOK_ELEM_BF16 = 1 } mok_elem_type;
+typedef enum { MOK_STATE_F32 = 0, MOK_STATE_MX8 = 1 } mok_state_type;
+
+typedef struct {
+  const void* grad;   /* n contiguous elements */
+  int64_t n;          /* >= 0 */
+  int32_t grad_type;  /* mok_elem_type */
+  int32_t reserved;   /* 0 */
+} mok_grad_tensor;
+
+/* out[0] = the 2-norm of all gradients together, out[1] = min(1, max_norm / (out[0] + 1e-6)), the
+ * factor that clips them to max_norm (> 0, may be infinite), or NaN where the norm is not finite.
+ * out is f32 [2] on the device.  ws: at least MOK_GRAD_NORM_WS_BYTES, 16-byte aligned, zero-filled
+ * once before its first use (each call leaves it ready for the next).  The sums run in a fixed
+ * order, in f64 across threads. */
+#define MOK_GRAD_NORM_WS_BYTES 33024
+mok_status mok_grad_norm(const mok_grad_tensor* tensors, int32_t count, float max_norm, float* out, void* ws,
+                         size_t ws_bytes, void* stream);
+
+/* One tensor of an AdamW step, n contiguous elements:
+ *   param    f32, or bf16; with bf16, master is its f32 copy (param becomes the rounded master) or
+ *            NULL (param is then rounded at random, up or down, with the mean unchanged: a step is
+ *            mostly smaller than half of a bf16 spacing, and rounded to nearest would be lost).
+ *            master must be NULL for an f32 param
+ *   grad     f32 or bf16
+ *   state_type  MOK_STATE_F32: m and v are f32 [n], v_scale and m_scale NULL.
+ *               MOK_STATE_MX8: m and v are E4M3 [n] holding m and sqrt(v) in blocks of 32 elements,
+ *               m_scale and v_scale [ceil(n / 32)] E8M0 bytes b standing for 2^(b - 127): the OCP
+ *               Microscaling layout the layer's MXFP8 operands have.  Elements are rounded at random,
+ *               with the mean unchanged; a nonzero sqrt(v) never becomes zero.  All-zero states are
+ *               zero bytes (scale bytes of any value).
+ *   counter  multiple of 8: element i takes the rounding bits of number counter + i.  Tensors whose
+ *            ranges [counter, counter + n) do not overlap are rounded independently
+ * Pointers are aligned to their element; 16-byte aligned ones are accessed in 16 bytes. */
+typedef struct {
+  void* param;
+  float* master;
+  const void* grad;
+  void* m;
+  void* v;
+  uint8_t* m_scale;
+  uint8_t* v_scale;
+  int64_t n;
+  uint64_t counter;
+  float lr, weight_decay;
+  int32_t param_type, grad_type; /* mok_elem_type */
+  int32_t state_type;            /* mok_state_type */
+  int32_t reserved;              /* 0 */
+} mok_adamw_tensor;
+
+/* beta1, beta2 in [0, 1), eps >= 0; step >= 1 is this step's number; seed chooses the rounding bits
+ * (with the step and the element's counter; the same three give the same bits). */
+typedef struct {
+  double beta1, beta2, eps;
+  int64_t step;
+  uint32_t seed;
+  uint32_t reserved; /* 0 */
+} mok_adamw_hyper;
+
+/* AdamW on every tensor, in place:
+ *   g' = c * grad, c = *grad_scale (f32 on the device, NULL = 1), e.g. out + 1 of mok_grad_norm
+ *   m = beta1 m + (1 - beta1) g';  v = beta2 v + (1 - beta2) g'^2
+ *   param -= lr * ((m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps) + weight_decay * param)
+ * in f32.  Where c is NaN nothing is changed. */
+mok_status mok_adamw_step(const mok_adamw_tensor* tensors, int32_t count, const mok_adamw_hyper* hyper,
+                          const float* grad_scale, void* stream);
+
 /* Synchronises `stream`, copies the device status word out of ws into
  * device_status[0] (code, a mok_status value) and device_status[1] (site), then clears it.
  * Host-blocking; not for use inside captured graphs. */

@@ -10,3 +10,4 @@ from ._native import (FLAG_GEMM_PAIR, FLAG_GEMM_SINGLE, FLAG_RING_PERSISTENT, FL
                       min_minibatch, moe_backward, moe_backward_mxfp8, moe_forward, moe_forward_mxfp8,
                       quantize_weights, quantize_weights_backward, read_status, schedule, status_string,
                       workspace_size)
+from .training import AdamW, GradNorm  # noqa: F401

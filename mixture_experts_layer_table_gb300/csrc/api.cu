@@ -6,32 +6,18 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
-#include <mutex>
 #include <new>
 
+#include "api_common.h"
 #include "kernels.cuh"
 #include "mok.h"
 #include "mx_tiles.h"
 
+using namespace mok_api;
+
 namespace {
 
-constexpr int kMaxDevices = 64;
-
-int sm_count() {
-  static int cache[kMaxDevices] = {0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
-  if (cache[dev] == 0) {
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    cache[dev] = n;
-  }
-  return cache[dev];
-}
-
 int64_t align256(int64_t x) { return (x + 255) & ~int64_t(255); }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 mok_status check_desc(const mok_layer_desc* d) {
   if (d == nullptr) return MOK_ERR_INVALID_ARG;
@@ -181,44 +167,6 @@ template <typename T>
 const T* at(const void* base, int64_t off) {
   return reinterpret_cast<const T*>(static_cast<const char*>(base) + off);
 }
-
-#define MOK_CUDA(call)                       \
-  do {                                       \
-    if ((call) != cudaSuccess) return MOK_ERR_CUDA; \
-  } while (0)
-
-// ------------------------------------------------------------------ per-kernel trace
-struct TraceRec {
-  const char* name;
-  cudaEvent_t start, stop;
-};
-
-struct Trace {
-  std::mutex mu;
-  bool on = false;
-  int cap = 0;
-  int used = 0;
-  TraceRec* recs = nullptr;
-} g_trace;
-
-// Records a start event before and a stop event after the launch `call` on stream `st`.
-template <typename F>
-cudaError_t traced(const char* name, cudaStream_t st, F&& call) {
-  TraceRec* rec = nullptr;
-  if (g_trace.on) {
-    std::lock_guard<std::mutex> lock(g_trace.mu);
-    if (g_trace.on && g_trace.used < g_trace.cap) {
-      rec = &g_trace.recs[g_trace.used++];
-      rec->name = name;
-    }
-  }
-  if (rec) cudaEventRecord(rec->start, st);
-  const cudaError_t err = call();
-  if (rec) cudaEventRecord(rec->stop, st);
-  return err;
-}
-
-#define MOK_LAUNCH(name, st, expr) MOK_CUDA(traced(name, st, [&] { return (expr); }))
 
 }  // namespace
 

@@ -1,0 +1,91 @@
+"""Refusals of the training-step entry points (CPU only): the C ABI answers before it touches the GPU,
+and the binding refuses what the bare pointers could not carry."""
+import ctypes
+
+import pytest
+import torch
+
+import mixture_experts_layer_table_gb300 as mok
+from mixture_experts_layer_table_gb300 import _native as N
+from mixture_experts_layer_table_gb300 import training as TR
+
+P = ctypes.c_void_p
+INVALID, WS_SMALL = 1, 3
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from mixture_experts_layer_table_gb300 import build
+    build.build()
+    if torch.cuda.is_available():
+        pytest.skip("placeholder addresses are for hosts without a GPU")
+    return N.load()
+
+
+def _adamw(**kw):
+    t = dict(param=0x100000, master=None, grad=0x200000, m=0x300000, v=0x400000, m_scale=None, v_scale=None, n=100,
+             counter=0, lr=1e-3, weight_decay=0.1, param_type=0, grad_type=0, state_type=0, reserved=0)
+    t.update(kw)
+    return TR.AdamWTensor(**t)
+
+
+@pytest.mark.parametrize("kw", [dict(param=None), dict(grad=None), dict(m=None), dict(v=None), dict(n=-1),
+                                dict(param_type=2), dict(grad_type=-1), dict(state_type=2), dict(reserved=1),
+                                dict(counter=4), dict(lr=float("nan")), dict(weight_decay=float("inf")),
+                                dict(master=0x500000), dict(m_scale=0x500000), dict(state_type=1),
+                                dict(param=0x100002), dict(grad=0x200001), dict(m=0x300002),
+                                dict(param_type=1, param=0x100001), dict(param_type=1, master=0x500002)])
+def test_adamw_refuses_a_bad_tensor(lib, kw):
+    call, hyper = TR._adamw_fn(), TR.AdamWHyper(0.9, 0.95, 1e-8, 1, 0, 0)
+    arr = (TR.AdamWTensor * 2)(_adamw(n=0, param=None, grad=None, m=None, v=None), _adamw(**kw))
+    assert call(arr, 2, ctypes.byref(hyper), None, None) == INVALID
+
+
+@pytest.mark.parametrize("hyper", [(1.0, 0.95, 1e-8, 1, 0, 0), (0.9, -0.1, 1e-8, 1, 0, 0), (0.9, 0.95, -1.0, 1, 0, 0),
+                                   (0.9, 0.95, float("inf"), 1, 0, 0), (0.9, 0.95, 1e-8, 0, 0, 0),
+                                   (0.9, 0.95, 1e-8, 1, 0, 1), (float("nan"), 0.95, 1e-8, 1, 0, 0)])
+def test_adamw_refuses_bad_hyperparameters(lib, hyper):
+    arr = (TR.AdamWTensor * 1)(_adamw())
+    call = TR._adamw_fn()
+    assert call(arr, 1, ctypes.byref(TR.AdamWHyper(*hyper)), None, None) == INVALID
+    assert call(arr, 1, None, None, None) == INVALID
+    ok = ctypes.byref(TR.AdamWHyper(0.9, 0.95, 1e-8, 1, 0, 0))
+    assert call(None, 1, ok, None, None) == INVALID
+    assert call(arr, -1, ok, None, None) == INVALID
+    assert call(arr, 1, ok, P(0x100002), None) == INVALID      # misaligned scale
+
+
+def test_grad_norm_refuses(lib):
+    call = TR._grad_norm_fn()
+    ok = TR.GradTensor(0x100000, 10, 0, 0)
+    arr = lambda t: (TR.GradTensor * 1)(t)  # noqa: E731
+    ws, n, out = P(0x200000), TR.GRAD_NORM_WS_BYTES, P(0x300000)
+    for bad in (TR.GradTensor(None, 10, 0, 0), TR.GradTensor(0x100000, -1, 0, 0), TR.GradTensor(0x100000, 10, 2, 0),
+                TR.GradTensor(0x100002, 10, 0, 0), TR.GradTensor(0x100001, 10, 1, 0), TR.GradTensor(0x100000, 10, 0, 1)):
+        assert call(arr(bad), 1, 1.0, out, ws, n, None) == INVALID
+    for max_norm in (0.0, -1.0, float("nan")):
+        assert call(arr(ok), 1, max_norm, out, ws, n, None) == INVALID
+    assert call(None, 1, 1.0, out, ws, n, None) == INVALID
+    assert call(arr(ok), -1, 1.0, out, ws, n, None) == INVALID
+    assert call(arr(ok), 1, 1.0, None, ws, n, None) == INVALID
+    assert call(arr(ok), 1, 1.0, out, None, n, None) == INVALID
+    assert call(arr(ok), 1, 1.0, out, P(0x200008), n, None) == INVALID
+    assert call(arr(ok), 1, 1.0, out, ws, n - 1, None) == WS_SMALL
+
+
+def test_the_binding_refuses_host_tensors_and_mismatches(lib):
+    t = torch.zeros(8)
+    with pytest.raises(ValueError, match="CUDA"):
+        mok.GradNorm([t], 1.0)
+    with pytest.raises(ValueError, match="CUDA"):
+        mok.AdamW([t], [t])
+    with pytest.raises(ValueError, match="expected a tensor"):
+        mok.AdamW([t.double()], [t])
+    with pytest.raises(ValueError, match="1 params and 0 grads"):
+        mok.AdamW([t], [])
+    with pytest.raises(ValueError, match="state"):
+        mok.AdamW([t], [t], state="int8")
+    with pytest.raises(ValueError, match="betas"):
+        mok.AdamW([t], [t], betas=(0.9, 1.0))
+    with pytest.raises(ValueError, match="max_norm"):
+        mok.GradNorm([t], 0.0)
