@@ -62,6 +62,7 @@ typedef enum {
 
 typedef enum { MOK_ROUTER_SOFTMAX = 0, MOK_ROUTER_SIGMOID = 1 } mok_router_kind;
 typedef enum { MOK_BF16 = 0, MOK_MXFP8 = 1 } mok_precision;
+typedef enum { MOK_ELEM_F32 = 0, MOK_ELEM_BF16 = 1 } mok_elem_type;
 
 /* Layer descriptor.
  *   T       tokens of this call, 1 <= T
@@ -112,6 +113,10 @@ typedef enum { MOK_BF16 = 0, MOK_MXFP8 = 1 } mok_precision;
  *   comm_sms     ring forward: CTAs (one per SM) that gather rows (0 = 12); even when GEMM1
  *                runs on the narrow-segment CTA-pair kernel (the default), since those
  *                CTAs are launched in clusters of two
+ *   n_group      0 or 1: the k experts are chosen among all E.  > 1: among those of the topk_group
+ *                best of n_group equal groups of consecutive experts, as mok_route does it
+ *                (group_score as there); a given selection is taken as it is
+ *   topk_group, group_score  read where n_group > 1
  * T*k*max(H, 2I) must stay below 2^31 elements. */
 #define MOK_FLAG_WGRAD_BF16 1
 #define MOK_FLAG_GEMM_PAIR 2
@@ -128,6 +133,7 @@ typedef struct {
   int64_t ring_bytes;
   int32_t flags;
   int32_t comm_sms;
+  int32_t n_group, topk_group, group_score;
 } mok_layer_desc;
 
 /* Byte offsets (from the base pointer) of the tensors inside ctx and ws.  ctx holds what
@@ -346,11 +352,69 @@ mok_status mok_moe_backward(const mok_layer_desc* desc, const void* dy, const vo
                             void* dw13, void* dw2, float* dgates, void* ws, size_t ws_bytes,
                             void* stream);
 
+/* ------------------------------------------------------------------ group-limited routing
+ * Expert selection from router logits in hand, with what load balancing needs of it (readings: the
+ * pages name a router that picks a few experts per token and no rule; this is DeepSeek-V3's, whose
+ * layout they target, with its softmax predecessor).
+ *   T        tokens, >= 0
+ *   E        experts, 1 .. 1024;  k  experts per token, 1 .. min(16, topk_group * E / n_group)
+ *   router, renorm, route_scale  as in mok_layer_desc
+ *   n_group  equal groups of consecutive experts, 1 .. 32, a divisor of E
+ *   topk_group   groups a token's experts come from, 1 .. n_group
+ *   group_score  mok_group_score: a group's value is its best rank value, or the sum of its two best
+ *   logits_type  mok_elem_type of the logits (and of their gradient)
+ *   logits_stride  elements between rows, >= E (0 = E)
+ *   balance_coef, bias_rate  factors of the balance loss and of the bias step
+ * With s the scores, an expert's rank value is s + bias (softmax without a bias: its logit, and
+ * e^(logit - max) in a sum of two, the same order without the rounding of the softmax's sum).  An
+ * expert whose logit is -inf (masked) or NaN ranks behind all others and counts in no group's value.
+ * The topk_group best groups stay, then the k best experts in them; ties go to the lower index. */
+typedef enum { MOK_GROUP_MAX = 0, MOK_GROUP_TOP2 = 1 } mok_group_score;
+typedef struct {
+  int64_t T, logits_stride;
+  int32_t E, k;
+  int32_t router, renorm;
+  float route_scale;
+  int32_t n_group, topk_group, group_score;
+  int32_t logits_type;
+  float balance_coef, bias_rate;
+  int32_t reserved; /* 0 */
+} mok_route_desc;
+
+/* logits [T][E] (device; rows logits_stride apart), bias f32 [E] or NULL (added to the rank value
+ * only).  Outputs, each NULL if not wanted unless noted:
+ *   topk_idx   i32 [T][k] (required): best first
+ *   gates      f32 [T][k]: route_scale * s, or route_scale * s / (sum of the k selected s) with renorm
+ *              (0 where that sum is 0, e.g. with every expert masked)
+ *   scores     f32 [T][E]
+ *   counts     i32 [E]: tokens of each expert
+ *   prob_sum   f32 [E]: sum over the tokens of s / (sum of the token's s)
+ *   loss       f32 [1]: balance_coef * E / (k T^2) * sum_e counts[e] * prob_sum[e]
+ *   dprob      f32 [E]: the loss's derivative by prob_sum (the counts are constants), for
+ *              mok_route_backward
+ *   bias_next  f32 [E]: bias + bias_rate * sign(T k / E - counts), may be bias itself
+ * The five from counts on need ws: at least MOK_ROUTE_WS_BYTES, 256-byte aligned, zero-filled once
+ * before its first use (each call leaves it ready for the next); otherwise ws may be NULL.  With
+ * them T stays below 2^31.  A logit that makes a token's scores NaN makes prob_sum and loss NaN. */
+#define MOK_ROUTE_WS_BYTES 12544
+mok_status mok_route(const mok_route_desc* desc, const void* logits, const float* bias, int32_t* topk_idx,
+                     float* gates, float* scores, int32_t* counts, float* prob_sum, float* loss, float* dprob,
+                     float* bias_next, void* ws, size_t ws_bytes, void* stream);
+
+/* dlogits [T][E] (the logits' type, rows dlogits_stride apart, 0 = E) for the gates' gradient
+ * dgates f32 [T][k] at the experts topk_idx i32 [T][k] (distinct) and the gradient dprob f32 [E] of
+ * prob_sum; either gradient may be NULL (topk_idx too without dgates), not both.  The selection is
+ * held fixed, the bias gets no gradient.  An index outside [0, E) is left out and reported as
+ * (MOK_ERR_INVALID_ROUTING, site) in device_status, a DEVICE buffer of 2 int32 that the caller has
+ * cleared, or NULL. */
+mok_status mok_route_backward(const mok_route_desc* desc, const void* logits, const int32_t* topk_idx,
+                              const float* dgates, const float* dprob, void* dlogits, int64_t dlogits_stride,
+                              int32_t* device_status, void* stream);
+
 /* ------------------------------------------------------------------ optimizer step
  * The step that consumes the layer's gradients (the pages end with the backward pass; the update
  * is plain AdamW, I. Loshchilov and F. Hutter, "Decoupled Weight Decay Regularization").  Tensors
  * are given as a host array that is read before the call returns; nothing of it is kept. */
-typedef enum { MOK_ELEM_F32 = 0, MOK_ELEM_BF16 = 1 } mok_elem_type;
 typedef enum { MOK_STATE_F32 = 0, MOK_STATE_MX8 = 1 } mok_state_type;
 
 typedef struct {

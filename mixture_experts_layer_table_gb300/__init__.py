@@ -10,4 +10,5 @@ from ._native import (FLAG_GEMM_PAIR, FLAG_GEMM_SINGLE, FLAG_RING_PERSISTENT, FL
                       min_minibatch, moe_backward, moe_backward_mxfp8, moe_forward, moe_forward_mxfp8,
                       quantize_weights, quantize_weights_backward, read_status, schedule, status_string,
                       workspace_size)
+from .routing import GROUP_MAX, GROUP_TOP2, RouteDesc, Router, make_route_desc  # noqa: F401
 from .training import AdamW, GradNorm  # noqa: F401

@@ -32,7 +32,8 @@ class LayerDesc(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("I", ctypes.c_int32), ("E", ctypes.c_int32),
                 ("k", ctypes.c_int32), ("router", ctypes.c_int32), ("renorm", ctypes.c_int32),
                 ("route_scale", ctypes.c_float), ("precision", ctypes.c_int32), ("minibatch", ctypes.c_int32),
-                ("ring_bytes", ctypes.c_int64), ("flags", ctypes.c_int32), ("comm_sms", ctypes.c_int32)]
+                ("ring_bytes", ctypes.c_int64), ("flags", ctypes.c_int32), ("comm_sms", ctypes.c_int32),
+                ("n_group", ctypes.c_int32), ("topk_group", ctypes.c_int32), ("group_score", ctypes.c_int32)]
 
 
 LAYOUT_FIELDS = ["topk_idx", "gates", "scores", "counts", "offsets", "row_of", "src_of", "tile_off", "gate_row",
@@ -122,9 +123,9 @@ def _check(fn: str, code: int):
 
 
 def make_desc(T, H, I, E, k, router, renorm, route_scale=1.0, precision=0, minibatch=0, ring_bytes=0,
-              flags=0, comm_sms=0) -> LayerDesc:
+              flags=0, comm_sms=0, n_group=0, topk_group=0, group_score=0) -> LayerDesc:
     return LayerDesc(T, H, I, E, k, router, int(bool(renorm)), route_scale, precision, minibatch, ring_bytes,
-                     flags, comm_sms)
+                     flags, comm_sms, n_group, topk_group, group_score)
 
 
 def desc_from_shape(shape, **kw) -> LayerDesc:

@@ -12,6 +12,7 @@
 #include "kernels.cuh"
 #include "mok.h"
 #include "mx_tiles.h"
+#include "router.cuh"
 
 using namespace mok_api;
 
@@ -32,10 +33,42 @@ mok_status check_desc(const mok_layer_desc* d) {
   // pair tile over H or I that reaches past the end reads zeros there and stores none of it
   if (d->H % 128 != 0 || d->I % 128 != 0) return MOK_ERR_UNSUPPORTED;
   if (d->E > 1024 || d->k > 16) return MOK_ERR_UNSUPPORTED;
+  if (d->n_group < 0) return MOK_ERR_INVALID_ARG;
+  if (d->n_group > 1) {
+    if (d->E % d->n_group != 0 || d->topk_group < 1 || d->topk_group > d->n_group) return MOK_ERR_INVALID_ARG;
+    if (d->k > d->topk_group * (d->E / d->n_group)) return MOK_ERR_INVALID_ARG;
+    if (d->group_score != MOK_GROUP_MAX && d->group_score != MOK_GROUP_TOP2) return MOK_ERR_INVALID_ARG;
+    if (d->n_group > mok::ROUTE_MAX_GROUPS) return MOK_ERR_UNSUPPORTED;
+  }
   const int64_t R = int64_t(d->T) * d->k;
   const int64_t width = d->H > 2 * d->I ? d->H : 2 * int64_t(d->I);
   if (R * width >= (int64_t(1) << 31)) return MOK_ERR_UNSUPPORTED;
   return MOK_OK;
+}
+
+// Scores, selected experts and gates of the layer's logits: among all experts, or limited to groups
+// (a given selection is taken as it is).
+cudaError_t select_experts(const mok_layer_desc* d, const float* logits, const float* bias, const int32_t* given,
+                           int32_t* topk_idx, float* gates, float* scores, int* status, int n_sm, cudaStream_t st) {
+  if (d->n_group <= 1 || given != nullptr)
+    return mok::launch_topk(logits, bias, given, d->T, d->E, d->k, d->router, d->renorm, d->route_scale, topk_idx,
+                            gates, scores, status, st);
+  mok::RouteArgs a = {};
+  a.logits = logits;
+  a.bias = bias;
+  a.T = d->T;
+  a.stride = a.E = d->E;
+  a.k = d->k;
+  a.router = d->router;
+  a.renorm = d->renorm;
+  a.scale = d->route_scale;
+  a.n_group = d->n_group;
+  a.topk_group = d->topk_group;
+  a.group_top2 = d->group_score == MOK_GROUP_TOP2;
+  a.topk_idx = topk_idx;
+  a.gates = gates;
+  a.scores = scores;
+  return mok::launch_route(a, false, n_sm, st);
 }
 
 // Expert GEMM kernels: by default the narrow-segment pair kernel (the expert's rows are the
@@ -228,8 +261,8 @@ mok_status mok_schedule(const mok_layer_desc* d, const void* x, const void* w_ro
   float* logits = at<float>(ws, L.logits);
   MOK_CUDA(cudaMemsetAsync(status, 0, mok::STATUS_BYTES, st));
   if (have_router) MOK_LAUNCH("router_gemm", st, mok::launch_router_gemm(x, w_router, d->T, d->H, d->E, logits, status, n_sm, st));
-  MOK_LAUNCH("topk", st, mok::launch_topk(have_router ? logits : nullptr, router_bias, given_topk, d->T, d->E, d->k, d->router,
-                            d->renorm, d->route_scale, topk_idx, gates, nullptr, status, st));
+  MOK_LAUNCH("topk", st, select_experts(d, have_router ? logits : nullptr, router_bias, given_topk, topk_idx, gates,
+                                        nullptr, status, n_sm, st));
   MOK_LAUNCH("schedule", st, mok::launch_schedule_multi(topk_idx, nullptr, d->T * d->k, d->E, counts, offsets, row_of,
                                                         src_of, nullptr, nullptr, at<int32_t>(ws, L.sched), status, st));
   return MOK_OK;
@@ -286,8 +319,8 @@ mok_status mok_moe_forward(const mok_layer_desc* d, const void* x, const void* w
   // 1. router logits x W_r^T (tensor cores, fp32 accumulate)
   MOK_LAUNCH("router_gemm", st, mok::launch_router_gemm(x, w_router, T, H, E, logits, status, n_sm, st));
   // 2. scores, top-k and gates
-  MOK_LAUNCH("topk", st, mok::launch_topk(logits, router_bias, given_topk, T, E, k, d->router, d->renorm, d->route_scale,
-                            topk_idx, gates, at<float>(ctx, L.scores), status, st));
+  MOK_LAUNCH("topk", st, select_experts(d, logits, router_bias, given_topk, topk_idx, gates, at<float>(ctx, L.scores),
+                                        status, n_sm, st));
   // 3. schedule table
   MOK_LAUNCH("schedule", st, mok::launch_schedule_multi(topk_idx, gates, R, E, at<int32_t>(ctx, L.counts), offsets, row_of,
                                                         src_of, tile_off, at<float>(ctx, L.gate_row),
@@ -530,8 +563,8 @@ mok_status mok_moe_forward_mxfp8(const mok_layer_desc* d, const void* x, const v
 
   MOK_CUDA(cudaMemsetAsync(status, 0, mok::STATUS_BYTES, st));
   MOK_LAUNCH("router_gemm", st, mok::launch_router_gemm(x, w_router, T, H, E, logits, status, n_sm, st));
-  MOK_LAUNCH("topk", st, mok::launch_topk(logits, router_bias, given_topk, T, E, k, d->router, d->renorm,
-                                          d->route_scale, topk_idx, gates, at<float>(ctx, L.scores), status, st));
+  MOK_LAUNCH("topk", st, select_experts(d, logits, router_bias, given_topk, topk_idx, gates, at<float>(ctx, L.scores),
+                                        status, n_sm, st));
   MOK_LAUNCH("schedule", st, mok::launch_schedule_multi(topk_idx, gates, R, E, at<int32_t>(ctx, L.counts), offsets,
                                                         row_of, src_of, tile_off, at<float>(ctx, L.gate_row),
                                                         at<int32_t>(ws, L.sched), status, st));

@@ -1,5 +1,5 @@
 // C ABI of the training step around the layer (include/mok.h): argument checks and launches of the
-// gradient norm and the AdamW step.  As for the layer: no allocation, no host synchronisation, every
+// group-limited routing and its backward, the gradient norm and the AdamW step.  As for the layer: no allocation, no host synchronisation, every
 // kernel enqueued on the caller's stream.
 #include <cuda_runtime.h>
 
@@ -9,6 +9,7 @@
 #include "api_common.h"
 #include "mok.h"
 #include "optim.cuh"
+#include "router.cuh"
 
 using namespace mok_api;
 
@@ -36,6 +37,22 @@ mok_status check_adamw(const mok_adamw_tensor& t) {
   return MOK_OK;
 }
 
+mok_status check_route(const mok_route_desc* d) {
+  if (d == nullptr || d->T < 0 || d->E < 1 || d->k < 1 || d->reserved != 0) return MOK_ERR_INVALID_ARG;
+  if (d->router != MOK_ROUTER_SOFTMAX && d->router != MOK_ROUTER_SIGMOID) return MOK_ERR_INVALID_ARG;
+  if (d->group_score != MOK_GROUP_MAX && d->group_score != MOK_GROUP_TOP2) return MOK_ERR_INVALID_ARG;
+  if (!elem_type(d->logits_type)) return MOK_ERR_INVALID_ARG;
+  if (!std::isfinite(d->route_scale) || !std::isfinite(d->balance_coef) || !std::isfinite(d->bias_rate))
+    return MOK_ERR_INVALID_ARG;
+  if (d->logits_stride != 0 && d->logits_stride < d->E) return MOK_ERR_INVALID_ARG;
+  if (d->n_group < 1 || d->E % d->n_group != 0 || d->topk_group < 1 || d->topk_group > d->n_group)
+    return MOK_ERR_INVALID_ARG;
+  if (d->k > (int64_t)d->topk_group * (d->E / d->n_group)) return MOK_ERR_INVALID_ARG;
+  if (d->E > mok::ROUTE_MAX_E || d->k > mok::ROUTE_MAX_K || d->n_group > mok::ROUTE_MAX_GROUPS)
+    return MOK_ERR_UNSUPPORTED;
+  return MOK_OK;
+}
+
 int param_kind(const mok_adamw_tensor& t) {
   if (t.param_type == MOK_ELEM_F32) return mok::PARAM_F32;
   return t.master != nullptr ? mok::PARAM_BF16_MASTER : mok::PARAM_BF16;
@@ -44,6 +61,99 @@ int param_kind(const mok_adamw_tensor& t) {
 }  // namespace
 
 extern "C" {
+
+mok_status mok_route(const mok_route_desc* d, const void* logits, const float* bias, int32_t* topk_idx, float* gates,
+                     float* scores, int32_t* counts, float* prob_sum, float* loss, float* dprob, float* bias_next,
+                     void* ws, size_t ws_bytes, void* stream) {
+  static_assert(MOK_ROUTE_WS_BYTES >= mok::ROUTE_WS_BYTES, "workspace of mok_route");
+  mok_status s = check_route(d);
+  if (s != MOK_OK) return s;
+  if (d->T > 0 && (!logits || !topk_idx)) return MOK_ERR_INVALID_ARG;
+  if (!aligned_elem(logits, d->logits_type)) return MOK_ERR_INVALID_ARG;
+  const void* words[] = {bias, topk_idx, gates, scores, counts, prob_sum, loss, dprob, bias_next};
+  for (const void* p : words)
+    if (!aligned_elem(p, MOK_ELEM_F32)) return MOK_ERR_INVALID_ARG;
+  if (bias_next != nullptr && bias == nullptr) return MOK_ERR_INVALID_ARG;
+  mok::RouteArgs a = {};
+  a.counts = counts;
+  a.prob_sum = prob_sum;
+  a.loss = loss;
+  a.dprob = dprob;
+  a.bias_next = bias_next;
+  if (mok::route_balances(a)) {
+    if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return MOK_ERR_INVALID_ARG;
+    if (ws_bytes < (size_t)MOK_ROUTE_WS_BYTES) return MOK_ERR_WORKSPACE_TOO_SMALL;
+    if (d->T >= (int64_t(1) << 31)) return MOK_ERR_UNSUPPORTED;
+    char* base = static_cast<char*>(ws);
+    a.ticket = reinterpret_cast<unsigned*>(base);
+    a.not_finite = a.ticket + 1;
+    a.acc_prob = reinterpret_cast<unsigned long long*>(base + mok::ROUTE_WS_SUMS);
+    a.acc_counts = reinterpret_cast<int32_t*>(base + mok::ROUTE_WS_COUNTS);
+  } else if (d->T == 0) {
+    return MOK_OK;
+  }
+  a.logits = logits;
+  a.bias = bias;
+  a.T = d->T;
+  a.stride = d->logits_stride != 0 ? d->logits_stride : d->E;
+  a.E = d->E;
+  a.k = d->k;
+  a.router = d->router;
+  a.renorm = d->renorm;
+  a.scale = d->route_scale;
+  a.n_group = d->n_group;
+  a.topk_group = d->topk_group;
+  a.group_top2 = d->group_score == MOK_GROUP_TOP2;
+  a.topk_idx = topk_idx;
+  a.gates = gates;
+  a.scores = scores;
+  a.dprob_unit = d->T == 0 ? 0.0f : (float)(d->balance_coef * (double)d->E / ((double)d->k * (double)d->T * (double)d->T));
+  a.bias_rate = d->bias_rate;
+  // a sum of T probabilities of at most 1 stays below 2^62 units
+  int bits = 0;
+  while ((d->T >> bits) != 0) ++bits;
+  a.sum_shift = std::min(52, 62 - bits);
+  const int n_sm = sm_count();
+  if (n_sm <= 0) return MOK_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  MOK_LAUNCH("route", st, mok::launch_route(a, d->logits_type == MOK_ELEM_BF16, n_sm, st));
+  return MOK_OK;
+}
+
+mok_status mok_route_backward(const mok_route_desc* d, const void* logits, const int32_t* topk_idx, const float* dgates,
+                              const float* dprob, void* dlogits, int64_t dlogits_stride, int32_t* device_status,
+                              void* stream) {
+  mok_status s = check_route(d);
+  if (s != MOK_OK) return s;
+  if (dlogits_stride != 0 && dlogits_stride < d->E) return MOK_ERR_INVALID_ARG;
+  if (!aligned_elem(logits, d->logits_type) || !aligned_elem(dlogits, d->logits_type)) return MOK_ERR_INVALID_ARG;
+  const void* words[] = {topk_idx, dgates, dprob, device_status};
+  for (const void* p : words)
+    if (!aligned_elem(p, MOK_ELEM_F32)) return MOK_ERR_INVALID_ARG;
+  if (d->T == 0) return MOK_OK;
+  if ((dgates == nullptr && dprob == nullptr) || (dgates != nullptr && topk_idx == nullptr)) return MOK_ERR_INVALID_ARG;
+  if (!logits || !dlogits) return MOK_ERR_INVALID_ARG;
+  mok::RouteBackwardArgs a = {};
+  a.logits = logits;
+  a.T = d->T;
+  a.stride = d->logits_stride != 0 ? d->logits_stride : d->E;
+  a.out_stride = dlogits_stride != 0 ? dlogits_stride : d->E;
+  a.E = d->E;
+  a.k = d->k;
+  a.router = d->router;
+  a.renorm = d->renorm;
+  a.scale = d->route_scale;
+  a.topk_idx = topk_idx;
+  a.dgates = dgates;
+  a.dprob = dprob;
+  a.dlogits = dlogits;
+  a.status = device_status;
+  const int n_sm = sm_count();
+  if (n_sm <= 0) return MOK_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  MOK_LAUNCH("route_backward", st, mok::launch_route_backward(a, d->logits_type == MOK_ELEM_BF16, n_sm, st));
+  return MOK_OK;
+}
 
 mok_status mok_grad_norm(const mok_grad_tensor* tensors, int32_t count, float max_norm, float* out, void* ws,
                          size_t ws_bytes, void* stream) {

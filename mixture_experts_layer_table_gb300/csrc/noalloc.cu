@@ -19,6 +19,7 @@
 
 #include "kernels.cuh"
 #include "mok.h"
+#include "router.cuh"
 
 namespace {
 
@@ -107,9 +108,26 @@ extern "C" mok_status mok_schedule_noalloc(const mok_layer_desc* d, const void* 
   if (have_router &&
       mok::launch_router_gemm(x, w_router, d->T, d->H, d->E, logits, status, n_sm, st) != cudaSuccess)
     return MOK_ERR_CUDA;
-  if (mok::launch_topk(have_router ? logits : nullptr, router_bias, given_topk, d->T, d->E, d->k, d->router,
-                       d->renorm, d->route_scale, topk_idx, gates, nullptr, status, st) != cudaSuccess)
+  if (d->n_group > 1 && given_topk == nullptr) {
+    mok::RouteArgs a = {};
+    a.logits = logits;
+    a.bias = router_bias;
+    a.T = d->T;
+    a.stride = a.E = d->E;
+    a.k = d->k;
+    a.router = d->router;
+    a.renorm = d->renorm;
+    a.scale = d->route_scale;
+    a.n_group = d->n_group;
+    a.topk_group = d->topk_group;
+    a.group_top2 = d->group_score == MOK_GROUP_TOP2;
+    a.topk_idx = topk_idx;
+    a.gates = gates;
+    if (mok::launch_route(a, false, n_sm, st) != cudaSuccess) return MOK_ERR_CUDA;
+  } else if (mok::launch_topk(have_router ? logits : nullptr, router_bias, given_topk, d->T, d->E, d->k, d->router,
+                              d->renorm, d->route_scale, topk_idx, gates, nullptr, status, st) != cudaSuccess) {
     return MOK_ERR_CUDA;
+  }
   if (mok::launch_schedule(topk_idx, nullptr, d->T * d->k, d->E, counts, offsets, row_of, src_of, nullptr, nullptr,
                            status, st) != cudaSuccess)
     return MOK_ERR_CUDA;

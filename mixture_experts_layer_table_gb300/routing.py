@@ -1,0 +1,126 @@
+"""Binding of the group-limited routing (include/mok.h): expert selection from router logits, with the
+load-balancing outputs, and its backward.
+
+As in ``_native``: argument marshalling only, every step runs in the library's CUDA kernels, the
+stream is PyTorch's current stream unless given, and there is no fallback.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Dict, Optional
+
+import torch
+
+from ._native import _check, _expect, _ptr, _stream, load
+
+P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+
+GROUP_MAX, GROUP_TOP2 = 0, 1
+ROUTE_WS_BYTES = 12544
+LOGIT_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+class RouteDesc(ctypes.Structure):
+    _fields_ = [("T", I64), ("logits_stride", I64), ("E", I32), ("k", I32), ("router", I32), ("renorm", I32),
+                ("route_scale", ctypes.c_float), ("n_group", I32), ("topk_group", I32), ("group_score", I32),
+                ("logits_type", I32), ("balance_coef", ctypes.c_float), ("bias_rate", ctypes.c_float),
+                ("reserved", I32)]
+
+
+def make_route_desc(T, E, k, router, renorm, route_scale=1.0, n_group=1, topk_group=1, group_score=GROUP_TOP2,
+                    balance_coef=0.0, bias_rate=0.0) -> RouteDesc:
+    return RouteDesc(T, 0, E, k, router, int(bool(renorm)), route_scale, n_group, topk_group, group_score, 0,
+                     balance_coef, bias_rate, 0)
+
+
+def _route_fn():
+    fn = load().mok_route
+    if fn.argtypes is None:
+        fn.argtypes = [ctypes.POINTER(RouteDesc)] + [P] * 11 + [SZ, P]
+        fn.restype = I32
+    return fn
+
+
+def _route_backward_fn():
+    fn = load().mok_route_backward
+    if fn.argtypes is None:
+        fn.argtypes = [ctypes.POINTER(RouteDesc)] + [P] * 5 + [I64, P, P]
+        fn.restype = I32
+    return fn
+
+
+def _rows(t, T, E, dtype, name) -> int:
+    """Row stride of a [T][E] CUDA tensor whose rows are contiguous."""
+    if t.shape != (T, E) or t.dtype != dtype:
+        raise ValueError(f"{name}: expected ({T}, {E}) {dtype}, got {tuple(t.shape)} {t.dtype}")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if T > 1 and (t.stride(1) != 1 and E > 1 or t.stride(0) < E) or T == 1 and E > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: rows must be contiguous and must not overlap, got strides {t.stride()}")
+    return t.stride(0) if T > 1 else E
+
+
+class Router:
+    """One routing descriptor with its output buffers, which each call overwrites.
+
+    ``forward`` returns {"topk_idx", "gates"}, with ``scores`` also "scores", and with ``balance``
+    also "counts", "prob_sum", "loss", "dprob" and, where a bias is given, "bias_next"."""
+
+    def __init__(self, desc: RouteDesc, dtype=torch.float32, balance: bool = False, scores: bool = False,
+                 device="cuda"):
+        if dtype not in LOGIT_TYPES:
+            raise ValueError(f"logits are float32 or bfloat16, got {dtype}")
+        # a descriptor of its own: the row stride is each call's
+        self.desc = RouteDesc.from_buffer_copy(desc)
+        self.desc.logits_type = LOGIT_TYPES[dtype]
+        self.dtype, self.balance = dtype, balance
+        T, E, k = desc.T, desc.E, desc.k
+        new = lambda shape, dt=torch.float32: torch.empty(shape, dtype=dt, device=device)  # noqa: E731
+        self.out = {"topk_idx": new((T, k), torch.int32), "gates": new((T, k))}
+        if scores:
+            self.out["scores"] = new((T, E))
+        self.ws = None
+        if balance:
+            self.out |= {"counts": new((E,), torch.int32), "prob_sum": new((E,)), "loss": new((1,)), "dprob": new((E,))}
+            self.ws = torch.zeros(ROUTE_WS_BYTES, dtype=torch.uint8, device=device)
+        self.bias_next = new((E,)) if balance else None
+        self._args = [_ptr(self.out.get(n)) for n in ("topk_idx", "gates", "scores", "counts", "prob_sum", "loss", "dprob")]
+        self._ws = _ptr(self.ws)
+        self._ref = ctypes.byref(self.desc)
+        self._call = _route_fn()
+        self._call_backward = _route_backward_fn()
+
+    def forward(self, logits: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                bias_next: Optional[torch.Tensor] = None, stream=None) -> Dict[str, torch.Tensor]:
+        """``bias_next``: where the moved bias goes (with ``balance``), e.g. ``bias`` itself."""
+        d = self.desc
+        d.logits_stride = _rows(logits, d.T, d.E, self.dtype, "logits")
+        out, moved = self.out, None
+        if bias is not None:
+            _expect(bias, (d.E,), torch.float32, "bias")
+            if self.balance:
+                moved = self.bias_next if bias_next is None else bias_next
+                _expect(moved, (d.E,), torch.float32, "bias_next")
+                out = dict(out, bias_next=moved)
+        _check("mok_route", self._call(self._ref, logits.data_ptr(), _ptr(bias), *self._args, _ptr(moved), self._ws,
+                                       ROUTE_WS_BYTES, _stream(stream)))
+        return out
+
+    def backward(self, logits: torch.Tensor, topk_idx: Optional[torch.Tensor], dgates: Optional[torch.Tensor],
+                 dprob: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                 device_status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """Gradient with respect to the logits, in their type; ``device_status``: int32 [2] CUDA tensor."""
+        d = self.desc
+        d.logits_stride = _rows(logits, d.T, d.E, self.dtype, "logits")
+        if dgates is not None:
+            _expect(dgates, (d.T, d.k), torch.float32, "dgates")
+            _expect(topk_idx, (d.T, d.k), torch.int32, "topk_idx")
+        _expect(dprob, (d.E,), torch.float32, "dprob", nullable=True)
+        _expect(device_status, (2,), torch.int32, "device_status", nullable=True)
+        if out is None:
+            out = torch.empty((d.T, d.E), dtype=self.dtype, device=logits.device)
+        stride = _rows(out, d.T, d.E, self.dtype, "out")
+        _check("mok_route_backward", self._call_backward(
+            self._ref, logits.data_ptr(), _ptr(topk_idx), _ptr(dgates), _ptr(dprob), out.data_ptr(), stride,
+            _ptr(device_status), _stream(stream)))
+        return out

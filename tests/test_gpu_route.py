@@ -1,0 +1,363 @@
+"""GPU parity of the group-limited routing and its backward against the float64 CPU oracle.
+
+The selection is compared exactly, on tokens whose deciding values lie at least 1e-5 apart in the
+oracle (f32 scores are off by less than 1e-6; tokens that are closer are left out before the run), on
+exact ties, and on masks.  Scores go through one exp, one sum of up to 1024 terms and one division in
+f32: gates, scores and probability sums are held to 2^-18 of themselves.  A logit gradient is a sum of
+terms that may cancel: 2^-18 of the terms' sizes, and half a bf16 spacing for bf16 gradients.
+"""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_layer_table_gb300 as mok
+from mixture_experts_layer_table_gb300 import workloads as W
+from oracle import route_oracle as O
+
+pytestmark = pytest.mark.gpu
+
+SOFTMAX, SIGMOID = 0, 1
+MAX, TOP2 = 0, 1
+REL = 2.0 ** -18
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib(cuda_ok):
+    from mixture_experts_layer_table_gb300 import build
+    build.build()
+    mok.load()
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+# (T, E, k, n_group, topk_group, group score): one expert, odd counts, groups of one, groups that are not
+# whole lanes, every experts-per-lane width, the largest
+SHAPES = [(1, 1, 1, 1, 1, MAX), (5, 7, 3, 1, 1, TOP2), (33, 20, 4, 20, 6, TOP2), (40, 60, 5, 6, 2, TOP2),
+          (17, 64, 6, 8, 3, MAX), (29, 96, 8, 3, 1, TOP2), (65, 128, 8, 4, 2, TOP2), (31, 160, 6, 8, 3, MAX),
+          (23, 192, 8, 8, 4, TOP2), (70, 256, 8, 8, 4, TOP2), (19, 300, 12, 12, 5, TOP2), (9, 384, 8, 16, 4, MAX),
+          (11, 502, 7, 2, 1, TOP2), (13, 1024, 16, 32, 8, TOP2), (8, 1000, 16, 8, 8, MAX), (3, 31, 16, 31, 16, MAX)]
+
+
+def _logits(T, E, seed, dtype, router, bias, k, G, kg, score):
+    """T tokens that the oracle's margins keep clear of rounding, as (CUDA tensor, float64)."""
+    rng = np.random.default_rng(seed)
+    x = torch.tensor(rng.normal(size=(6 * T + 40, E)) * 1.5).to(dtype)
+    keep = O.select(x.double().numpy(), bias, router, k, G, kg, score)[1] > 1e-5
+    x = x[torch.tensor(keep)][:T]
+    assert x.shape[0] == T
+    return x.contiguous().cuda(), x.double().numpy()
+
+
+def _bias(E, seed, with_bias):
+    return np.random.default_rng(seed).normal(size=E).astype(np.float32) * np.float32(0.1) if with_bias else None
+
+
+def _cuda(a):
+    return None if a is None else torch.tensor(a).cuda()
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "T%d_E%d_k%d_G%d_kg%d_s%d" % s)
+@pytest.mark.parametrize("router,with_bias", [(SIGMOID, True), (SIGMOID, False), (SOFTMAX, False), (SOFTMAX, True)])
+def test_route(shape, router, with_bias):
+    T, E, k, G, kg, score = shape
+    bias = _bias(E, 5, with_bias)
+    renorm, scale = bool((T + E) % 2) or router == SIGMOID, 2.5
+    x, x64 = _logits(T, E, 7, torch.float32, router, bias, k, G, kg, score)
+    desc = mok.make_route_desc(T, E, k, router, renorm, route_scale=scale, n_group=G, topk_group=kg, group_score=score,
+                               balance_coef=0.3, bias_rate=0.01)
+    out = mok.Router(desc, balance=True, scores=True).forward(x, _cuda(bias))
+    idx, _ = O.select(x64, bias, router, k, G, kg, score)
+    s = O.scores(x64, router)
+    assert np.array_equal(out["topk_idx"].cpu().numpy(), idx)
+    assert np.allclose(f64(out["gates"]), O.gates(s, idx, renorm, scale), rtol=REL, atol=0)
+    assert np.allclose(f64(out["scores"]), s, rtol=REL, atol=0)
+    counts, prob_sum, loss, dprob, moved = O.balance(s, idx, 0.3, bias, 0.01)
+    assert np.array_equal(out["counts"].cpu().numpy(), counts)
+    assert np.allclose(f64(out["prob_sum"]), prob_sum, rtol=REL, atol=0)
+    assert np.allclose(f64(out["dprob"]), dprob, rtol=REL, atol=0)
+    assert np.allclose(f64(out["loss"]), [loss], rtol=REL, atol=0)
+    if bias is not None:
+        assert np.allclose(f64(out["bias_next"]), moved, rtol=0, atol=2.0 ** -23 * (np.abs(moved).max() + 0.01))
+    # the selection alone gives the same
+    plain = mok.Router(desc).forward(x, _cuda(bias))
+    assert torch.equal(plain["topk_idx"], out["topk_idx"]) and torch.equal(plain["gates"], out["gates"])
+
+
+@pytest.mark.parametrize("E,k,G,kg,score", [(256, 8, 8, 4, MAX), (60, 7, 6, 3, MAX), (100, 9, 1, 1, MAX), (16, 5, 16, 7, TOP2)])
+@pytest.mark.parametrize("router", [SIGMOID, SOFTMAX])
+def test_exact_ties_go_to_the_lower_index(E, k, G, kg, score, router):
+    """bf16 logits on a grid of 9 values: most tokens have ties at the cut; and rows of one value."""
+    T = 200
+    rng = np.random.default_rng(2)
+    x = torch.tensor(rng.integers(-4, 5, (T, E)) * 0.25).bfloat16()
+    x[:3] = torch.tensor([[0.0], [-1.0], [2.0]]).bfloat16()
+    out = mok.Router(mok.make_route_desc(T, E, k, router, True, n_group=G, topk_group=kg, group_score=score),
+                     dtype=torch.bfloat16).forward(x.cuda())
+    assert np.array_equal(out["topk_idx"].cpu().numpy(), O.select(x.double().numpy(), None, router, k, G, kg, score)[0])
+
+
+def test_sum_of_two_ties_on_equal_rows():
+    out = mok.Router(mok.make_route_desc(4, 64, 6, SIGMOID, True, n_group=8, topk_group=2)).forward(torch.zeros(4, 64).cuda())
+    assert out["topk_idx"].cpu().tolist() == [[0, 1, 2, 3, 4, 5]] * 4
+
+
+@pytest.mark.parametrize("G,kg,score", [(1, 1, MAX), (8, 3, TOP2), (8, 3, MAX), (5, 2, TOP2)])
+@pytest.mark.parametrize("router", [SIGMOID, SOFTMAX])
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_masked_experts(G, kg, score, router, with_bias):
+    """-inf logits: here and there, whole groups, all but two experts, all of them."""
+    T, E, k = 24, 40, 5
+    bias = _bias(E, 6, with_bias)
+    x, x64 = _logits(T, E, 8, torch.float32, router, bias, k, G, kg, score)
+    rng = np.random.default_rng(9)
+    x64 = x64.copy()
+    x64[:10][rng.random((10, E)) < 0.3] = -np.inf
+    x64[10:16, :E // 2] = -np.inf
+    x64[16:20] = np.where(np.isin(np.arange(E), (11, 29)), x64[16:20], -np.inf)
+    x64[20:] = -np.inf
+    idx, margin = O.select(x64, bias, router, k, G, kg, score)
+    clear = margin > 1e-5
+    desc = mok.make_route_desc(T, E, k, router, True, n_group=G, topk_group=kg, group_score=score, balance_coef=1.0)
+    r = mok.Router(desc, balance=True, scores=True)
+    out = r.forward(torch.tensor(x64).float().cuda(), _cuda(bias))
+    got = out["topk_idx"].cpu().numpy()
+    assert clear[20:].all() and np.array_equal(got[clear], idx[clear])
+    s = O.scores(x64, router)
+    assert np.allclose(f64(out["gates"]), O.gates(s, got, True, 1.0), rtol=REL, atol=0)
+    assert np.allclose(f64(out["prob_sum"]), O.probabilities(s).sum(axis=0), rtol=REL, atol=0)
+    dg = np.random.default_rng(1).normal(size=(T, k)).astype(np.float32)
+    dp = np.random.default_rng(2).normal(size=E).astype(np.float32)
+    dl = f64(r.backward(torch.tensor(x64).float().cuda(), out["topk_idx"], _cuda(dg), _cuda(dp)))
+    want = O.backward(x64, got, dg.astype(np.float64), dp.astype(np.float64), router, True, 1.0)
+    # sums over the token's terms: at most 8 times its largest score and gradients
+    size = (np.abs(dg).max() + np.abs(dp).max()) * 8 / np.maximum(np.take_along_axis(s, got.astype(np.int64), 1).sum(1), 1e-30)
+    assert np.isfinite(dl).all()
+    assert (np.abs(dl - want) <= REL * np.minimum(size, 1e4)[:, None]).all()
+    assert not dl[20:].any() and not dl[np.isneginf(x64)].any()
+
+
+def test_nan_logits_rank_last():
+    """An expert with a NaN logit is taken only when nothing else is left; indices stay valid and distinct."""
+    x = torch.randn(16, 24, generator=torch.Generator().manual_seed(0))
+    x[:8, 5] = float("nan")
+    x[8:, :] = float("nan")
+    x[8:, 3] = 1.0
+    for router in (SIGMOID, SOFTMAX):
+        r = mok.Router(mok.make_route_desc(16, 24, 4, router, True, n_group=4, topk_group=2, balance_coef=1.0), balance=True)
+        out = r.forward(x.cuda())
+        idx = out["topk_idx"].cpu().numpy()
+        assert not (idx[:8] == 5).any()
+        assert all(len(set(row)) == 4 and min(row) >= 0 and max(row) < 24 for row in idx.tolist())
+        assert (idx[8:, 0] == 3).all()
+        assert torch.isnan(out["prob_sum"]).all() and torch.isnan(out["loss"]).all()
+        # the next call on finite logits is not touched by it
+        again = r.forward(torch.zeros(16, 24).cuda())
+        assert torch.allclose(again["prob_sum"], torch.full((24,), 16 / 24).cuda(), rtol=1e-6)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("E,offset", [(256, 0), (256, 3), (160, 8), (61, 1)])
+def test_rows_of_a_wider_tensor(dtype, E, offset):
+    """Rows that are a slice of wider ones (aligned and not): forward and backward as on a copy."""
+    T, k = 50, 6
+    wide = torch.randn(T, E + 16, generator=torch.Generator().manual_seed(1)).to(dtype).cuda()
+    x = wide[:, offset:offset + E]
+    r = mok.Router(mok.make_route_desc(T, E, k, SIGMOID, True), dtype=dtype)
+    a = {n: t.clone() for n, t in r.forward(x).items()}
+    b = r.forward(x.contiguous())
+    assert all(torch.equal(a[n], b[n]) for n in a)
+    dg = torch.randn(T, k, generator=torch.Generator().manual_seed(2)).cuda()
+    dp = torch.randn(E, generator=torch.Generator().manual_seed(3)).cuda()
+    room = torch.full((T, E + 16), 7.0, dtype=dtype, device="cuda")
+    r.backward(x, a["topk_idx"], dg, dp, out=room[:, offset:offset + E])
+    assert torch.equal(room[:, offset:offset + E], r.backward(x.contiguous(), a["topk_idx"], dg, dp))
+    assert (room[:, :offset] == 7).all() and (room[:, offset + E:] == 7).all()
+
+
+@pytest.mark.parametrize("T", [0, 1, 2, 300, 5000, 20000])
+def test_balance_outputs_at_every_length(T):
+    E, k = 256, 8
+    x = torch.randn(T, E, generator=torch.Generator().manual_seed(T)) + torch.linspace(-1, 1, E)
+    bias = torch.linspace(0.02, -0.02, E)
+    desc = mok.make_route_desc(T, E, k, SIGMOID, True, n_group=8, topk_group=4, balance_coef=2.0, bias_rate=0.001)
+    r = mok.Router(desc, balance=True)
+    b = bias.cuda()
+    first = {n: t.clone() for n, t in r.forward(x.cuda(), b).items()}
+    again = r.forward(x.cuda(), b)
+    assert all(torch.equal(first[n], again[n]) for n in first)       # any order of the blocks gives these bits
+    idx = first["topk_idx"].cpu().numpy()
+    s = O.scores(x.double().numpy(), SIGMOID)
+    counts, prob_sum, loss, dprob, moved = O.balance(s, idx, 2.0, bias.double().numpy(), float(np.float32(0.001)))
+    assert np.array_equal(first["counts"].cpu().numpy(), counts)
+    assert np.allclose(f64(first["prob_sum"]), prob_sum, rtol=REL, atol=0)
+    assert np.allclose(f64(first["loss"]), [loss], rtol=REL, atol=0)
+    assert np.allclose(f64(first["dprob"]), dprob, rtol=REL, atol=0)
+    assert np.allclose(f64(first["bias_next"]), moved, rtol=0, atol=2.0 ** -24)
+    r.forward(x.cuda(), b, bias_next=b)                               # the bias moved in place
+    assert torch.equal(b, first["bias_next"])
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "T%d_E%d_k%d" % s[:3])
+@pytest.mark.parametrize("router", [SIGMOID, SOFTMAX])
+@pytest.mark.parametrize("use", ["gates", "prob", "both"])
+def test_route_backward(shape, router, use):
+    T, E, k, G, kg, score = shape
+    rng = np.random.default_rng(13)
+    for dtype, renorm in ((torch.float32, True), (torch.bfloat16, False)):
+        x = torch.tensor(rng.normal(size=(T, E)) * 1.5).to(dtype)
+        x64 = x.double().numpy()
+        idx = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+        dg = rng.normal(size=(T, k)).astype(np.float32) if use != "prob" else None
+        dp = rng.normal(size=E).astype(np.float32) if use != "gates" else None
+        desc = mok.make_route_desc(T, E, k, router, renorm, route_scale=2.5, n_group=G, topk_group=kg, group_score=score)
+        status = torch.zeros(2, dtype=torch.int32, device="cuda")
+        got = f64(mok.Router(desc, dtype=dtype).backward(x.cuda(), _cuda(idx), _cuda(dg), _cuda(dp), device_status=status))
+        want = O.backward(x64, idx, None if dg is None else dg.astype(np.float64),
+                          None if dp is None else dp.astype(np.float64), router, renorm, 2.5)
+        s = O.scores(x64, router)
+        S = np.take_along_axis(s, idx.astype(np.int64), 1).sum(1, keepdims=True)
+        # sizes of the terms that each entry is a sum of
+        dsel = np.zeros((T, E))
+        if dg is not None:
+            np.put_along_axis(dsel, idx.astype(np.int64), 2.5 * (np.abs(dg) + np.abs(dg).max(1, keepdims=True) * renorm) /
+                              (S if renorm else 1.0), 1)
+        both = dsel if dp is None else dsel + (np.abs(dp) + np.abs(dp).max()) / (s.sum(1, keepdims=True) if router else 1.0)
+        size = s * (both + (0 if router else (s * both).sum(1, keepdims=True)))
+        tol = REL * size + (np.abs(want) * 2.0 ** -8 if dtype == torch.bfloat16 else 0) + 1e-38
+        assert (np.abs(got - want) <= tol).all(), (dtype, np.abs(got - want).max())
+        assert status.tolist() == [0, 0]
+
+
+def test_backward_leaves_out_and_reports_a_bad_index():
+    T, E, k = 4, 32, 3
+    x = torch.randn(T, E, generator=torch.Generator().manual_seed(0)).cuda()
+    idx = torch.tensor([[0, 1, 2]] * T, dtype=torch.int32)
+    bad = idx.clone()
+    bad[1, 2], bad[2, 0] = E, -1
+    dg = torch.ones(T, k).cuda()
+    r = mok.Router(mok.make_route_desc(T, E, k, SIGMOID, False))
+    status = torch.zeros(2, dtype=torch.int32, device="cuda")
+    a = r.backward(x, bad.cuda(), dg, device_status=status)
+    assert status[0].item() == 6
+    b = r.backward(x, idx.cuda(), dg)
+    b[1, 2], b[2, 0] = 0, 0
+    assert torch.equal(a, b)
+
+
+def test_no_tokens():
+    r = mok.Router(mok.make_route_desc(0, 16, 2, SIGMOID, True))
+    x = torch.empty(0, 16).cuda()
+    assert r.forward(x)["topk_idx"].shape == (0, 2)
+    assert r.backward(x, torch.empty(0, 2, dtype=torch.int32).cuda(), torch.empty(0, 2).cuda()).shape == (0, 16)
+
+
+def test_rows_past_32_bit_offsets():
+    """More than 2^31 logits: the last tokens are routed, and their gradients written, as on their own."""
+    T, E, k, tail = 2 ** 21 + 3, 1024, 4, 100
+    x = torch.zeros(T, E, dtype=torch.bfloat16, device="cuda")
+    x[-tail:] = torch.randn(tail, E, generator=torch.Generator().manual_seed(0)).bfloat16().cuda()
+    x[-2 * tail:-tail] = x[-tail:]
+    big = mok.Router(mok.make_route_desc(T, E, k, SIGMOID, True, n_group=8, topk_group=4), dtype=torch.bfloat16)
+    small = mok.Router(mok.make_route_desc(tail, E, k, SIGMOID, True, n_group=8, topk_group=4), dtype=torch.bfloat16)
+    a, b = big.forward(x), small.forward(x[-tail:])
+    assert torch.equal(a["topk_idx"][-tail:], b["topk_idx"]) and torch.equal(a["gates"][-2 * tail:-tail], b["gates"])
+    assert (a["topk_idx"][:1000] == torch.arange(k, device="cuda")).all()
+    dg = torch.ones(T, k, device="cuda") + torch.arange(k, device="cuda")
+    dl, small_dl = big.backward(x, a["topk_idx"], dg), small.backward(x[-tail:], b["topk_idx"], dg[:tail])
+    assert torch.equal(dl[-tail:], small_dl) and torch.equal(dl[-2 * tail:-tail], small_dl)
+
+
+def test_on_another_stream_and_in_a_graph():
+    T, E, k = 300, 256, 8
+    x = torch.randn(T, E, generator=torch.Generator().manual_seed(4)).cuda()
+    bias = torch.zeros(E, device="cuda")
+    r = mok.Router(mok.make_route_desc(T, E, k, SIGMOID, True, n_group=8, topk_group=4, balance_coef=1.0, bias_rate=0.1),
+                   balance=True)
+    want = {n: t.clone() for n, t in r.forward(x, bias).items()}
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for t in r.out.values():
+        t.zero_()
+    torch.cuda.synchronize()
+    out = r.forward(x, bias, stream=side)
+    side.synchronize()
+    assert all(torch.equal(out[n], want[n]) for n in want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r.forward(x, bias)
+        dl = r.backward(x, r.out["topk_idx"], torch.ones(T, k, device="cuda"), r.out["dprob"])
+    for _ in range(2):
+        for t in r.out.values():
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(out[n], want[n]) for n in want)
+    assert torch.equal(dl, r.backward(x, r.out["topk_idx"], torch.ones(T, k, device="cuda"), r.out["dprob"]))
+
+
+# ------------------------------------------------------------------ the layer with groups
+
+GROUPED = W.MoEShape("grouped_T200_H256_E32_I256_top4", T=200, H=256, E=32, I=256, k=4, router=SIGMOID, renorm=True,
+                     x_std=1.0, w_std=0.05)
+
+
+@pytest.mark.parametrize("router,score", [(SIGMOID, TOP2), (SOFTMAX, MAX)])
+@pytest.mark.parametrize("mxfp8", [False, True])
+def test_layer_routes_within_groups(router, score, mxfp8):
+    """The layer's selection, gates and scores with groups are mok_route's on the layer's own logits; the rest
+    of the forward is the layer's on that selection, given."""
+    shape = GROUPED.scaled(router=router, renorm=router == SIGMOID, mxfp8=mxfp8)
+    inp = {n: t.cuda() for n, t in W.make_inputs(shape, seed=3).items() if t is not None}
+    bias = _cuda(_bias(32, 4, router == SIGMOID))
+    kw = dict(n_group=8, topk_group=3, group_score=score)
+    layer, given = mok.MoELayer(mok.desc_from_shape(shape, **kw)), mok.MoELayer(mok.desc_from_shape(shape))
+    results = []
+    for lay, sel in ((layer, None), (given, "given")):
+        sel = None if sel is None else layer.view("topk_idx").clone()
+        if mxfp8:
+            wq = mok.quantize_weights(lay.desc, inp["w13"], inp["w2"])
+            y = torch.empty((shape.T, shape.H), dtype=torch.bfloat16, device="cuda")
+            mok.moe_forward_mxfp8(lay.desc, inp["x"], inp["w_router"], bias, sel, wq, y, lay.ctx, lay.ws)
+        else:
+            y = lay.forward(inp["x"], inp["w_router"], inp["w13"], inp["w2"], router_bias=bias, given_topk=sel)
+        assert lay.status() == (0, 0)
+        results.append(y)
+    assert torch.equal(results[0], results[1])
+    desc = mok.make_route_desc(shape.T, 32, 4, router, shape.renorm, **kw)
+    out = mok.Router(desc, scores=True).forward(layer.view("logits"), bias)
+    for n in ("topk_idx", "gates", "scores"):
+        assert torch.equal(out[n], layer.view(n)), n
+    idx = out["topk_idx"].cpu().numpy()
+    assert max(len(set(row // 4)) for row in idx) <= 3
+    if mxfp8:
+        return
+    # the schedule entry points take the same selection
+    outs = {n: torch.empty(s, dtype=torch.int32, device="cuda") for n, s in
+            (("topk_idx", (200, 4)), ("counts", (32,)), ("offsets", (33,)), ("row_of", (800,)), ("src_of", (800,)))}
+    gates = torch.empty((200, 4), device="cuda")
+    rest = (outs["topk_idx"], gates, outs["counts"], outs["offsets"], outs["row_of"], outs["src_of"])
+    from mixture_experts_layer_table_gb300 import _native as N
+    for call in (lambda: mok.schedule(layer.desc, inp["x"], inp["w_router"], bias, None, *rest, layer.ws),
+                 lambda: N.schedule_noalloc(layer.desc, inp["x"], inp["w_router"], bias, None, *rest)):
+        outs["topk_idx"].fill_(-1)
+        call()
+        assert torch.equal(outs["topk_idx"], out["topk_idx"]) and torch.equal(gates, out["gates"])
+    # the gate gradients go back through the same Jacobian
+    grads = given.backward(inp["dy"], inp["x"], inp["w_router"], inp["w13"], inp["w2"])
+    mine = layer.forward(inp["x"], inp["w_router"], inp["w13"], inp["w2"], router_bias=bias)
+    assert torch.equal(mine, results[0])
+    grouped = layer.backward(inp["dy"], inp["x"], inp["w_router"], inp["w13"], inp["w2"])
+    assert all(torch.equal(grads[n], grouped[n]) for n in grads)
+    dl = mok.Router(desc).backward(layer.view("logits"), layer.view("topk_idx"), grads["dgates"])
+    assert torch.allclose(dl, layer.view("dlogits"), rtol=1e-4, atol=1e-6 * layer.view("dlogits").abs().max().item())
+
+
+def test_layer_refuses_bad_groups():
+    for kw in (dict(n_group=-1), dict(n_group=5, topk_group=1), dict(n_group=8, topk_group=0),
+               dict(n_group=8, topk_group=9), dict(n_group=32, topk_group=3), dict(n_group=8, topk_group=2, group_score=2)):
+        with pytest.raises(mok.MokError):
+            mok.get_layout(mok.desc_from_shape(GROUPED, **kw))

@@ -89,3 +89,67 @@ def test_the_binding_refuses_host_tensors_and_mismatches(lib):
         mok.AdamW([t], [t], betas=(0.9, 1.0))
     with pytest.raises(ValueError, match="max_norm"):
         mok.GradNorm([t], 0.0)
+
+
+def _route_desc(**kw):
+    d = mok.make_route_desc(10, 32, 4, 1, True, n_group=8, topk_group=4)
+    for n, v in kw.items():
+        setattr(d, n, v)
+    return d
+
+
+@pytest.mark.parametrize("kw,code", [(dict(T=-1), 1), (dict(E=0), 1), (dict(k=0), 1), (dict(k=17), 1), (dict(router=2), 1),
+                                     (dict(group_score=2), 1), (dict(n_group=0), 1), (dict(n_group=5), 1),
+                                     (dict(topk_group=0), 1), (dict(topk_group=9), 1), (dict(logits_type=2), 1),
+                                     (dict(logits_stride=31), 1), (dict(route_scale=float("nan")), 1),
+                                     (dict(balance_coef=float("inf")), 1), (dict(bias_rate=float("nan")), 1),
+                                     (dict(reserved=1), 1), (dict(E=2048), 2), (dict(E=64, n_group=64, topk_group=64), 2),
+                                     (dict(E=64, n_group=1, topk_group=1, k=17), 2), (dict(topk_group=1, k=5), 1)])
+def test_route_refuses_a_bad_descriptor(lib, kw, code):
+    from mixture_experts_layer_table_gb300 import routing as RT
+    a = [P(0x100000 * (i + 1)) for i in range(12)]
+    d = ctypes.byref(_route_desc(**kw))
+    assert RT._route_fn()(d, *a[:10], a[10], RT.ROUTE_WS_BYTES, None) == code
+    assert RT._route_backward_fn()(d, *a[:5], 0, a[5], None) == code
+
+
+def test_route_refuses_bad_pointers_and_workspaces(lib):
+    from mixture_experts_layer_table_gb300 import routing as RT
+    d = _route_desc()
+    names = ("logits", "bias", "topk_idx", "gates", "scores", "counts", "prob_sum", "loss", "dprob", "bias_next")
+    ok = {n: 0x100000 * (i + 1) for i, n in enumerate(names)}
+
+    def call(ws=0xF00000, n=RT.ROUTE_WS_BYTES, **kw):
+        p = {**ok, **kw}
+        return RT._route_fn()(ctypes.byref(d), *[p[n] for n in names], ws, n, None)
+
+    for n in names:
+        assert call(n=0, **{n: 0x100002}) == INVALID, n
+    assert call(logits=None) == INVALID and call(topk_idx=None) == INVALID
+    assert call(bias=None) == INVALID                       # bias_next without a bias
+    assert call(ws=None) == INVALID and call(ws=0xF00010) == INVALID
+    assert call(n=RT.ROUTE_WS_BYTES - 1) == WS_SMALL
+    d.T = 1 << 31
+    assert call() == 2
+    d.T = 10
+    back = RT._route_backward_fn()
+    a = [P(0x100000 * (i + 1)) for i in range(6)]
+
+    def call_back(logits=a[0], idx=a[1], dg=a[2], dp=a[3], out=a[4], stride=0, status=a[5]):
+        return back(ctypes.byref(d), logits, idx, dg, dp, out, stride, status, None)
+
+    assert call_back(dg=None, dp=None) == INVALID
+    assert call_back(idx=None) == INVALID and call_back(logits=None) == INVALID and call_back(out=None) == INVALID
+    assert call_back(stride=31) == INVALID and call_back(out=P(0x100002)) == INVALID and call_back(status=P(0x100001)) == INVALID
+
+
+def test_the_router_binding_refuses_mismatches(lib):
+    r = mok.Router(mok.make_route_desc(4, 8, 2, 1, True), device="cpu")
+    with pytest.raises(ValueError, match="CUDA"):
+        r.forward(torch.zeros(4, 8))
+    with pytest.raises(ValueError, match="logits"):
+        r.forward(torch.zeros(4, 9))
+    with pytest.raises(ValueError, match="logits"):
+        r.forward(torch.zeros(4, 8).bfloat16())
+    with pytest.raises(ValueError, match="float32 or bfloat16"):
+        mok.Router(mok.make_route_desc(4, 8, 2, 1, True), dtype=torch.float16, device="cpu")
