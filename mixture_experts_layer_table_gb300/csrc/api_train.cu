@@ -200,9 +200,12 @@ mok_status mok_adamw_step(const mok_adamw_tensor* tensors, int32_t count, const 
       !(hyper->eps >= 0.0) || !std::isfinite(hyper->eps) || hyper->step < 1 || hyper->reserved != 0)
     return MOK_ERR_INVALID_ARG;
   if (!aligned_elem(grad_scale, MOK_ELEM_F32)) return MOK_ERR_INVALID_ARG;
+  unsigned kinds = 0;  // bit kind_of(t) of every kind of tensor there is
+  auto kind_of = [](const mok_adamw_tensor& t) { return (param_kind(t) * 2 + t.grad_type) * 2 + t.state_type; };
   for (int32_t i = 0; i < count; ++i) {
     const mok_status s = check_adamw(tensors[i]);
     if (s != MOK_OK) return s;
+    if (tensors[i].n > 0) kinds |= 1u << kind_of(tensors[i]);
   }
   const int n_sm = sm_count();
   if (n_sm <= 0) return MOK_ERR_CUDA;
@@ -216,28 +219,19 @@ mok_status mok_adamw_step(const mok_adamw_tensor* tensors, int32_t count, const 
   h.inv_bc1 = (float)(1.0 / (1.0 - std::pow(hyper->beta1, (double)hyper->step)));
   h.inv_bc2_sqrt = (float)(1.0 / std::sqrt(1.0 - std::pow(hyper->beta2, (double)hyper->step)));
   h.seed = hyper->seed ^ ((uint32_t)hyper->step * 0x9E3779B1u);
-  // tensors of the same kinds share a launch
-  for (int param = 0; param < 3; ++param) {
-    for (int grad = 0; grad < 2; ++grad) {
-      for (int state = 0; state < 2; ++state) {
-        mok::AdamTensor part[mok::OPTIM_TABLE];
-        int n = 0;
-        auto flush = [&]() -> mok_status {
-          if (n > 0) MOK_LAUNCH("adamw", st, mok::launch_adamw(part, n, param, grad, state, h, grad_scale, n_sm, st));
-          n = 0;
-          return MOK_OK;
-        };
-        for (int32_t i = 0; i < count; ++i) {
-          const mok_adamw_tensor& t = tensors[i];
-          if (t.n == 0 || param_kind(t) != param || t.grad_type != grad || t.state_type != state) continue;
-          part[n++] = {t.param, t.master, t.grad, t.m, t.v, t.m_scale, t.v_scale, t.n, t.counter, t.lr, t.weight_decay};
-          if (n == mok::OPTIM_TABLE) {
-            const mok_status s = flush();
-            if (s != MOK_OK) return s;
-          }
-        }
-        const mok_status s = flush();
-        if (s != MOK_OK) return s;
+  // tensors of one kind share a launch
+  for (int kind = 0; kind < 12; ++kind) {
+    if (!(kinds >> kind & 1u)) continue;
+    mok::AdamTensor part[mok::OPTIM_TABLE];
+    int n = 0;
+    for (int32_t i = 0; i < count; ++i) {
+      const mok_adamw_tensor& t = tensors[i];
+      if (t.n > 0 && kind_of(t) == kind)
+        part[n++] = {t.param, t.master, t.grad, t.m, t.v, t.m_scale, t.v_scale, t.n, t.counter, t.lr, t.weight_decay};
+      if (n == mok::OPTIM_TABLE || (n > 0 && i == count - 1)) {
+        MOK_LAUNCH("adamw", st,
+                   mok::launch_adamw(part, n, kind / 4, kind / 2 % 2, kind % 2, h, grad_scale, n_sm, st));
+        n = 0;
       }
     }
   }

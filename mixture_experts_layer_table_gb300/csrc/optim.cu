@@ -16,16 +16,18 @@ constexpr int CHUNK = ADAM_THREADS * VEC;   // elements of one block
 constexpr int NORM_THREADS = 512;
 constexpr int NORM_CHUNK = NORM_THREADS * VEC * 4;
 
-template <typename Tensor>
+// Two sizes: a launch with 21 KB of parameters costs its caller about 0.7 us more than one with 1.4 KB.
+constexpr int SMALL_TABLE = 16;
+template <typename Tensor, int CAP>
 struct Table {
-  Tensor t[OPTIM_TABLE];
-  int32_t first[OPTIM_TABLE + 1];  // first chunk of each tensor; first[count] = chunks in all
+  Tensor t[CAP];
+  int32_t first[CAP + 1];  // first chunk of each tensor; first[count] = chunks in all
   int32_t count;
 };
 
 // The tensor that holds chunk c: the last one whose first chunk is <= c (empty tensors have none).
-template <typename Tensor>
-__device__ __forceinline__ int tensor_of(const Table<Tensor>& tab, int c) {
+template <typename Tensor, int CAP>
+__device__ __forceinline__ int tensor_of(const Table<Tensor, CAP>& tab, int c) {
   int lo = 0, hi = tab.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -171,9 +173,9 @@ __device__ __forceinline__ void store_state8(uint8_t* q, uint8_t* scale, int64_t
 // at random with the mean unchanged.  sqrt(v) > 0 never becomes 0, so that no step divides by eps alone.
 // bf16 parameters without an f32 master are rounded the same way (their updates are below half a spacing too).
 // A clip factor c that is NaN leaves the tensor as it is (grad_norm gives one for gradients that are not finite).
-template <int PK, int GK, int SK>
+template <int PK, int GK, int SK, int CAP>
 __global__ void __launch_bounds__(ADAM_THREADS)
-    adamw_kernel(const __grid_constant__ Table<AdamTensor> tab, const AdamHyper h, const float* __restrict__ grad_scale) {
+    adamw_kernel(const __grid_constant__ Table<AdamTensor, CAP> tab, const AdamHyper h, const float* __restrict__ grad_scale) {
   const float c = grad_scale != nullptr ? *grad_scale : 1.0f;
   if (isnan(c)) return;
   const int chunk = blockIdx.x;
@@ -246,8 +248,9 @@ __global__ void __launch_bounds__(ADAM_THREADS)
 // ----------------------------------------------------------------------------- gradient norm
 // Each block sums its chunks' squares in f32 per thread and in f64 from there on; the block that comes last in
 // the call adds the blocks' sums in their order, so that the result does not depend on the order of arrival.
+template <int CAP>
 __global__ void __launch_bounds__(NORM_THREADS)
-    grad_norm_kernel(const __grid_constant__ Table<GradTensor> tab, int first_block, int total_blocks, float max_norm,
+    grad_norm_kernel(const __grid_constant__ Table<GradTensor, CAP> tab, int first_block, int total_blocks, float max_norm,
                      float* __restrict__ out, unsigned* __restrict__ ticket, double* __restrict__ partials) {
   __shared__ double warp_sum[NORM_THREADS / 32];
   __shared__ bool last;
@@ -304,60 +307,74 @@ __global__ void __launch_bounds__(NORM_THREADS)
   }
 }
 
-template <int PK, int GK>
-cudaError_t launch_state(int state, int blocks, const Table<AdamTensor>& tab, const AdamHyper& h, const float* scale,
-                         cudaStream_t st) {
-  if (state == STATE_F32) adamw_kernel<PK, GK, STATE_F32><<<blocks, ADAM_THREADS, 0, st>>>(tab, h, scale);
-  else adamw_kernel<PK, GK, STATE_MX8><<<blocks, ADAM_THREADS, 0, st>>>(tab, h, scale);
-  return cudaGetLastError();
-}
-
-template <int PK>
-cudaError_t launch_grad_kind(int grad, int state, int blocks, const Table<AdamTensor>& tab, const AdamHyper& h,
-                             const float* scale, cudaStream_t st) {
-  return grad == GRAD_F32 ? launch_state<PK, GRAD_F32>(state, blocks, tab, h, scale, st)
-                          : launch_state<PK, GRAD_BF16>(state, blocks, tab, h, scale, st);
-}
-
-}  // namespace
-
-cudaError_t launch_adamw(const AdamTensor* tensors, int count, int param, int grad, int state, const AdamHyper& h,
-                         const float* grad_scale, int n_sm, cudaStream_t st) {
-  Table<AdamTensor> tab;
-  tab.count = count;
+// The table of `count` tensors; returns their chunks, or -1 if there are more than a grid has blocks.
+template <typename Tensor, int CAP, typename Chunks>
+int64_t fill_table(Table<Tensor, CAP>& tab, const Tensor* tensors, int count, Chunks chunks_of) {
   int64_t chunks = 0;
   for (int i = 0; i < count; ++i) {
     tab.t[i] = tensors[i];
     tab.first[i] = (int32_t)chunks;
-    chunks += (tensors[i].n + CHUNK - 1) / CHUNK;
-    if (chunks > INT32_MAX) return cudaErrorInvalidValue;
+    chunks += chunks_of(tensors[i].n);
+    if (chunks > INT32_MAX) return -1;
   }
   tab.first[count] = (int32_t)chunks;
+  tab.count = count;
+  return chunks;
+}
+
+template <int PK, int GK, int SK, int CAP>
+cudaError_t launch_table(const AdamTensor* tensors, int count, const AdamHyper& h, const float* scale, cudaStream_t st) {
+  Table<AdamTensor, CAP> tab;
+  const int64_t chunks = fill_table(tab, tensors, count, [](int64_t n) { return (n + CHUNK - 1) / CHUNK; });
+  if (chunks < 0) return cudaErrorInvalidValue;
   if (chunks == 0) return cudaSuccess;
-  if (param == PARAM_F32) return launch_grad_kind<PARAM_F32>(grad, state, (int)chunks, tab, h, grad_scale, st);
-  if (param == PARAM_BF16_MASTER)
-    return launch_grad_kind<PARAM_BF16_MASTER>(grad, state, (int)chunks, tab, h, grad_scale, st);
-  return launch_grad_kind<PARAM_BF16>(grad, state, (int)chunks, tab, h, grad_scale, st);
+  adamw_kernel<PK, GK, SK, CAP><<<(int)chunks, ADAM_THREADS, 0, st>>>(tab, h, scale);
+  return cudaGetLastError();
+}
+
+template <int PK, int GK>
+cudaError_t launch_kind(const AdamTensor* t, int count, int state, const AdamHyper& h, const float* scale,
+                        cudaStream_t st) {
+  const bool small = count <= SMALL_TABLE;
+  if (state == STATE_F32)
+    return small ? launch_table<PK, GK, STATE_F32, SMALL_TABLE>(t, count, h, scale, st)
+                 : launch_table<PK, GK, STATE_F32, OPTIM_TABLE>(t, count, h, scale, st);
+  return small ? launch_table<PK, GK, STATE_MX8, SMALL_TABLE>(t, count, h, scale, st)
+               : launch_table<PK, GK, STATE_MX8, OPTIM_TABLE>(t, count, h, scale, st);
+}
+
+template <int CAP>
+cudaError_t launch_norm(const GradTensor* tensors, int count, int blocks, int first_block, int total_blocks,
+                        float max_norm, float* out, void* ws, cudaStream_t st) {
+  Table<GradTensor, CAP> tab;
+  if (fill_table(tab, tensors, count, grad_norm_chunks) < 0) return cudaErrorInvalidValue;
+  grad_norm_kernel<CAP><<<blocks, NORM_THREADS, 0, st>>>(
+      tab, first_block, total_blocks, max_norm, out, static_cast<unsigned*>(ws),
+      reinterpret_cast<double*>(static_cast<char*>(ws) + NORM_PARTIALS_OFFSET));
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_adamw(const AdamTensor* t, int count, int param, int grad, int state, const AdamHyper& h,
+                         const float* grad_scale, int n_sm, cudaStream_t st) {
+  switch (param * 2 + grad) {
+    case PARAM_F32 * 2 + GRAD_F32: return launch_kind<PARAM_F32, GRAD_F32>(t, count, state, h, grad_scale, st);
+    case PARAM_F32 * 2 + GRAD_BF16: return launch_kind<PARAM_F32, GRAD_BF16>(t, count, state, h, grad_scale, st);
+    case PARAM_BF16_MASTER * 2 + GRAD_F32: return launch_kind<PARAM_BF16_MASTER, GRAD_F32>(t, count, state, h, grad_scale, st);
+    case PARAM_BF16_MASTER * 2 + GRAD_BF16: return launch_kind<PARAM_BF16_MASTER, GRAD_BF16>(t, count, state, h, grad_scale, st);
+    case PARAM_BF16 * 2 + GRAD_F32: return launch_kind<PARAM_BF16, GRAD_F32>(t, count, state, h, grad_scale, st);
+    default: return launch_kind<PARAM_BF16, GRAD_BF16>(t, count, state, h, grad_scale, st);
+  }
 }
 
 int64_t grad_norm_chunks(int64_t n) { return (n + NORM_CHUNK - 1) / NORM_CHUNK; }
 
 cudaError_t launch_grad_norm(const GradTensor* tensors, int count, int blocks, int first_block, int total_blocks,
                              float max_norm, float* out, void* ws, cudaStream_t st) {
-  Table<GradTensor> tab;
-  tab.count = count;
-  int64_t chunks = 0;
-  for (int i = 0; i < count; ++i) {
-    tab.t[i] = tensors[i];
-    tab.first[i] = (int32_t)chunks;
-    chunks += grad_norm_chunks(tensors[i].n);
-    if (chunks > INT32_MAX) return cudaErrorInvalidValue;
-  }
-  tab.first[count] = (int32_t)chunks;
-  grad_norm_kernel<<<blocks, NORM_THREADS, 0, st>>>(
-      tab, first_block, total_blocks, max_norm, out, static_cast<unsigned*>(ws),
-      reinterpret_cast<double*>(static_cast<char*>(ws) + NORM_PARTIALS_OFFSET));
-  return cudaGetLastError();
+  if (count <= SMALL_TABLE)
+    return launch_norm<SMALL_TABLE>(tensors, count, blocks, first_block, total_blocks, max_norm, out, ws, st);
+  return launch_norm<OPTIM_TABLE>(tensors, count, blocks, first_block, total_blocks, max_norm, out, ws, st);
 }
 
 }  // namespace mok

@@ -11,7 +11,7 @@ from typing import Dict, Optional
 
 import torch
 
-from ._native import _check, _expect, _ptr, _stream, load
+from ._native import _check, _expect, _stream, load
 
 P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 
@@ -60,8 +60,16 @@ def _rows(t, T, E, dtype, name) -> int:
     return t.stride(0) if T > 1 else E
 
 
+def _address(t, shape, dtype, name):
+    """The address of a contiguous CUDA tensor of this shape and type."""
+    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.is_cuda and t.is_contiguous()):
+        _expect(t, shape, dtype, name)
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
 class Router:
-    """One routing descriptor with its output buffers, which each call overwrites.
+    """One routing descriptor with its output buffers, which each ``forward`` overwrites.
 
     ``forward`` returns {"topk_idx", "gates"}, with ``scores`` also "scores", and with ``balance``
     also "counts", "prob_sum", "loss", "dprob" and, where a bias is given, "bias_next"."""
@@ -84,8 +92,11 @@ class Router:
             self.out |= {"counts": new((E,), torch.int32), "prob_sum": new((E,)), "loss": new((1,)), "dprob": new((E,))}
             self.ws = torch.zeros(ROUTE_WS_BYTES, dtype=torch.uint8, device=device)
         self.bias_next = new((E,)) if balance else None
-        self._args = [_ptr(self.out.get(n)) for n in ("topk_idx", "gates", "scores", "counts", "prob_sum", "loss", "dprob")]
-        self._ws = _ptr(self.ws)
+        address = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        self._args = tuple(address(self.out.get(n))
+                           for n in ("topk_idx", "gates", "scores", "counts", "prob_sum", "loss", "dprob"))
+        self._ws = address(self.ws)
+        self._shape, self._sel, self._experts = (T, E), (T, k), (E,)
         self._ref = ctypes.byref(self.desc)
         self._call = _route_fn()
         self._call_backward = _route_backward_fn()
@@ -93,34 +104,47 @@ class Router:
     def forward(self, logits: torch.Tensor, bias: Optional[torch.Tensor] = None,
                 bias_next: Optional[torch.Tensor] = None, stream=None) -> Dict[str, torch.Tensor]:
         """``bias_next``: where the moved bias goes (with ``balance``), e.g. ``bias`` itself."""
-        d = self.desc
-        d.logits_stride = _rows(logits, d.T, d.E, self.dtype, "logits")
-        out, moved = self.out, None
+        self._take_logits(logits)
+        out, moved, b = self.out, None, None
         if bias is not None:
-            _expect(bias, (d.E,), torch.float32, "bias")
+            b = _address(bias, self._experts, torch.float32, "bias")
             if self.balance:
-                moved = self.bias_next if bias_next is None else bias_next
-                _expect(moved, (d.E,), torch.float32, "bias_next")
-                out = dict(out, bias_next=moved)
-        _check("mok_route", self._call(self._ref, logits.data_ptr(), _ptr(bias), *self._args, _ptr(moved), self._ws,
-                                       ROUTE_WS_BYTES, _stream(stream)))
+                to = self.bias_next if bias_next is None else bias_next
+                moved = _address(to, self._experts, torch.float32, "bias_next")
+                out = dict(out, bias_next=to)
+        code = self._call(self._ref, logits.data_ptr(), b, *self._args, moved, self._ws, ROUTE_WS_BYTES,
+                          _stream(stream))
+        if code:
+            _check("mok_route", code)
         return out
 
     def backward(self, logits: torch.Tensor, topk_idx: Optional[torch.Tensor], dgates: Optional[torch.Tensor],
                  dprob: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
                  device_status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-        """Gradient with respect to the logits, in their type; ``device_status``: int32 [2] CUDA tensor."""
-        d = self.desc
-        d.logits_stride = _rows(logits, d.T, d.E, self.dtype, "logits")
+        """Gradient with respect to the logits, in their type (``out`` or a new tensor); ``device_status``: int32 [2]
+        CUDA tensor."""
+        self._take_logits(logits)
+        idx = dg = dp = status = None
         if dgates is not None:
-            _expect(dgates, (d.T, d.k), torch.float32, "dgates")
-            _expect(topk_idx, (d.T, d.k), torch.int32, "topk_idx")
-        _expect(dprob, (d.E,), torch.float32, "dprob", nullable=True)
-        _expect(device_status, (2,), torch.int32, "device_status", nullable=True)
+            dg = _address(dgates, self._sel, torch.float32, "dgates")
+            idx = _address(topk_idx, self._sel, torch.int32, "topk_idx")
+        if dprob is not None:
+            dp = _address(dprob, self._experts, torch.float32, "dprob")
+        if device_status is not None:
+            status = _address(device_status, (2,), torch.int32, "device_status")
+        stride = 0
         if out is None:
-            out = torch.empty((d.T, d.E), dtype=self.dtype, device=logits.device)
-        stride = _rows(out, d.T, d.E, self.dtype, "out")
-        _check("mok_route_backward", self._call_backward(
-            self._ref, logits.data_ptr(), _ptr(topk_idx), _ptr(dgates), _ptr(dprob), out.data_ptr(), stride,
-            _ptr(device_status), _stream(stream)))
+            out = torch.empty(self._shape, dtype=self.dtype, device=logits.device)
+        else:
+            stride = _rows(out, *self._shape, self.dtype, "out")
+        code = self._call_backward(self._ref, logits.data_ptr(), idx, dg, dp, out.data_ptr(), stride, status,
+                                   _stream(stream))
+        if code:
+            _check("mok_route_backward", code)
         return out
+
+    def _take_logits(self, logits):
+        if logits.shape == self._shape and logits.dtype is self.dtype and logits.is_cuda and logits.is_contiguous():
+            self.desc.logits_stride = 0
+        else:
+            self.desc.logits_stride = _rows(logits, *self._shape, self.dtype, "logits")

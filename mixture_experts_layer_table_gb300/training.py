@@ -101,8 +101,10 @@ class GradNorm:
         self._out, self._ws = self.result.data_ptr(), self.ws.data_ptr()
 
     def compute(self, stream=None) -> torch.Tensor:
-        _check("mok_grad_norm", self._call(self._table, len(self.grads), self.max_norm, self._out, self._ws,
-                                           GRAD_NORM_WS_BYTES, _stream(stream)))
+        code = self._call(self._table, len(self.grads), self.max_norm, self._out, self._ws, GRAD_NORM_WS_BYTES,
+                          _stream(stream))
+        if code:
+            _check("mok_grad_norm", code)
         return self.result
 
 
@@ -205,13 +207,14 @@ class AdamW:
         factor on every gradient (a NaN skips the update)."""
         scale = None
         if grad_scale is not None:
-            _expect_tensor(grad_scale, "grad_scale", (torch.float32,), 1)
+            if not (grad_scale.dtype is torch.float32 and grad_scale.is_cuda and grad_scale.numel() == 1):
+                _expect_tensor(grad_scale, "grad_scale", (torch.float32,), 1)
             scale = grad_scale.data_ptr()
         self._hyper.step += 1
         code = self._call(self._table, len(self.params), self._hyper_ref, scale, _stream(stream))
-        if code != 0:
+        if code:
             self._hyper.step -= 1
-        _check("mok_adamw_step", code)
+            _check("mok_adamw_step", code)
 
     def state_values(self, i: int) -> Dict[str, torch.Tensor]:
         """m and v of tensor i as float32 values."""
