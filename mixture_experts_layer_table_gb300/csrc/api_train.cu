@@ -215,6 +215,8 @@ mok_status mok_adamw_step(const mok_adamw_tensor* tensors, int32_t count, const 
   h.one_minus_beta1 = (float)(1.0 - hyper->beta1);
   h.beta2 = (float)hyper->beta2;
   h.one_minus_beta2 = (float)(1.0 - hyper->beta2);
+  h.beta2_sqrt = (float)std::sqrt(hyper->beta2);
+  h.one_minus_beta2_sqrt = (float)std::sqrt(1.0 - hyper->beta2);
   h.eps = (float)hyper->eps;
   h.inv_bc1 = (float)(1.0 / (1.0 - std::pow(hyper->beta1, (double)hyper->step)));
   h.inv_bc2_sqrt = (float)(1.0 / std::sqrt(1.0 - std::pow(hyper->beta2, (double)hyper->step)));

@@ -21,6 +21,7 @@ struct AdamTensor {
 
 struct AdamHyper {
   float beta1, one_minus_beta1, beta2, one_minus_beta2, eps;
+  float beta2_sqrt, one_minus_beta2_sqrt;  // square roots of beta2 and 1 - beta2
   float inv_bc1;       // 1 / (1 - beta1^t)
   float inv_bc2_sqrt;  // 1 / sqrt(1 - beta2^t)
   uint32_t seed;
