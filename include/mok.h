@@ -427,9 +427,10 @@ typedef struct {
 /* out[0] = the 2-norm of all gradients together, out[1] = min(1, max_norm / (out[0] + 1e-6)), the
  * factor that clips them to max_norm (> 0, may be infinite), or NaN where the norm is not finite.
  * out is f32 [2] on the device.  ws: at least MOK_GRAD_NORM_WS_BYTES, 16-byte aligned, zero-filled
- * once before its first use (each call leaves it ready for the next).  The sums run in a fixed
- * order, in f64 across threads. */
-#define MOK_GRAD_NORM_WS_BYTES 33024
+ * once before its first use (each call leaves it ready for the next).  The
+ * squares are formed and added in f32, a block's sums in f64, in a fixed order; a gradient above
+ * 1.8e19 in magnitude makes the norm infinite. */
+#define MOK_GRAD_NORM_WS_BYTES 16640
 mok_status mok_grad_norm(const mok_grad_tensor* tensors, int32_t count, float max_norm, float* out, void* ws,
                          size_t ws_bytes, void* stream);
 

@@ -516,13 +516,20 @@ __global__ void __launch_bounds__(MX8_THREADS, 4)
 }
 
 // ----------------------------------------------------------------------------- gradient norm
-// Each block sums its chunks' squares in f32 per thread and in f64 from there on; the block that comes last in
-// the call adds the blocks' sums in their order, so that the result does not depend on the order of arrival.
+// Each block sums its chunks' squares in f32, 8 sums to a thread and a tree over the threads; one warp of the
+// block that comes last in the call adds the blocks' sums in f64 in a fixed order, so that the result does not
+// depend on the order of arrival.
+__device__ __forceinline__ float warp_total(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
 template <int CAP>
 __global__ void __launch_bounds__(NORM_THREADS)
     grad_norm_kernel(const __grid_constant__ Table<GradTensor, CAP> tab, int first_block, int total_blocks, float max_norm,
-                     float* __restrict__ out, unsigned* __restrict__ ticket, double* __restrict__ partials) {
-  __shared__ double warp_sum[NORM_THREADS / 32];
+                     float* __restrict__ out, unsigned* __restrict__ ticket, float* __restrict__ partials) {
+  __shared__ float warp_sum[NORM_THREADS / 32];
   __shared__ bool last;
   float acc[VEC];
 #pragma unroll
@@ -550,36 +557,32 @@ __global__ void __launch_bounds__(NORM_THREADS)
       for (int j = 0; j < VEC; ++j) acc[j] = fmaf(g[j], g[j], acc[j]);
     }
   }
-  double s = 0.0;
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) s += (double)acc[j];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float s = 0.0f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  for (int j = 0; j < VEC; ++j) s += acc[j];
+  s = warp_total(s);
   if (lane == 0) warp_sum[warp] = s;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    double b = 0.0;
-    for (int w = 0; w < NORM_THREADS / 32; ++w) b += warp_sum[w];
-    partials[first_block + blockIdx.x] = b;
-    __threadfence();
-    last = atomicAdd(ticket, 1u) == (unsigned)(total_blocks - 1);
+  if (warp == 0) {
+    s = warp_total(lane < NORM_THREADS / 32 ? warp_sum[lane] : 0.0f);
+    if (lane == 0) {
+      partials[first_block + blockIdx.x] = s;
+      __threadfence();
+      last = atomicAdd(ticket, 1u) == (unsigned)(total_blocks - 1);
+    }
   }
   __syncthreads();
-  if (!last) return;
+  if (!last || warp != 0) return;
   __threadfence();
-  s = 0.0;
-  for (int b = threadIdx.x; b < total_blocks; b += NORM_THREADS) s += __ldcg(&partials[b]);
+  double total = 0.0;
+  for (int b = lane; b < total_blocks; b += 32) total += (double)__ldcg(&partials[b]);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (lane == 0) warp_sum[warp] = s;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    double b = 0.0;
-    for (int w = 0; w < NORM_THREADS / 32; ++w) b += warp_sum[w];
-    const double norm = sqrt(b);
-    out[0] = (float)norm;
-    out[1] = isfinite(norm) ? (float)fmin(1.0, (double)max_norm / (norm + 1e-6)) : __int_as_float(0x7fffffff);
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  if (lane == 0) {
+    const float norm = (float)sqrt(total);
+    out[0] = norm;
+    out[1] = isfinite(norm) ? fminf(1.0f, max_norm / (norm + 1e-6f)) : __int_as_float(0x7fffffff);
     *ticket = 0u;
   }
 }
@@ -647,7 +650,7 @@ cudaError_t launch_norm(const GradTensor* tensors, int count, int blocks, int fi
   if (fill_table(tab, tensors, count, grad_norm_chunks) < 0) return cudaErrorInvalidValue;
   grad_norm_kernel<CAP><<<blocks, NORM_THREADS, 0, st>>>(
       tab, first_block, total_blocks, max_norm, out, static_cast<unsigned*>(ws),
-      reinterpret_cast<double*>(static_cast<char*>(ws) + NORM_PARTIALS_OFFSET));
+      reinterpret_cast<float*>(static_cast<char*>(ws) + NORM_PARTIALS_OFFSET));
   return cudaGetLastError();
 }
 

@@ -40,10 +40,10 @@ enum StateKind { STATE_F32 = 0, STATE_MX8 = 1 };
 
 // Most tensors of one launch: the table and its chunk starts fit the kernel's parameters (32,764 bytes).
 constexpr int OPTIM_TABLE = 256;
-// grad_norm's workspace: a ticket (zero between calls), then one double per block of the call.
+// grad_norm's workspace: a ticket (zero between calls), then one f32 sum per block of the call.
 constexpr int NORM_MAX_PARTIALS = 4096;
 constexpr int NORM_PARTIALS_OFFSET = 256;
-constexpr int NORM_WS_BYTES = NORM_PARTIALS_OFFSET + NORM_MAX_PARTIALS * 8;
+constexpr int NORM_WS_BYTES = NORM_PARTIALS_OFFSET + NORM_MAX_PARTIALS * 4;
 
 cudaError_t launch_adamw(const AdamTensor* tensors, int count, int param, int grad, int state, const AdamHyper& h,
                          const float* grad_scale, int n_sm, cudaStream_t st);

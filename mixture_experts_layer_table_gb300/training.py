@@ -19,7 +19,7 @@ P, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
 
 ELEM_TYPES = {torch.float32: 0, torch.bfloat16: 1}
 STATE_F32, STATE_MX8 = 0, 1
-GRAD_NORM_WS_BYTES = 33024
+GRAD_NORM_WS_BYTES = 16640
 
 
 class GradTensor(ctypes.Structure):
