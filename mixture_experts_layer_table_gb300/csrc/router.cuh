@@ -24,6 +24,10 @@ struct RouteArgs {
   float dprob_unit;        // dprob[e] = dprob_unit * counts[e]
   float bias_rate;
   int sum_shift;           // probabilities are summed in units of 2^-sum_shift
+  // set by the launcher: rows can be read, scores written, in words of 4 to 16 bytes; tokens whose gates are formed
+  // together; log2 of the next power of two of k; lanes of a segment
+  bool wide, wide_scores;
+  int batch, slot_bits, segment_lanes;
   unsigned* ticket;        // workspace: zero between calls
   unsigned* not_finite;
   unsigned long long* acc_prob;  // [E]
@@ -52,6 +56,9 @@ constexpr int ROUTE_WS_BYTES = ROUTE_WS_COUNTS + 4 * ROUTE_MAX_E;
 
 inline bool route_balances(const RouteArgs& a) { return a.counts || a.prob_sum || a.loss || a.dprob || a.bias_next; }
 
+// Two tokens to a warp, for many tokens (router_pairs.cu); launch_route chooses.
+bool route_pairs_fit(const RouteArgs& a);
+cudaError_t launch_route_pairs(const RouteArgs& a, bool bf16, int n_sm, cudaStream_t st);
 cudaError_t launch_route(const RouteArgs& a, bool bf16, int n_sm, cudaStream_t st);
 cudaError_t launch_route_backward(const RouteBackwardArgs& a, bool bf16, int n_sm, cudaStream_t st);
 

@@ -1,0 +1,595 @@
+// Group-limited expert selection for many tokens: two tokens to a warp, 16 lanes to each.
+//
+// With a warp to a token (router.cu) most of the instructions steer lanes: about 1,150 a token at 256 experts, k
+// rounds of "the best left" among them.  Here a warp's steps serve two tokens, and each token is selected in a few
+// steps (about 300 instructions):
+//   1. a lane holds C consecutive experts (16 C >= E) and finds the two largest of their rank values; lanes of a
+//      segment, a group or an equal part of one, merge theirs;
+//   2. each group's lanes count the groups that are better;
+//   3. the least of the chosen segments' second largest values has at least 2 * topk_group * (segments of a group)
+//      >= k experts at or above it: a bound from below of the k-th largest value.  The experts that reach it (about
+//      11 of 128) are listed in shared memory;
+//   4. a lane to each listed expert counts how many are better: its place;
+//   5. the gates of the tokens of a few such steps are formed together, a lane to each selected expert.
+// A token for which this does not do (more than 32 experts listed, too few unmasked) is selected by the whole warp, one expert at a time, by the definition.
+#include <algorithm>
+#include <cstddef>
+
+#include "router_common.cuh"
+
+namespace mok {
+
+namespace {
+
+constexpr int WARPS = 8;
+constexpr int THREADS = 32 * WARPS;
+constexpr int BLOCKS_OF_SM = 3;  // 72 to 80 registers; 4 (64 registers) were 9% slower, 2 8%
+
+// How rank values are formed.  LOGITS: softmax without a bias, ranked by the logits.  FAST: a biased sigmoid by the
+// hardware's exponential and reciprocal, 4 instructions instead of about 18, with a check that the order is certain.
+enum PairMode { LOGITS = 0, SIGMOID = 1, SIGMOID_FAST = 2 };
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float inverse_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+constexpr float LOG2E = 1.442695041f;
+// 1 / (1 + e^-x), off by less than 4e-7
+__device__ __forceinline__ float sigmoid_fast(float x) { return inverse_fast(1.0f + exp2_fast(x * -LOG2E)); }
+
+
+// One token by the definition, by the whole warp: lane j < k returns the j-th best expert, its score in *score.
+// `row` [E] is overwritten with the rank values.
+template <typename TL>
+__device__ __noinline__ int select_by_warp(const RouteArgs& a, int64_t t, float* row, int lane, float* score) {
+  const TL* from = static_cast<const TL*>(a.logits) + t * a.stride;
+  const bool by_logit = a.router == 0 && a.bias == nullptr;
+  float m = -INFINITY, inv = 1.0f;
+  if (a.router == 0) {
+    for (int e = lane; e < a.E; e += 32) m = fmaxf(m, to_f32(from[e]));
+    m = warp_max(m);
+    if (m == -INFINITY) m = 0.0f;
+    float sum = 0.0f;
+    for (int e = lane; e < a.E; e += 32) sum += expf(to_f32(from[e]) - m);
+    sum = warp_sum(sum);
+    inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  }
+  __syncwarp();
+  for (int e = lane; e < a.E; e += 32) {
+    const float x = to_f32(from[e]), b = a.bias != nullptr ? a.bias[e] : 0.0f;
+    const float r = by_logit ? x : a.router == 0 ? fmaf(expf(x - m), inv, b) : sigmoid(x) + b;
+    row[e] = x > -INFINITY && r > -INFINITY ? r : -INFINITY;
+  }
+  __syncwarp();
+  const int size = a.E / a.n_group;
+  unsigned keep = ALL;
+  if (a.n_group > 1) {
+    float m1 = -INFINITY, m2 = -INFINITY;
+    if (lane < a.n_group)
+      for (int i = 0; i < size; ++i) merge_top2(m1, m2, row[lane * size + i], -INFINITY);
+    if (by_logit && a.group_top2) m1 = m1 > -INFINITY ? expf(m1 - m) : m1, m2 = m2 > -INFINITY ? expf(m2 - m) : m2;
+    const float value = a.group_top2 && m2 > -INFINITY ? m1 + m2 : m1;
+    int better = 0;
+    for (int h = 0; h < a.n_group; ++h) {
+      const float o = __shfl_sync(ALL, value, h);
+      better += h < lane ? o >= value : o > value;
+    }
+    keep = __ballot_sync(ALL, lane < a.n_group && better < a.topk_group);
+  }
+  int my_e = 0;
+  for (int j = 0; j < a.k; ++j) {
+    uint32_t top = 0u;  // 0: nothing left; a taken expert holds NaN
+    int at = a.E;
+    for (int e = lane; e < a.E; e += 32) {
+      const float r = row[e];
+      const uint32_t key = (a.n_group == 1 || (keep >> (e / size)) & 1u) && r == r ? ordered(r) : 0u;
+      if (key > top) top = key, at = e;
+    }
+    const uint32_t best = __reduce_max_sync(ALL, top);
+    const int e = __reduce_min_sync(ALL, top == best ? at : a.E);
+    if (lane == (e & 31)) row[e] = __int_as_float(0x7fffffff);
+    __syncwarp();
+    if (lane == j) my_e = e;
+  }
+  if (lane < a.k) {
+    const float x = to_f32(from[my_e]);
+    *score = a.router == 0 ? expf(x - m) * inv : sigmoid(x);
+  }
+  return my_e;
+}
+
+constexpr int SLOW_TOKENS = 32;
+// A warp's shared memory, but for its rank values and sums.
+struct __align__(16) Scratch {
+  float value[2][36];  // rank values of the two tokens' listed experts, -inf behind them (read four at a time)
+  int expert[2][32];
+  int pick[32];               // selected experts of the tokens of a batch
+  float shift[32], inv[32];   // of the softmax of each
+  int64_t slow[SLOW_TOKENS];  // tokens left over
+};
+static_assert(sizeof(Scratch) % 16 == 0 && offsetof(Scratch, value) == 0, "read in words of 16 bytes");
+
+// Bytes that a lane's C experts are read and written by.
+template <int C, typename T>
+constexpr int unit_of() {
+  constexpr int BYTES = C * (int)sizeof(T);
+  return BYTES % 16 == 0 ? 16 : BYTES % 8 == 0 ? 8 : 4;
+}
+// Floats from one lane's C values to the next lane's in shared memory: 8 lanes' accesses of 16 bytes (16 of 8) then
+// fall on all 32 banks.
+template <int C>
+constexpr int lane_stride() {
+  return C == 8 || C == 16 ? C + 4 : C;
+}
+
+// A lane's experts of a row (-inf beyond E).
+template <int C, typename TL>
+__device__ __forceinline__ void load_part(const TL* row, int first, int E, bool wide, float (&x)[C]) {
+  constexpr int BYTES = C * (int)sizeof(TL), UNIT = unit_of<C, TL>();
+  const bool in = first < E;
+  if (wide) {
+    uint32_t w[BYTES / 4];
+    const TL* from = row + (in ? first : 0);
+#pragma unroll
+    for (int j = 0; j < BYTES / UNIT; ++j) {
+      if constexpr (UNIT == 16) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(from) + j);
+        w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
+      } else if constexpr (UNIT == 8) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(from) + j);
+        w[2 * j] = v.x, w[2 * j + 1] = v.y;
+      } else {
+        w[j] = __ldg(reinterpret_cast<const uint32_t*>(from) + j);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < BYTES / 4; ++j) {
+      if constexpr (sizeof(TL) == 4) x[j] = __uint_as_float(w[j]);
+      else x[2 * j] = __uint_as_float(w[j] << 16), x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+  } else if (in) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) x[c] = to_f32(row[first + c]);
+  }
+  if (!in) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) x[c] = -INFINITY;
+  }
+}
+
+// A lane's C values in shared (or 16-byte aligned global) memory.
+template <int C>
+__device__ __forceinline__ void put(float* to, const float (&v)[C]) {
+  if constexpr (C % 4 == 0) {
+#pragma unroll
+    for (int c = 0; c < C; c += 4) *reinterpret_cast<float4*>(to + c) = make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]);
+  } else {
+#pragma unroll
+    for (int c = 0; c < C; c += 2) *reinterpret_cast<float2*>(to + c) = make_float2(v[c], v[c + 1]);
+  }
+}
+template <int C>
+__device__ __forceinline__ void get(const float* from, float (&v)[C]) {
+  if constexpr (C % 4 == 0) {
+#pragma unroll
+    for (int c = 0; c < C; c += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(from + c);
+      v[c] = f.x, v[c + 1] = f.y, v[c + 2] = f.z, v[c + 3] = f.w;
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < C; c += 2) {
+      const float2 f = *reinterpret_cast<const float2*>(from + c);
+      v[c] = f.x, v[c + 1] = f.y;
+    }
+  }
+}
+
+// The two largest of N values.
+template <int N>
+__device__ __forceinline__ void two_largest(const float (&v)[N], float& first, float& second) {
+  first = fmaxf(v[0], v[1]), second = fminf(v[0], v[1]);
+#pragma unroll
+  for (int c = 2; c < N; c += 2) {
+    const float hi = fmaxf(v[c], v[c + 1]), lo = fminf(v[c], v[c + 1]);
+    second = fmaxf(fmaxf(fminf(first, hi), second), lo), first = fmaxf(first, hi);
+  }
+}
+
+// over the 16 lanes of a token
+__device__ __forceinline__ float half_max(float x) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(ALL, x, o));
+  return x;
+}
+__device__ __forceinline__ float half_min(float x) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) x = fminf(x, __shfl_xor_sync(ALL, x, o));
+  return x;
+}
+__device__ __forceinline__ float half_sum(float x) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(ALL, x, o);
+  return x;
+}
+
+// Writes the selected expert e of token t (`on`: this lane has one) and its gate, as the layer's ungrouped top-k
+// forms it: the sum over the token's lanes, from `first` on, in the order of the selection (a lane without an expert
+// adds 0).
+template <typename TL, int MODE>
+__device__ __forceinline__ void store_selected(const RouteArgs& a, int64_t t, bool on, int j_of, int first, int e,
+                                               float shift, float inv, int* counts) {
+  float sel = 0.0f;
+  if (on) {
+    const float xe = to_f32(static_cast<const TL*>(a.logits)[t * a.stride + e]);
+    sel = MODE == LOGITS ? expf(xe - shift) * inv : sigmoid(xe);
+  }
+  float sum = 0.0f;
+  if (a.renorm) {
+    if (a.slot_bits <= 3) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum += j >> a.slot_bits ? 0.0f : __shfl_sync(ALL, sel, first + j);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) sum += __shfl_sync(ALL, sel, first + j);
+    }
+  }
+  if (on) {
+    a.topk_idx[t * a.k + j_of] = e;
+    if (a.gates != nullptr)
+      a.gates[t * a.k + j_of] = (!a.renorm ? sel : sum == 0.0f ? 0.0f : sel * (1.0f / sum)) * a.scale;
+    if (counts != nullptr) atomicAdd(&counts[e], 1);
+  }
+}
+
+// How a block's tokens are cut up.
+struct PairShape {
+  int lanes, group;    // lanes of a group; this lane's
+  bool part_in;        // this lane has experts
+  bool choose, top2;
+};
+
+// The selection of a warp's two tokens from their lanes' rank values r (shift: of each softmax): the places of the
+// experts in pick.  Returns (on all 16 lanes of a token): 0 done; 1 not certain, with approximate values (FAST: off by
+// less than margin / 2); 2 more than the list holds, or too few experts.
+template <int C, bool LOGIT_VALUES, bool FAST>
+__device__ __forceinline__ int select_pair(const RouteArgs& a, const PairShape& p, const float (&r)[C], float shift,
+                                           float margin, int lane, float* mine, Scratch& w, int* pick) {
+  const int half = lane >> 4, part = lane & 15;
+  put(mine, r);
+  // 1. the two largest of the lane, of its segment and of its group
+  float m1, m2;
+  two_largest(r, m1, m2);
+  float low = m2;  // the segment's second largest
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) {
+    if (o < p.lanes) {
+      merge_top2(m1, m2, __shfl_xor_sync(ALL, m1, o), __shfl_xor_sync(ALL, m2, o));
+      if (o < a.segment_lanes) low = m2;
+    }
+  }
+  // 2. the groups
+  bool in_play = p.part_in, unsure = false;
+  if (p.choose) {
+    float value = m1;
+    if (p.top2) {
+      if (LOGIT_VALUES) value = m1 > -INFINITY ? expf(m1 - shift) + expf(m2 - shift) : m1;
+      else value = m2 > -INFINITY ? m1 + m2 : m1;
+    }
+    const float reach = FAST ? value - fmaf(1e-6f, fabsf(value), 2e-6f) : 0.0f;
+    int better = 0, near = 0;
+#pragma unroll 4
+    for (int h = 0; h < a.n_group; ++h) {
+      const float o = __shfl_sync(ALL, value, (lane & 16) + h * p.lanes);
+      if (FAST) {
+        better += o > value;
+        near += o > reach;  // itself among them
+      } else {
+        better += h < p.group ? o >= value : o > value;
+      }
+    }
+    in_play = p.part_in && better < a.topk_group;
+    if (FAST) unsure = in_play && near > better + 1;
+  }
+  // 3. the listed experts, in their order
+  float bound = half_min(in_play ? low : INFINITY);
+  const bool none = !(bound > -INFINITY);
+  bound = in_play ? bound - margin : INFINITY;
+  unsigned listed = 0u;
+#pragma unroll
+  for (int c = 0; c < C; ++c) listed |= r[c] >= bound ? 1u << c : 0u;
+  const int own = __popc(listed);
+  int before = own;
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) {
+    const int v = __shfl_up_sync(ALL, before, o, 16);
+    if (part >= o) before += v;
+  }
+  int n = __shfl_sync(ALL, before, lane | 15);
+  const bool out = none || n > 32;  // the same on the token's lanes
+  if (out) n = 0, listed = 0u;
+  before -= own;
+  while (listed != 0u) {
+    const int c = __ffs(listed) - 1;
+    listed &= listed - 1u;
+    w.value[half][before] = mine[c];
+    w.expert[half][before++] = part * C + c;
+  }
+  if (part >= n) w.value[half][part] = -INFINITY;
+  if (part + 16 >= n) w.value[half][part + 16] = -INFINITY;
+  __syncwarp();
+  // 4. their places
+  const int longest = max(n, __shfl_xor_sync(ALL, n, 16));
+  for (int at = part; at - part < longest; at += 16) {
+    const float v = w.value[half][at];
+    const float reach = v - margin;
+    int better = 0, near = 0;
+    for (int j = 0; j < longest; j += 4) {
+      const float4 o = *reinterpret_cast<const float4*>(&w.value[half][j]);
+      if (FAST) {
+        better += o.x > v, near += o.x > reach;
+        better += o.y > v, near += o.y > reach;
+        better += o.z > v, near += o.z > reach;
+        better += o.w > v, near += o.w > reach;
+      } else {  // ties to the expert before
+        better += at > j ? o.x >= v : o.x > v;
+        better += at > j + 1 ? o.y >= v : o.y > v;
+        better += at > j + 2 ? o.z >= v : o.z > v;
+        better += at > j + 3 ? o.w >= v : o.w > v;
+      }
+    }
+    if (at < n && better < a.k) {
+      // one of the best k must not have another (itself apart) within the margin below it
+      if (FAST && near > better + 1) unsure = true;
+      pick[better] = w.expert[half][at];
+    }
+  }
+  const unsigned doubts = FAST ? __ballot_sync(ALL, unsure) : 0u;
+  return out ? 2 : (doubts >> (16 * half)) & 0xffffu ? 1 : 0;
+}
+
+template <int C, typename TL, int MODE>
+__global__ void __launch_bounds__(THREADS, BLOCKS_OF_SM) route_pairs_kernel(const RouteArgs a) {
+  // [16] lanes' bias, [WARPS][32] lanes' rank values; balance: [16 C] counts, [2 WARPS][16] lanes' sums
+  extern __shared__ __align__(16) float sh[];
+  constexpr int S = lane_stride<C>();
+  __shared__ Scratch scratch[WARPS];
+  constexpr bool FAST = MODE == SIGMOID_FAST;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = lane >> 4, part = lane & 15;
+  const int E = a.E, k = a.k;
+  const bool balance = a.ticket != nullptr;
+  float* rows = sh + 16 * S;
+  int* counts = balance ? reinterpret_cast<int*>(rows + WARPS * 32 * S) : nullptr;
+  float* sums = rows + WARPS * 32 * S + 16 * C;
+  Scratch& w = scratch[warp];
+  float* mine = rows + (warp * 32 + lane) * S;
+  float* my_sums = sums + (warp * 32 + lane) * S;
+  const float* bias = sh + part * S;
+  float margin = 0.0f;
+  for (int e = threadIdx.x; e < 16 * C; e += THREADS)
+    sh[e / C * S + e % C] = e >= E ? -INFINITY : a.bias != nullptr ? a.bias[e] : 0.0f;
+  if (balance) {
+    for (int e = threadIdx.x; e < 16 * C; e += THREADS) counts[e] = 0;
+#pragma unroll
+    for (int c = 0; c < C; ++c) my_sums[c] = 0.0f;
+  }
+  if (lane < 8) w.value[lane >> 2][32 + (lane & 3)] = -INFINITY;
+  __syncthreads();
+  // Approximate rank values s + b are off by less than 4e-7 + 2^-23 |s + b|: their order is certain from twice that on.
+  if (FAST) {
+    if (part * C < E) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) margin = fmaxf(margin, fabsf(bias[c]));
+    }
+    margin = fmaf(5e-7f, 1.0f + warp_max(margin), 1e-6f);
+  }
+  const bool part_in = part * C < E;
+  const int lanes = a.n_group > 1 ? E / a.n_group / C : 16;
+  const PairShape shape = {lanes, part / lanes, part_in, a.topk_group < a.n_group, a.group_top2 != 0};
+  const int slot = lane >> a.slot_bits, j_of = lane & ((1 << a.slot_bits) - 1);
+  const int64_t step = (int64_t)gridDim.x * WARPS * a.batch;
+  int64_t base = ((int64_t)blockIdx.x * WARPS + warp) * a.batch;
+  const TL* logits = static_cast<const TL*>(a.logits);
+
+  while (base < a.T) {
+    int slow_count = 0;
+    for (; base < a.T && slow_count + a.batch <= SLOW_TOKENS; base += step) {
+      const int count = (int)min((int64_t)a.batch, a.T - base);
+      unsigned passed = 0u;  // tokens of the batch that are left over
+      for (int i = 0; i < count; i += 2) {
+        const bool on = i + half < count;
+        const int64_t t = base + (on ? i + half : i);
+        float x[C], s[C], r[C];
+        load_part<C>(logits + t * a.stride, part * C, E, a.wide, x);
+        float inv = 1.0f, shift = 0.0f, least = INFINITY;
+#pragma unroll
+        for (int c = 0; c < C; ++c) least = fminf(least, x[c]);
+        if constexpr (MODE == LOGITS) {
+          shift = -INFINITY;
+          float sum = 0.0f;
+#pragma unroll
+          for (int c = 0; c < C; ++c) shift = fmaxf(shift, x[c]);
+          shift = half_max(shift);
+          if (shift == -INFINITY) shift = 0.0f;
+          const float offset = -shift * LOG2E;
+#pragma unroll
+          for (int c = 0; c < C; ++c) {
+            s[c] = exp2_fast(fmaf(x[c], LOG2E, offset));
+            sum += s[c];
+            r[c] = x[c];
+          }
+          sum = half_sum(sum);
+          inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+          if (part == 0) w.shift[i + half] = shift, w.inv[i + half] = inv;
+        } else {
+          get(bias, r);
+#pragma unroll
+          for (int c = 0; c < C; ++c) {
+            s[c] = FAST ? sigmoid_fast(x[c]) : sigmoid(x[c]);
+            r[c] += s[c];
+          }
+        }
+        const bool masked = MODE != LOGITS && __any_sync(ALL, part_in && least == -INFINITY);
+        if (masked) {
+#pragma unroll
+          for (int c = 0; c < C; ++c) r[c] = x[c] == -INFINITY ? -INFINITY : r[c];
+        }
+        int* pick = w.pick + ((i + half) << a.slot_bits);
+        int result = select_pair<C, MODE == LOGITS, FAST>(a, shape, r, shift, margin, lane, mine, w, pick);
+        if (FAST && __any_sync(ALL, result == 1)) {  // not certain: again, with the exact scores
+          __syncwarp();
+          get(bias, r);
+#pragma unroll
+          for (int c = 0; c < C; ++c) r[c] = x[c] == -INFINITY ? -INFINITY : r[c] + sigmoid(x[c]);
+          result = select_pair<C, false, false>(a, shape, r, 0.0f, 0.0f, lane, mine, w, pick);
+        }
+        const unsigned skips = __ballot_sync(ALL, result == 2 && on);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if ((skips >> (16 * h)) & 0xffffu) {
+            passed |= 1u << (i + h);
+            if (lane == 0) w.slow[slow_count] = base + i + h;
+            ++slow_count;
+          }
+        }
+        if (a.scores != nullptr && on && part_in) {
+          float* to = a.scores + t * E + part * C;
+#pragma unroll
+          for (int c = 0; c < C; ++c) r[c] = s[c] * inv;
+          if (a.wide_scores) {
+            put(to, r);
+          } else {
+#pragma unroll
+            for (int c = 0; c < C; ++c) to[c] = r[c];
+          }
+        }
+        if (balance) {
+          float q = inv;
+          if (MODE != LOGITS) {
+            float total = 0.0f;
+#pragma unroll
+            for (int c = 0; c < C; ++c) total += s[c];  // 0 beyond E
+            total = half_sum(total);
+            q = total == 0.0f ? 0.0f : 1.0f / total;
+          }
+          if (on) {
+            float sum[C];
+            get(my_sums, sum);
+#pragma unroll
+            for (int c = 0; c < C; ++c) sum[c] = fmaf(s[c], q, sum[c]);
+            put(my_sums, sum);
+          }
+        }
+        __syncwarp();  // the lists are free again, the picks can be read
+      }
+      // 5.
+      const bool on = slot < count && j_of < k && !((passed >> slot) & 1u);
+      store_selected<TL, MODE>(a, base + slot, on, j_of, slot << a.slot_bits, on ? w.pick[lane] : 0,
+                               MODE == LOGITS && on ? w.shift[slot] : 0.0f, MODE == LOGITS && on ? w.inv[slot] : 1.0f,
+                               counts);
+      __syncwarp();  // the picks are free again
+    }
+    // the tokens left over, in a loop of their own: no call stands in the loop over the others
+    for (int i = 0; i < slow_count; ++i) {
+      const int64_t t = w.slow[i];
+      float score = 0.0f;
+      const int e = select_by_warp<TL>(a, t, rows + warp * 32 * S, lane, &score);
+      float sum = 0.0f;
+      for (int j = 0; j < k; ++j) sum += __shfl_sync(ALL, score, j);
+      if (lane < k) {
+        a.topk_idx[t * k + lane] = e;
+        if (a.gates != nullptr)
+          a.gates[t * k + lane] = (!a.renorm ? score : sum == 0.0f ? 0.0f : score * (1.0f / sum)) * a.scale;
+        if (balance) atomicAdd(&counts[e], 1);
+      }
+    }
+    __syncwarp();
+  }
+  if (balance) {
+    __syncthreads();
+    finish_balance(a, counts, [&](int e) {
+      float p = 0.0f;
+#pragma unroll
+      for (int h = 0; h < 2 * WARPS; ++h) p += sums[h * 16 * S + e / C * S + e % C];
+      return p;
+    });
+  }
+}
+
+// Experts of a lane for which there is a kernel; 0: none.
+int lane_experts(const RouteArgs& a) {
+  const int c = (a.E + 15) / 16;
+  const int C = c <= 4 ? 4 : c <= 8 ? 8 : c <= 10 ? 10 : c <= 16 ? 16 : 0;
+  if (C == 0 || a.E % C != 0 || (a.router == 0 && a.bias != nullptr)) return 0;
+  if (a.n_group == 1) return a.E / C * 2 >= a.k ? C : 0;
+  const int size = a.E / a.n_group, lanes = size / C;
+  if (size % C != 0 || (lanes & (lanes - 1)) != 0) return 0;
+  return 2 * a.topk_group * lanes >= a.k ? C : 0;
+}
+
+template <int C, typename TL, int MODE>
+cudaError_t launch_pairs(const RouteArgs& args, int n_sm, cudaStream_t st) {
+  RouteArgs a = args;
+  constexpr int UNIT = unit_of<C, TL>(), S = lane_stride<C>();
+  a.wide = reinterpret_cast<uintptr_t>(a.logits) % UNIT == 0 && a.stride * (int64_t)sizeof(TL) % UNIT == 0;
+  constexpr int SCORES_UNIT = C % 4 == 0 ? 16 : 8;
+  a.wide_scores = reinterpret_cast<uintptr_t>(a.scores) % SCORES_UNIT == 0 && a.E * 4 % SCORES_UNIT == 0;
+  a.slot_bits = 0;
+  while ((1 << a.slot_bits) < a.k) ++a.slot_bits;
+  // the longest segments of which topk_group groups have k / 2
+  const int lanes = a.n_group > 1 ? a.E / a.n_group / C : 16;
+  a.segment_lanes = 1;
+  const int in_group = a.n_group > 1 ? lanes : a.E / C;
+  while (2 * a.segment_lanes <= in_group && in_group % (2 * a.segment_lanes) == 0 &&
+         2 * a.topk_group * (in_group / (2 * a.segment_lanes)) >= a.k)
+    a.segment_lanes *= 2;
+  // tokens whose gates are formed together: as many as fill a warp, once every resident warp has a batch
+  a.batch = 32 >> a.slot_bits;
+  while (a.batch > 2 && a.T < (int64_t)a.batch * WARPS * BLOCKS_OF_SM * n_sm) a.batch >>= 1;
+  const bool balance = a.ticket != nullptr;
+  const int smem = (16 * S + WARPS * 32 * S + (balance ? 16 * C + WARPS * 32 * S : 0)) * 4;
+  auto kernel = route_pairs_kernel<C, TL, MODE>;
+  if (smem > 32 * 1024) {
+    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err != cudaSuccess) return err;
+  }
+  const int64_t want = (a.T + (int64_t)WARPS * a.batch - 1) / ((int64_t)WARPS * a.batch);
+  const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>(want, BLOCKS_OF_SM * n_sm));
+  kernel<<<blocks, THREADS, smem, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <int C, typename TL>
+cudaError_t launch_mode(const RouteArgs& a, int n_sm, cudaStream_t st) {
+  if (a.router == 0) return launch_pairs<C, TL, LOGITS>(a, n_sm, st);
+  // without a bias ties are common (equal logits), and the scores that are handed out are the exact ones
+  if (a.bias != nullptr && a.scores == nullptr) return launch_pairs<C, TL, SIGMOID_FAST>(a, n_sm, st);
+  return launch_pairs<C, TL, SIGMOID>(a, n_sm, st);
+}
+
+template <typename TL>
+cudaError_t launch_type(const RouteArgs& a, int n_sm, cudaStream_t st) {
+  switch (lane_experts(a)) {
+    case 4: return launch_mode<4, TL>(a, n_sm, st);
+    case 8: return launch_mode<8, TL>(a, n_sm, st);
+    case 10: return launch_mode<10, TL>(a, n_sm, st);
+    case 16: return launch_mode<16, TL>(a, n_sm, st);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace
+
+bool route_pairs_fit(const RouteArgs& a) { return lane_experts(a) != 0; }
+
+cudaError_t launch_route_pairs(const RouteArgs& a, bool bf16, int n_sm, cudaStream_t st) {
+  return bf16 ? launch_type<__nv_bfloat16>(a, n_sm, st) : launch_type<float>(a, n_sm, st);
+}
+
+}  // namespace mok

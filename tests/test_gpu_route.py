@@ -105,6 +105,90 @@ def test_sum_of_two_ties_on_equal_rows():
     assert out["topk_idx"].cpu().tolist() == [[0, 1, 2, 3, 4, 5]] * 4
 
 
+# shapes that many tokens are routed with two to a warp (4, 8, 10 and 16 experts to a lane, groups of one to 16
+# lanes, groups in segments, all groups in play), and ones that are not (a group of part of a lane, 512 experts)
+MANY = [(64, 6, 8, 3, MAX), (64, 6, 1, 1, MAX), (60, 5, 1, 1, TOP2), (96, 8, 3, 1, TOP2), (128, 8, 4, 2, TOP2),
+        (128, 16, 4, 2, MAX), (160, 6, 8, 3, MAX), (160, 3, 8, 8, TOP2), (256, 8, 8, 4, TOP2), (256, 1, 16, 2, MAX),
+        (256, 12, 4, 3, TOP2), (240, 7, 15, 5, TOP2), (252, 9, 9, 4, TOP2), (512, 8, 8, 4, TOP2), (16, 4, 4, 2, TOP2)]
+
+
+@pytest.mark.parametrize("shape", MANY, ids=lambda s: "E%d_k%d_G%d_kg%d_s%d" % s)
+@pytest.mark.parametrize("router,with_bias", [(SIGMOID, True), (SIGMOID, False), (SOFTMAX, False), (SOFTMAX, True)])
+def test_route_many_tokens(shape, router, with_bias):
+    """40 tokens, over and over to 2,500 and then 5,001 of them: every copy is routed as the oracle's."""
+    E, k, G, kg, score = shape
+    bias = _bias(E, 15, with_bias)
+    x, x64 = _logits(40, E, 17, torch.bfloat16 if k % 2 else torch.float32, router, bias, k, G, kg, score)
+    idx, _ = O.select(x64, bias, router, k, G, kg, score)
+    s = O.scores(x64, router)
+    gates = O.gates(s, idx, True, 2.5)
+    for T in (2500, 5001):
+        of = np.arange(T) % 40
+        desc = mok.make_route_desc(T, E, k, router, True, route_scale=2.5, n_group=G, topk_group=kg, group_score=score,
+                                   balance_coef=0.3, bias_rate=0.01)
+        rows = x[torch.tensor(of).cuda()]
+        plain = mok.Router(desc, dtype=x.dtype).forward(rows, _cuda(bias))
+        full = mok.Router(desc, dtype=x.dtype, balance=True, scores=True).forward(rows, _cuda(bias))
+        counts, prob_sum, loss, dprob, _ = O.balance(s[of], idx[of], 0.3, bias, 0.01)
+        for out in (plain, full):
+            assert np.array_equal(out["topk_idx"].cpu().numpy(), idx[of])
+            assert np.allclose(f64(out["gates"]), gates[of], rtol=REL, atol=0)
+        assert np.allclose(f64(full["scores"]), s[of], rtol=REL, atol=0)
+        assert np.array_equal(full["counts"].cpu().numpy(), counts)
+        assert np.allclose(f64(full["prob_sum"]), prob_sum, rtol=REL, atol=0)
+        assert np.allclose(f64(full["loss"]), [loss], rtol=REL, atol=0)
+        # rows of a wider tensor, not aligned
+        wide = torch.zeros((T, E + 3), dtype=x.dtype, device="cuda")
+        wide[:, 1:E + 1] = rows
+        again = mok.Router(desc, dtype=x.dtype, balance=True).forward(wide[:, 1:E + 1], _cuda(bias))
+        assert torch.equal(again["topk_idx"], plain["topk_idx"]) and torch.equal(again["counts"], full["counts"])
+
+
+@pytest.mark.parametrize("E,k,G,kg,score", [(256, 8, 8, 4, MAX), (64, 6, 1, 1, MAX), (160, 6, 8, 3, MAX)])
+@pytest.mark.parametrize("router", [SIGMOID, SOFTMAX])
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_many_tokens_with_ties_masks_and_near_values(E, k, G, kg, score, router, with_bias):
+    """Exact ties (also of logit and bias together), rows of one value, masked experts and groups, rows with too few
+    experts left and with none, values one f32 step apart: the definition's order in f32 (no oracle margin is asked:
+    the rank values here are the same in f32 and f64, or equal in f32 by construction)."""
+    T = 3000
+    rng = np.random.default_rng(5)
+    x = rng.integers(-4, 5, (T, E)) * 0.25
+    x[:3] = [[0.0], [-1.0], [2.0]]
+    x[10:700][rng.random((690, E)) < 0.2] = -np.inf
+    x[700:900, :E // 2] = -np.inf
+    x[900:950] = np.where(np.isin(np.arange(E), (3, E - 2)), x[900:950], -np.inf)
+    x[950:1000] = -np.inf
+    bias = np.zeros(E, np.float32) if with_bias else None
+    if with_bias and router == SOFTMAX:
+        pytest.skip("the softmax's sum rounds a biased rank value")
+    out = mok.Router(mok.make_route_desc(T, E, k, router, True, n_group=G, topk_group=kg, group_score=score)).forward(
+        torch.tensor(x).float().cuda(), _cuda(bias))
+    got = out["topk_idx"].cpu().numpy()
+    want, _ = O.select(x, bias, router, k, G, kg, score)
+    assert np.array_equal(got, want)
+    s = O.scores(x, router)
+    assert np.allclose(f64(out["gates"]), O.gates(s, got, True, 1.0), rtol=REL, atol=0)
+
+
+def test_selection_is_that_of_the_f32_scores_however_near():
+    """Rank values a few f32 steps apart, with a bias (the many-token kernel forms approximate scores first): the
+    order is that of s + b in f32, s = 1 / (1 + e^-x) by steps rounded to f32."""
+    T, E, k = 4096, 256, 8
+    g = torch.Generator(device="cuda").manual_seed(0)
+    x = (torch.randn(T, E, generator=g, device="cuda") * 1e-6 + torch.randn(T, 1, generator=g, device="cuda"))
+    bias = torch.randint(-4, 5, (E,), generator=g, device="cuda").float() * 2.0 ** -23
+    out = mok.Router(mok.make_route_desc(T, E, k, SIGMOID, True, n_group=8, topk_group=4)).forward(x, bias)
+    r = 1.0 / (1.0 + torch.exp(-x)) + bias
+    best = r.view(T, 8, 32).sort(dim=2, descending=True, stable=True).values
+    chosen = (best[:, :, 0] + best[:, :, 1]).sort(dim=1, descending=True, stable=True).indices[:, :4]
+    keep = torch.zeros((T, 8), dtype=torch.bool, device="cuda").scatter_(1, chosen, True).repeat_interleave(32, 1)
+    want = torch.where(keep, r, -float("inf")).sort(dim=1, descending=True, stable=True).indices[:, :k]
+    assert torch.equal(out["topk_idx"].long(), want)
+    one = mok.Router(mok.make_route_desc(100, E, k, SIGMOID, True, n_group=8, topk_group=4)).forward(x[:100], bias)
+    assert torch.equal(one["topk_idx"], out["topk_idx"][:100])
+
+
 @pytest.mark.parametrize("G,kg,score", [(1, 1, MAX), (8, 3, TOP2), (8, 3, MAX), (5, 2, TOP2)])
 @pytest.mark.parametrize("router", [SIGMOID, SOFTMAX])
 @pytest.mark.parametrize("with_bias", [False, True])
