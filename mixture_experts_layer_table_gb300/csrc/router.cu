@@ -215,6 +215,13 @@ __global__ void __launch_bounds__(THREADS) route_kernel(const RouteArgs a) {
 //   sigmoid: dl = (ds + (dprob - sum_e q dprob) / sum_e s) s (1 - s), q = s / sum_e s
 //   softmax: dl = p (D - sum_e p D), D = ds + dprob
 // The dense row is stored first; then lane j stores the entry of the j-th selected expert over it.
+// sigmoid's value and derivative, both without cancellation
+__device__ __forceinline__ void sigmoid_and_slope(float x, float& s, float& slope) {  // s may be x itself
+  const float e = expf(-fabsf(x)), f = 1.0f / (1.0f + e);
+  s = x >= 0.0f ? f : e * f;
+  slope = e * f * f;
+}
+
 template <int C, typename TL>
 __global__ void __launch_bounds__(THREADS) route_backward_kernel(const RouteBackwardArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -244,15 +251,15 @@ __global__ void __launch_bounds__(THREADS) route_backward_kernel(const RouteBack
         dj = a.dprob != nullptr ? a.dprob[e] : 0.0f;
       }
     }
-    float sj, inv = 1.0f;
+    float sj, slope_j = 0.0f, slope[C], inv = 1.0f;
     if (a.router == 0) {
       float m;
       inv = softmax_row<C>(s, &m);
       sj = e >= 0 ? expf(xj - m) * inv : 0.0f;
     } else {
 #pragma unroll
-      for (int c = 0; c < C; ++c) s[c] = lane * C + c < E ? sigmoid(s[c]) : 0.0f;
-      sj = e >= 0 ? sigmoid(xj) : 0.0f;
+      for (int c = 0; c < C; ++c) sigmoid_and_slope(s[c], s[c], slope[c]);
+      sigmoid_and_slope(xj, sj, slope_j);
     }
     float ds = e >= 0 ? a.scale * dg : 0.0f;
     if (a.renorm) {
@@ -289,11 +296,205 @@ __global__ void __launch_bounds__(THREADS) route_backward_kernel(const RouteBack
       }
 #pragma unroll
       for (int c = 0; c < C; ++c)
-        if (lane * C + c < E) from_f32((d[c] - dot) * inv * s[c] * (1.0f - s[c]), out + lane * C + c);
+        if (lane * C + c < E) from_f32((d[c] - dot) * inv * slope[c], out + lane * C + c);
       __syncwarp();
-      if (e >= 0) from_f32((ds + (dj - dot) * inv) * sj * (1.0f - sj), out + e);
+      if (e >= 0) from_f32((ds + (dj - dot) * inv) * slope_j, out + e);
     }
   }
+}
+
+// The same for up to 256 experts, in words of 4: 8 lanes to a token, 4 tokens to a warp, lane p the words p, p + 8, ...
+// of the row, so that a warp's accesses are whole 128-byte (bf16: 64-byte) pieces of 4 rows, the sums over a token
+// take 3 exchanges for 4 tokens at once, and the lanes that hold the selected experts are all in use (k = 8).
+// Q: words of a lane; rows that are not aligned are read and written one expert at a time.  DENSE: the row's scores are needed (softmax, or dprob); without it the row is zero but for the
+// selected experts, whose logits alone are read.
+__device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+  return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                     __uint_as_float(v.y & 0xffff0000u));
+}
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+// The same by the hardware's exponential and reciprocal (off by 2^-22 and by 2^-24 |x|): 8 instructions instead of 22
+// for the entries that only the balance term reaches.
+__device__ __forceinline__ void sigmoid_and_slope_fast(float x, float& s, float& slope) {
+  float e, f;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fabsf(x) * -1.442695041f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(1.0f + e));
+  s = x >= 0.0f ? f : e * f;
+  slope = e * f * f;
+}
+
+// Experts e .. e + 3 of a row, -inf beyond E.
+template <typename TL>
+__device__ __forceinline__ float4 load_word(const TL* row, int e, int E, bool wide) {
+  if (wide && e < E) return load4(row + e);
+  return make_float4(e < E ? to_f32(row[e]) : -INFINITY, e + 1 < E ? to_f32(row[e + 1]) : -INFINITY,
+                     e + 2 < E ? to_f32(row[e + 2]) : -INFINITY, e + 3 < E ? to_f32(row[e + 3]) : -INFINITY);
+}
+template <typename TL>
+__device__ __forceinline__ void store_word(TL* row, int e, int E, bool wide, float4 v) {
+  if (wide) {
+    if (e < E) store4(row + e, v);
+  } else {
+    if (e < E) from_f32(v.x, row + e);
+    if (e + 1 < E) from_f32(v.y, row + e + 1);
+    if (e + 2 < E) from_f32(v.z, row + e + 2);
+    if (e + 3 < E) from_f32(v.w, row + e + 3);
+  }
+}
+__device__ __forceinline__ float sum_of_8(float x) {
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) x += __shfl_xor_sync(ALL, x, o);
+  return x;
+}
+template <int Q, typename TL, int ROUTER, bool DENSE>
+__global__ void __launch_bounds__(THREADS) route_backward_words_kernel(const RouteBackwardArgs a) {
+  __shared__ float4 d[Q * 8];
+  const int lane = threadIdx.x & 31, row = lane >> 3, part = lane & 7;
+  const int E = a.E, k = a.k;
+  if (DENSE) {
+    for (int e = threadIdx.x; e < Q * 32; e += THREADS)
+      reinterpret_cast<float*>(d)[e] = a.dprob != nullptr && e < E ? a.dprob[e] : 0.0f;
+    __syncthreads();
+  }
+  const int64_t step = (int64_t)gridDim.x * WARPS * 4;
+  for (int64_t base = ((int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5)) * 4; base < a.T; base += step) {
+    const bool on = base + row < a.T;
+    const int64_t t = on ? base + row : a.T - 1;
+    const TL* from = static_cast<const TL*>(a.logits) + t * a.stride;
+    TL* out = static_cast<TL*>(a.dlogits) + t * a.out_stride;
+    float4 s[Q];
+    if (DENSE) {
+#pragma unroll
+      for (int i = 0; i < Q; ++i) s[i] = load_word(from, 4 * (part + 8 * i), E, a.wide);
+    }
+    // the selected experts: one to a lane, a second one where k > 8
+    int e[2] = {-1, -1};
+    float x[2], dg[2] = {0.0f, 0.0f}, dj[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int j = part + 8 * h;
+      x[h] = -INFINITY;
+      if (j < k && a.dgates != nullptr) {
+        e[h] = a.topk_idx[t * k + j];
+        if (e[h] < 0 || e[h] >= E) {
+          report_status(a.status, MOK_DEV_INVALID_ROUTING, SITE_TOPK_INDEX);
+          e[h] = -1;
+        } else {
+          x[h] = to_f32(from[e[h]]);
+          dg[h] = a.dgates[t * k + j];
+          if (DENSE) dj[h] = reinterpret_cast<const float*>(d)[e[h]];
+        }
+      }
+    }
+    float shift = 0.0f, inv = 0.0f, sj[2], slope[2];
+    if (ROUTER == 0) {
+      shift = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < Q; ++i) shift = fmaxf(fmaxf(shift, fmaxf(s[i].x, s[i].y)), fmaxf(s[i].z, s[i].w));
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) shift = fmaxf(shift, __shfl_xor_sync(ALL, shift, o));
+      if (shift == -INFINITY) shift = 0.0f;
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < Q; ++i) {
+        s[i] = make_float4(expf(s[i].x - shift), expf(s[i].y - shift), expf(s[i].z - shift), expf(s[i].w - shift));
+        sum += (s[i].x + s[i].y) + (s[i].z + s[i].w);
+      }
+      sum = sum_of_8(sum);
+      inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) sj[h] = e[h] >= 0 ? expf(x[h] - shift) * inv : 0.0f;
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        sigmoid_and_slope(x[h], sj[h], slope[h]);
+        if (e[h] < 0) sj[h] = slope[h] = 0.0f;
+      }
+    }
+    float ds[2] = {a.scale * dg[0], a.scale * dg[1]};
+    if (a.renorm) {
+      const float S = sum_of_8(sj[0] + sj[1]), dot = sum_of_8(fmaf(dg[0], sj[0], dg[1] * sj[1]));
+      const float inv_s = S == 0.0f ? 0.0f : 1.0f / S;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) ds[h] = e[h] >= 0 ? a.scale * (dg[h] - dot * inv_s) * inv_s : 0.0f;
+    }
+    float dot = 0.0f;
+    if (ROUTER == 0) {
+#pragma unroll
+      for (int i = 0; i < Q; ++i) {
+        const float4 di = d[part + 8 * i];
+        s[i].x *= inv, s[i].y *= inv, s[i].z *= inv, s[i].w *= inv;
+        dot = fmaf(s[i].x, di.x, fmaf(s[i].y, di.y, fmaf(s[i].z, di.z, fmaf(s[i].w, di.w, dot))));
+      }
+      dot = sum_of_8(fmaf(sj[0], ds[0], fmaf(sj[1], ds[1], dot)));
+    } else if (DENSE) {
+      float total = 0.0f;
+#pragma unroll
+      for (int i = 0; i < Q; ++i) {  // the slopes in place of the logits
+        const float4 di = d[part + 8 * i];
+        float4 v;
+        sigmoid_and_slope_fast(s[i].x, v.x, s[i].x);
+        sigmoid_and_slope_fast(s[i].y, v.y, s[i].y);
+        sigmoid_and_slope_fast(s[i].z, v.z, s[i].z);
+        sigmoid_and_slope_fast(s[i].w, v.w, s[i].w);
+        total += (v.x + v.y) + (v.z + v.w);
+        dot = fmaf(v.x, di.x, fmaf(v.y, di.y, fmaf(v.z, di.z, fmaf(v.w, di.w, dot))));
+      }
+      total = sum_of_8(total);
+      inv = total == 0.0f ? 0.0f : 1.0f / total;
+      dot = sum_of_8(dot) * inv;
+    }
+    if (on) {
+#pragma unroll
+      for (int i = 0; i < Q; ++i) {
+        const int q = part + 8 * i;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (DENSE) {
+          const float4 di = d[q];
+          const float f = ROUTER == 0 ? 1.0f : inv;
+          v = make_float4(s[i].x * ((di.x - dot) * f), s[i].y * ((di.y - dot) * f), s[i].z * ((di.z - dot) * f),
+                          s[i].w * ((di.w - dot) * f));
+        }
+        store_word(out, 4 * q, E, a.wide, v);
+      }
+    }
+    __syncwarp();  // the selected entries go over the row's
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (on && e[h] >= 0)
+        from_f32(ROUTER == 0 ? sj[h] * (dj[h] + ds[h] - dot) : (ds[h] + (dj[h] - dot) * inv) * slope[h], out + e[h]);
+    }
+  }
+}
+
+template <int Q, typename TL>
+cudaError_t launch_backward_words(const RouteBackwardArgs& a, int n_sm, cudaStream_t st) {
+  auto kernel = route_backward_words_kernel<Q, TL, 1, false>;
+  if (a.router == 0) kernel = route_backward_words_kernel<Q, TL, 0, true>;
+  else if (a.dprob != nullptr) kernel = route_backward_words_kernel<Q, TL, 1, true>;
+  const int64_t want = (a.T + 4 * WARPS - 1) / (4 * WARPS);
+  kernel<<<(int)std::min<int64_t>(want, 8 * n_sm), THREADS, 0, st>>>(a);
+  return cudaGetLastError();
+}
+template <typename TL>
+cudaError_t launch_backward_words(const RouteBackwardArgs& args, int n_sm, cudaStream_t st) {
+  RouteBackwardArgs a = args;
+  const size_t unit = 4 * sizeof(TL);
+  a.wide = a.E % 4 == 0 && a.stride % 4 == 0 && a.out_stride % 4 == 0 &&
+           reinterpret_cast<uintptr_t>(a.logits) % unit == 0 && reinterpret_cast<uintptr_t>(a.dlogits) % unit == 0;
+  const int q = (a.E + 31) / 32;
+  if (q <= 1) return launch_backward_words<1, TL>(a, n_sm, st);
+  if (q <= 2) return launch_backward_words<2, TL>(a, n_sm, st);
+  if (q <= 4) return launch_backward_words<4, TL>(a, n_sm, st);
+  if (q <= 5) return launch_backward_words<5, TL>(a, n_sm, st);
+  if (q <= 6) return launch_backward_words<6, TL>(a, n_sm, st);
+  return launch_backward_words<8, TL>(a, n_sm, st);
 }
 
 template <int C, typename TL>
@@ -339,8 +540,13 @@ cudaError_t launch_route(const RouteArgs& a, bool bf16, int n_sm, cudaStream_t s
 }
 
 cudaError_t launch_route_backward(const RouteBackwardArgs& a, bool bf16, int n_sm, cudaStream_t st) {
-  if (bf16) ROUTE_BY_C(launch_route_backward_c, __nv_bfloat16);
-  ROUTE_BY_C(launch_route_backward_c, float);
+  if (a.E <= 256) return bf16 ? launch_backward_words<__nv_bfloat16>(a, n_sm, st) : launch_backward_words<float>(a, n_sm, st);
+  if (bf16) {
+    if (a.E <= 512) return launch_route_backward_c<16, __nv_bfloat16>(a, n_sm, st);
+    return launch_route_backward_c<32, __nv_bfloat16>(a, n_sm, st);
+  }
+  if (a.E <= 512) return launch_route_backward_c<16, float>(a, n_sm, st);
+  return launch_route_backward_c<32, float>(a, n_sm, st);
 }
 
 }  // namespace mok

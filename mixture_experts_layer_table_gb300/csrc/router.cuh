@@ -44,6 +44,7 @@ struct RouteBackwardArgs {
   const float* dprob;       // [E] or null
   void* dlogits;            // the logits' type
   int* status;              // or null
+  bool wide;                // set by the launcher: rows can be read and written 4 experts at a time
 };
 
 constexpr int ROUTE_MAX_E = 1024;

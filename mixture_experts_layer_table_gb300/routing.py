@@ -134,7 +134,7 @@ class Router:
             status = _address(device_status, (2,), torch.int32, "device_status")
         stride = 0
         if out is None:
-            out = torch.empty(self._shape, dtype=self.dtype, device=logits.device)
+            out = logits.new_empty(self._shape)
         else:
             stride = _rows(out, *self._shape, self.dtype, "out")
         code = self._call_backward(self._ref, logits.data_ptr(), idx, dg, dp, out.data_ptr(), stride, status,
