@@ -322,9 +322,7 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
 // The same by the hardware's exponential and reciprocal (off by 2^-22 and by 2^-24 |x|): 8 instructions instead of 22
 // for the entries that only the balance term reaches.
 __device__ __forceinline__ void sigmoid_and_slope_fast(float x, float& s, float& slope) {
-  float e, f;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fabsf(x) * -1.442695041f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(1.0f + e));
+  const float e = exp2_fast(fabsf(x) * -LOG2E), f = inverse_fast(1.0f + e);
   s = x >= 0.0f ? f : e * f;
   slope = e * f * f;
 }
@@ -352,9 +350,36 @@ __device__ __forceinline__ float sum_of_8(float x) {
   for (int o = 4; o > 0; o >>= 1) x += __shfl_xor_sync(ALL, x, o);
   return x;
 }
+// 4 experts as they lie in a row
+template <typename TL>
+struct Word {
+  using type = uint4;
+};
+template <>
+struct Word<__nv_bfloat16> {
+  using type = uint2;
+};
+__device__ __forceinline__ float4 unpack_word(uint4 v) {
+  return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+}
+__device__ __forceinline__ float4 unpack_word(uint2 v) {
+  return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                     __uint_as_float(v.y & 0xffff0000u));
+}
+
+// Blocks on an SM, and for dense rows the grid: more of them, of which the last find a part of the SMs idle, cost up to
+// 20%; with fewer registers for one more block 256 experts took 36 us instead of 27.
+constexpr int backward_blocks(int Q, bool dense) { return !dense ? 4 : Q <= 5 ? 3 : 2; }
+
+// Aligned rows come through shared memory, the next four tokens' under the arithmetic of these (cp.async), and the
+// selected logits are read from there: no load waits for another.
 template <int Q, typename TL, int ROUTER, bool DENSE>
-__global__ void __launch_bounds__(THREADS) route_backward_words_kernel(const RouteBackwardArgs a) {
+__global__ void __launch_bounds__(THREADS, backward_blocks(Q, DENSE)) route_backward_words_kernel(const RouteBackwardArgs a) {
   __shared__ float4 d[Q * 8];
+  using W = typename Word<TL>::type;
+  extern __shared__ __align__(16) unsigned char ring_bytes[];  // DENSE, aligned: [WARPS][2][Q][32] words
+  W* ring = reinterpret_cast<W*>(ring_bytes) + (threadIdx.x >> 5) * (2 * Q * 32);
+  const bool ringed = DENSE && a.wide;
   const int lane = threadIdx.x & 31, row = lane >> 3, part = lane & 7;
   const int E = a.E, k = a.k;
   if (DENSE) {
@@ -363,31 +388,74 @@ __global__ void __launch_bounds__(THREADS) route_backward_words_kernel(const Rou
     __syncthreads();
   }
   const int64_t step = (int64_t)gridDim.x * WARPS * 4;
-  for (int64_t base = ((int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5)) * 4; base < a.T; base += step) {
-    const bool on = base + row < a.T;
-    const int64_t t = on ? base + row : a.T - 1;
-    const TL* from = static_cast<const TL*>(a.logits) + t * a.stride;
-    TL* out = static_cast<TL*>(a.dlogits) + t * a.out_stride;
-    float4 s[Q];
-    if (DENSE) {
+  int64_t base = ((int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5)) * 4;
+  const TL* logits = static_cast<const TL*>(a.logits);
+  auto token = [&](int64_t first) { return min(first + row, a.T - 1); };
+  auto fetch = [&](int64_t first, int stage) {
+    if (ringed && first < a.T) {
+      const TL* from = logits + token(first) * a.stride;
+      const uint32_t to = (uint32_t)__cvta_generic_to_shared(ring + stage * (Q * 32) + lane);
 #pragma unroll
-      for (int i = 0; i < Q; ++i) s[i] = load_word(from, 4 * (part + 8 * i), E, a.wide);
+      for (int i = 0; i < Q; ++i) {
+        const int e = 4 * (part + 8 * i);
+        if (e < E)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to + i * 32 * (int)sizeof(W)), "l"(from + e),
+                       "n"(sizeof(W))
+                       : "memory");
+      }
     }
-    // the selected experts: one to a lane, a second one where k > 8
-    int e[2] = {-1, -1};
-    float x[2], dg[2] = {0.0f, 0.0f}, dj[2] = {0.0f, 0.0f};
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // the selected experts, one to a lane, a second one where k > 8, and their gates' gradients
+  auto selected = [&](int64_t first, int (&e)[2], float (&dg)[2]) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int j = part + 8 * h;
+      e[h] = -1, dg[h] = 0.0f;
+      if (j < k && a.dgates != nullptr && first < a.T) {
+        e[h] = a.topk_idx[token(first) * k + j];
+        dg[h] = a.dgates[token(first) * k + j];
+      }
+    }
+  };
+  int e_next[2];
+  float dg_next[2];
+  fetch(base, 0);
+  selected(base, e_next, dg_next);
+  for (int stage = 0; base < a.T; base += step, stage ^= 1) {
+    const bool on = base + row < a.T;
+    const int64_t t = token(base);
+    const TL* from = logits + t * a.stride;
+    TL* out = static_cast<TL*>(a.dlogits) + t * a.out_stride;
+    int e[2] = {e_next[0], e_next[1]};
+    float x[2], dg[2] = {dg_next[0], dg_next[1]}, dj[2] = {0.0f, 0.0f};
+    fetch(base + step, stage ^ 1);
+    selected(base + step, e_next, dg_next);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncwarp();
+    const W* words = ring + stage * (Q * 32);
+    float4 s[Q];
+    if (DENSE) {
+#pragma unroll
+      for (int i = 0; i < Q; ++i) {
+        const int at = 4 * (part + 8 * i);
+        if (ringed) s[i] = at < E ? unpack_word(words[i * 32 + lane]) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        else s[i] = load_word(from, at, E, false);
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
       x[h] = -INFINITY;
-      if (j < k && a.dgates != nullptr) {
-        e[h] = a.topk_idx[t * k + j];
+      if (part + 8 * h < k && a.dgates != nullptr) {
         if (e[h] < 0 || e[h] >= E) {
           report_status(a.status, MOK_DEV_INVALID_ROUTING, SITE_TOPK_INDEX);
-          e[h] = -1;
+          e[h] = -1, dg[h] = 0.0f;
         } else {
-          x[h] = to_f32(from[e[h]]);
-          dg[h] = a.dgates[t * k + j];
+          const int q = e[h] >> 2;
+          if (ringed)
+            x[h] = to_f32(reinterpret_cast<const TL*>(words + (q >> 3) * 32 + row * 8 + (q & 7))[e[h] & 3]);
+          else
+            x[h] = to_f32(from[e[h]]);
           if (DENSE) dj[h] = reinterpret_cast<const float*>(d)[e[h]];
         }
       }
@@ -400,10 +468,12 @@ __global__ void __launch_bounds__(THREADS) route_backward_words_kernel(const Rou
 #pragma unroll
       for (int o = 4; o > 0; o >>= 1) shift = fmaxf(shift, __shfl_xor_sync(ALL, shift, o));
       if (shift == -INFINITY) shift = 0.0f;
+      const float offset = -shift * LOG2E;
       float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < Q; ++i) {
-        s[i] = make_float4(expf(s[i].x - shift), expf(s[i].y - shift), expf(s[i].z - shift), expf(s[i].w - shift));
+        s[i] = make_float4(exp2_fast(fmaf(s[i].x, LOG2E, offset)), exp2_fast(fmaf(s[i].y, LOG2E, offset)),
+                           exp2_fast(fmaf(s[i].z, LOG2E, offset)), exp2_fast(fmaf(s[i].w, LOG2E, offset)));
         sum += (s[i].x + s[i].y) + (s[i].z + s[i].w);
       }
       sum = sum_of_8(sum);
@@ -470,6 +540,7 @@ __global__ void __launch_bounds__(THREADS) route_backward_words_kernel(const Rou
       if (on && e[h] >= 0)
         from_f32(ROUTER == 0 ? sj[h] * (dj[h] + ds[h] - dot) : (ds[h] + (dj[h] - dot) * inv) * slope[h], out + e[h]);
     }
+    // (the barrier above also frees this stage: every lane has read it)
   }
 }
 
@@ -478,8 +549,15 @@ cudaError_t launch_backward_words(const RouteBackwardArgs& a, int n_sm, cudaStre
   auto kernel = route_backward_words_kernel<Q, TL, 1, false>;
   if (a.router == 0) kernel = route_backward_words_kernel<Q, TL, 0, true>;
   else if (a.dprob != nullptr) kernel = route_backward_words_kernel<Q, TL, 1, true>;
+  const bool dense = a.router == 0 || a.dprob != nullptr;
+  const int smem = dense && a.wide ? WARPS * 2 * Q * 32 * 4 * (int)sizeof(TL) : 0;
+  if (smem > 40 * 1024) {
+    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err != cudaSuccess) return err;
+  }
   const int64_t want = (a.T + 4 * WARPS - 1) / (4 * WARPS);
-  kernel<<<(int)std::min<int64_t>(want, 8 * n_sm), THREADS, 0, st>>>(a);
+  const int most = dense ? backward_blocks(Q, true) : 8;
+  kernel<<<(int)std::min<int64_t>(want, most * n_sm), THREADS, smem, st>>>(a);
   return cudaGetLastError();
 }
 template <typename TL>

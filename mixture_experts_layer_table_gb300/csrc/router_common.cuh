@@ -30,6 +30,19 @@ __device__ __forceinline__ float warp_max(float x) {
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
+// The hardware's exponential and reciprocal, off by about 2^-22.
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float inverse_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+constexpr float LOG2E = 1.442695041f;
+
 // Unsigned integers in the order of the floats (-inf is the least, above 0); -0 equals +0.
 __device__ __forceinline__ uint32_t ordered(float r) {
   const int b = __float_as_int(r + 0.0f);

@@ -29,17 +29,6 @@ constexpr int BLOCKS_OF_SM = 3;  // 72 to 80 registers; 4 (64 registers) were 9%
 // hardware's exponential and reciprocal, 4 instructions instead of about 18, with a check that the order is certain.
 enum PairMode { LOGITS = 0, SIGMOID = 1, SIGMOID_FAST = 2 };
 
-__device__ __forceinline__ float exp2_fast(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ float inverse_fast(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-constexpr float LOG2E = 1.442695041f;
 // 1 / (1 + e^-x), off by less than 4e-7
 __device__ __forceinline__ float sigmoid_fast(float x) { return inverse_fast(1.0f + exp2_fast(x * -LOG2E)); }
 
