@@ -396,7 +396,7 @@ typedef struct {
  * The five from counts on need ws: at least MOK_ROUTE_WS_BYTES, 256-byte aligned, zero-filled once
  * before its first use (each call leaves it ready for the next); otherwise ws may be NULL.  With
  * them T stays below 2^31.  A logit that makes a token's scores NaN makes prob_sum and loss NaN. */
-#define MOK_ROUTE_WS_BYTES 12544
+#define MOK_ROUTE_WS_BYTES 98560
 mok_status mok_route(const mok_route_desc* desc, const void* logits, const float* bias, int32_t* topk_idx,
                      float* gates, float* scores, int32_t* counts, float* prob_sum, float* loss, float* dprob,
                      float* bias_next, void* ws, size_t ws_bytes, void* stream);

@@ -66,9 +66,10 @@ __device__ __forceinline__ void finish_balance(const RouteArgs& a, const int* co
   const float units_of = __int_as_float((127 + a.sum_shift) << 23);
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
     const float p = sum_of(e);
-    if (isfinite(p)) atomicAdd(&a.acc_prob[e], (unsigned long long)__float2ll_rn(p * units_of));
+    const int at = (blockIdx.x % ROUTE_COPIES) * ROUTE_MAX_E + e;
+    if (isfinite(p)) atomicAdd(&a.acc_prob[at], (unsigned long long)__float2ll_rn(p * units_of));
     else atomicOr(a.not_finite, 1u);
-    if (counts[e] != 0) atomicAdd(&a.acc_counts[e], counts[e]);
+    if (counts[e] != 0) atomicAdd(&a.acc_counts[at], counts[e]);
   }
   __threadfence();
   __syncthreads();
@@ -80,10 +81,15 @@ __device__ __forceinline__ void finish_balance(const RouteArgs& a, const int* co
   const float unit = __int_as_float((127 - a.sum_shift) << 23);
   float loss = 0.0f;
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
-    const long long units = (long long)__ldcg(&a.acc_prob[e]);
-    const int n = __ldcg(&a.acc_counts[e]);
-    a.acc_prob[e] = 0ull;
-    a.acc_counts[e] = 0;
+    long long units = 0;
+    int n = 0;
+#pragma unroll
+    for (int c = 0; c < ROUTE_COPIES; ++c) {
+      units += (long long)__ldcg(&a.acc_prob[c * ROUTE_MAX_E + e]);
+      n += __ldcg(&a.acc_counts[c * ROUTE_MAX_E + e]);
+    }
+#pragma unroll
+    for (int c = 0; c < ROUTE_COPIES; ++c) a.acc_prob[c * ROUTE_MAX_E + e] = 0ull, a.acc_counts[c * ROUTE_MAX_E + e] = 0;
     const float p = bad ? __int_as_float(0x7fffffff) : __ll2float_rn(units) * unit;
     const float d = (float)n * a.dprob_unit;
     if (a.counts != nullptr) a.counts[e] = n;

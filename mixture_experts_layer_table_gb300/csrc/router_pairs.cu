@@ -11,7 +11,7 @@
 //      11 of 128) are listed in shared memory;
 //   4. a lane to each listed expert counts how many are better: its place;
 //   5. the gates of the tokens of a few such steps are formed together, a lane to each selected expert.
-// A token for which this does not do (more than 32 experts listed, too few unmasked) is selected by the whole warp, one expert at a time, by the definition.
+// A token for which this does not do (more than 64 experts listed, too few unmasked) is selected by the whole warp, one expert at a time, by the definition.
 #include <algorithm>
 #include <cstddef>
 
@@ -23,6 +23,7 @@ namespace {
 
 constexpr int WARPS = 8;
 constexpr int THREADS = 32 * WARPS;
+constexpr int MAX_EXPERTS = 256;  // 16 lanes of at most 16
 constexpr int BLOCKS_OF_SM = 3;  // 72 to 80 registers; 4 (64 registers) were 9% slower, 2 8%
 
 // How rank values are formed.  LOGITS: softmax without a bias, ranked by the logits.  FAST: a biased sigmoid by the
@@ -34,26 +35,39 @@ __device__ __forceinline__ float sigmoid_fast(float x) { return inverse_fast(1.0
 
 
 // One token by the definition, by the whole warp: lane j < k returns the j-th best expert, its score in *score.
-// `row` [E] is overwritten with the rank values.
+// `row` [E] is overwritten with the rank values; lane l holds those of the experts l, l + 32, ... (at most 256).
 template <typename TL>
 __device__ __noinline__ int select_by_warp(const RouteArgs& a, int64_t t, float* row, int lane, float* score) {
+  constexpr int HELD = MAX_EXPERTS / 32;
   const TL* from = static_cast<const TL*>(a.logits) + t * a.stride;
-  const bool by_logit = a.router == 0 && a.bias == nullptr;
-  float m = -INFINITY, inv = 1.0f;
-  if (a.router == 0) {
-    for (int e = lane; e < a.E; e += 32) m = fmaxf(m, to_f32(from[e]));
+  const bool softmax = a.router == 0;  // without a bias: ranked by its logits
+  float x[HELD], m = -INFINITY, inv = 1.0f;
+#pragma unroll
+  for (int i = 0; i < HELD; ++i) {
+    const int e = lane + 32 * i;
+    x[i] = e < a.E ? to_f32(from[e]) : -INFINITY;
+    m = fmaxf(m, x[i]);
+  }
+  if (softmax) {
     m = warp_max(m);
     if (m == -INFINITY) m = 0.0f;
     float sum = 0.0f;
-    for (int e = lane; e < a.E; e += 32) sum += expf(to_f32(from[e]) - m);
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) sum += expf(x[i] - m);
     sum = warp_sum(sum);
     inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   }
   __syncwarp();
-  for (int e = lane; e < a.E; e += 32) {
-    const float x = to_f32(from[e]), b = a.bias != nullptr ? a.bias[e] : 0.0f;
-    const float r = by_logit ? x : a.router == 0 ? fmaf(expf(x - m), inv, b) : sigmoid(x) + b;
-    row[e] = x > -INFINITY && r > -INFINITY ? r : -INFINITY;
+  float r[HELD];
+#pragma unroll
+  for (int i = 0; i < HELD; ++i) {
+    const int e = lane + 32 * i;
+    r[i] = x[i];
+    if (e < a.E) {
+      if (!softmax) r[i] = sigmoid(x[i]) + (a.bias != nullptr ? a.bias[e] : 0.0f);
+      if (!(x[i] > -INFINITY) || !(r[i] > -INFINITY)) r[i] = -INFINITY;
+      row[e] = r[i];
+    }
   }
   __syncwarp();
   const int size = a.E / a.n_group;
@@ -61,8 +75,9 @@ __device__ __noinline__ int select_by_warp(const RouteArgs& a, int64_t t, float*
   if (a.n_group > 1) {
     float m1 = -INFINITY, m2 = -INFINITY;
     if (lane < a.n_group)
+#pragma unroll 4
       for (int i = 0; i < size; ++i) merge_top2(m1, m2, row[lane * size + i], -INFINITY);
-    if (by_logit && a.group_top2) m1 = m1 > -INFINITY ? expf(m1 - m) : m1, m2 = m2 > -INFINITY ? expf(m2 - m) : m2;
+    if (softmax && a.group_top2) m1 = m1 > -INFINITY ? expf(m1 - m) : m1, m2 = m2 > -INFINITY ? expf(m2 - m) : m2;
     const float value = a.group_top2 && m2 > -INFINITY ? m1 + m2 : m1;
     int better = 0;
     for (int h = 0; h < a.n_group; ++h) {
@@ -71,33 +86,39 @@ __device__ __noinline__ int select_by_warp(const RouteArgs& a, int64_t t, float*
     }
     keep = __ballot_sync(ALL, lane < a.n_group && better < a.topk_group);
   }
+  uint32_t key[HELD];  // 0: not in play, or taken
+#pragma unroll
+  for (int i = 0; i < HELD; ++i) {
+    const int e = lane + 32 * i;
+    key[i] = e < a.E && (a.n_group == 1 || (keep >> (e / size)) & 1u) ? ordered(r[i]) : 0u;
+  }
   int my_e = 0;
   for (int j = 0; j < a.k; ++j) {
-    uint32_t top = 0u;  // 0: nothing left; a taken expert holds NaN
-    int at = a.E;
-    for (int e = lane; e < a.E; e += 32) {
-      const float r = row[e];
-      const uint32_t key = (a.n_group == 1 || (keep >> (e / size)) & 1u) && r == r ? ordered(r) : 0u;
-      if (key > top) top = key, at = e;
-    }
+    uint32_t top = 0u;
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < HELD; ++i)
+      if (key[i] > top) top = key[i], at = i;
     const uint32_t best = __reduce_max_sync(ALL, top);
-    const int e = __reduce_min_sync(ALL, top == best ? at : a.E);
-    if (lane == (e & 31)) row[e] = __int_as_float(0x7fffffff);
-    __syncwarp();
+    const int e = __reduce_min_sync(ALL, top == best ? lane + 32 * at : MAX_EXPERTS);
+#pragma unroll
+    for (int i = 0; i < HELD; ++i)
+      if (lane + 32 * i == e) key[i] = 0u;
     if (lane == j) my_e = e;
   }
   if (lane < a.k) {
-    const float x = to_f32(from[my_e]);
-    *score = a.router == 0 ? expf(x - m) * inv : sigmoid(x);
+    const float xe = to_f32(from[my_e]);
+    *score = softmax ? expf(xe - m) * inv : sigmoid(xe);
   }
   return my_e;
 }
 
 constexpr int SLOW_TOKENS = 32;
+constexpr int LIST = 64;
 // A warp's shared memory, but for its rank values and sums.
 struct __align__(16) Scratch {
-  float value[2][36];  // rank values of the two tokens' listed experts, -inf behind them (read four at a time)
-  int expert[2][32];
+  float value[2][LIST + 4];  // rank values of the two tokens' listed experts, -inf behind them (read four at a time)
+  int expert[2][LIST];
   int pick[32];               // selected experts of the tokens of a batch
   float shift[32], inv[32];   // of the softmax of each
   int64_t slow[SLOW_TOKENS];  // tokens left over
@@ -301,7 +322,7 @@ __device__ __forceinline__ int select_pair(const RouteArgs& a, const PairShape& 
     if (part >= o) before += v;
   }
   int n = __shfl_sync(ALL, before, lane | 15);
-  const bool out = none || n > 32;  // the same on the token's lanes
+  const bool out = none || n > LIST;  // the same on the token's lanes
   if (out) n = 0, listed = 0u;
   before -= own;
   while (listed != 0u) {
@@ -310,11 +331,11 @@ __device__ __forceinline__ int select_pair(const RouteArgs& a, const PairShape& 
     w.value[half][before] = mine[c];
     w.expert[half][before++] = part * C + c;
   }
-  if (part >= n) w.value[half][part] = -INFINITY;
-  if (part + 16 >= n) w.value[half][part + 16] = -INFINITY;
-  __syncwarp();
-  // 4. their places
+  // 4. their places; -inf behind the list, as far as the longer of the two lists is read
   const int longest = max(n, __shfl_xor_sync(ALL, n, 16));
+  for (int at = part; at < longest + 4; at += 16)
+    if (at >= n) w.value[half][at] = -INFINITY;
+  __syncwarp();
   for (int at = part; at - part < longest; at += 16) {
     const float v = w.value[half][at];
     const float reach = v - margin;
@@ -368,7 +389,6 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_OF_SM) route_pairs_kernel(cons
 #pragma unroll
     for (int c = 0; c < C; ++c) my_sums[c] = 0.0f;
   }
-  if (lane < 8) w.value[lane >> 2][32 + (lane & 3)] = -INFINITY;
   __syncthreads();
   // Approximate rank values s + b are off by less than 4e-7 + 2^-23 |s + b|: their order is certain from twice that on.
   if (FAST) {

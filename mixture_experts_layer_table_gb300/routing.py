@@ -16,7 +16,7 @@ from ._native import _check, _expect, _stream, load
 P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 
 GROUP_MAX, GROUP_TOP2 = 0, 1
-ROUTE_WS_BYTES = 12544
+ROUTE_WS_BYTES = 98560
 LOGIT_TYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 
