@@ -201,7 +201,13 @@ __device__ __forceinline__ void get(const float* from, float (&v)[C]) {
   }
 }
 
-// The two largest of N values.
+__device__ __forceinline__ float min_nan(float a, float b) {  // NaN if one is
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// The two largest of N values, none of them NaN.
 template <int N>
 __device__ __forceinline__ void two_largest(const float (&v)[N], float& first, float& second) {
   first = fmaxf(v[0], v[1]), second = fminf(v[0], v[1]);
@@ -322,7 +328,7 @@ __device__ __forceinline__ int select_pair(const RouteArgs& a, const PairShape& 
     if (part >= o) before += v;
   }
   int n = __shfl_sync(ALL, before, lane | 15);
-  const bool out = none || n > LIST;  // the same on the token's lanes
+  const bool out = none || n > LIST || n < a.k;  // the same on the token's lanes
   if (out) n = 0, listed = 0u;
   before -= own;
   while (listed != 0u) {
@@ -383,7 +389,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_OF_SM) route_pairs_kernel(cons
   const float* bias = sh + part * S;
   float margin = 0.0f;
   for (int e = threadIdx.x; e < 16 * C; e += THREADS)
-    sh[e / C * S + e % C] = e >= E ? -INFINITY : a.bias != nullptr ? a.bias[e] : 0.0f;
+    sh[e / C * S + e % C] = e >= E ? -INFINITY : a.bias != nullptr ? fmaxf(a.bias[e], -INFINITY) : 0.0f;  // no NaN
   if (balance) {
     for (int e = threadIdx.x; e < 16 * C; e += THREADS) counts[e] = 0;
 #pragma unroll
@@ -418,7 +424,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_OF_SM) route_pairs_kernel(cons
         load_part<C>(logits + t * a.stride, part * C, E, a.wide, x);
         float inv = 1.0f, shift = 0.0f, least = INFINITY;
 #pragma unroll
-        for (int c = 0; c < C; ++c) least = fminf(least, x[c]);
+        for (int c = 0; c < C; ++c) least = min_nan(least, x[c]);
         if constexpr (MODE == LOGITS) {
           shift = -INFINITY;
           float sum = 0.0f;
@@ -444,10 +450,9 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_OF_SM) route_pairs_kernel(cons
             r[c] += s[c];
           }
         }
-        const bool masked = MODE != LOGITS && __any_sync(ALL, part_in && least == -INFINITY);
-        if (masked) {
+        if (__any_sync(ALL, part_in && !(least > -INFINITY))) {  // masked experts, or NaN
 #pragma unroll
-          for (int c = 0; c < C; ++c) r[c] = x[c] == -INFINITY ? -INFINITY : r[c];
+          for (int c = 0; c < C; ++c) r[c] = x[c] > -INFINITY ? r[c] : -INFINITY;
         }
         int* pick = w.pick + ((i + half) << a.slot_bits);
         int result = select_pair<C, MODE == LOGITS, FAST>(a, shape, r, shift, margin, lane, mine, w, pick);
@@ -455,7 +460,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_OF_SM) route_pairs_kernel(cons
           __syncwarp();
           get(bias, r);
 #pragma unroll
-          for (int c = 0; c < C; ++c) r[c] = x[c] == -INFINITY ? -INFINITY : r[c] + sigmoid(x[c]);
+          for (int c = 0; c < C; ++c) r[c] = x[c] > -INFINITY ? r[c] + sigmoid(x[c]) : -INFINITY;
           result = select_pair<C, false, false>(a, shape, r, 0.0f, 0.0f, lane, mine, w, pick);
         }
         const unsigned skips = __ballot_sync(ALL, result == 2 && on);
