@@ -117,8 +117,9 @@ constexpr int SLOW_TOKENS = 32;
 constexpr int LIST = 64;
 // A warp's shared memory, but for its rank values and sums.
 struct __align__(16) Scratch {
-  float value[2][LIST + 4];  // rank values of the two tokens' listed experts, -inf behind them (read four at a time)
+  float value[2][LIST];      // rank values of the two tokens' listed experts, -inf behind them (read four at a time)
   int expert[2][LIST];
+  float sorted[2][20];        // the best k and the next
   int pick[32];               // selected experts of the tokens of a batch
   float shift[32], inv[32];   // of the softmax of each
   int64_t slow[SLOW_TOKENS];  // tokens left over
@@ -201,9 +202,9 @@ __device__ __forceinline__ void get(const float* from, float (&v)[C]) {
   }
 }
 
-__device__ __forceinline__ float min_nan(float a, float b) {  // NaN if one is
+__device__ __forceinline__ float min_nan(float a, float b, float c) {  // NaN if one is
   float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 
@@ -337,34 +338,42 @@ __device__ __forceinline__ int select_pair(const RouteArgs& a, const PairShape& 
     w.value[half][before] = mine[c];
     w.expert[half][before++] = part * C + c;
   }
-  // 4. their places; -inf behind the list, as far as the longer of the two lists is read
+  // 4. their places, 16 against 16; -inf behind the list, as far as the longer of the two lists is read
   const int longest = max(n, __shfl_xor_sync(ALL, n, 16));
-  for (int at = part; at < longest + 4; at += 16)
+  for (int at = part; at - part < longest; at += 16)
     if (at >= n) w.value[half][at] = -INFINITY;
+  if (FAST) {
+    w.sorted[half][part] = part == n ? -INFINITY : INFINITY;
+    if (part == 0) w.sorted[half][16] = n == 16 ? -INFINITY : INFINITY;
+  }
   __syncwarp();
   for (int at = part; at - part < longest; at += 16) {
     const float v = w.value[half][at];
-    const float reach = v - margin;
-    int better = 0, near = 0;
-    for (int j = 0; j < longest; j += 4) {
-      const float4 o = *reinterpret_cast<const float4*>(&w.value[half][j]);
-      if (FAST) {
-        better += o.x > v, near += o.x > reach;
-        better += o.y > v, near += o.y > reach;
-        better += o.z > v, near += o.z > reach;
-        better += o.w > v, near += o.w > reach;
-      } else {  // ties to the expert before
-        better += at > j ? o.x >= v : o.x > v;
-        better += at > j + 1 ? o.y >= v : o.y > v;
-        better += at > j + 2 ? o.z >= v : o.z > v;
-        better += at > j + 3 ? o.w >= v : o.w > v;
+    int better = 0;
+    for (int block = 0; block < longest; block += 16) {
+#pragma unroll
+      for (int j = 0; j < 16; j += 4) {
+        const float4 o = *reinterpret_cast<const float4*>(&w.value[half][block + j]);
+        if (FAST) {
+          better += o.x > v;
+          better += o.y > v;
+          better += o.z > v;
+          better += o.w > v;
+        } else {  // ties to the expert before
+          better += at > block + j ? o.x >= v : o.x > v;
+          better += at > block + j + 1 ? o.y >= v : o.y > v;
+          better += at > block + j + 2 ? o.z >= v : o.z > v;
+          better += at > block + j + 3 ? o.w >= v : o.w > v;
+        }
       }
     }
-    if (at < n && better < a.k) {
-      // one of the best k must not have another (itself apart) within the margin below it
-      if (FAST && near > better + 1) unsure = true;
-      pick[better] = w.expert[half][at];
-    }
+    if (FAST && at < n && better <= a.k) w.sorted[half][better] = v;
+    if (at < n && better < a.k) pick[better] = w.expert[half][at];
+  }
+  if (FAST) {
+    // each of the best k is at least the margin above the next (equal values leave a place at infinity)
+    __syncwarp();
+    unsure = unsure || (part < a.k && !(w.sorted[half][part] - w.sorted[half][part + 1] >= margin));
   }
   const unsigned doubts = FAST ? __ballot_sync(ALL, unsure) : 0u;
   return out ? 2 : (doubts >> (16 * half)) & 0xffffu ? 1 : 0;
@@ -424,7 +433,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_OF_SM) route_pairs_kernel(cons
         load_part<C>(logits + t * a.stride, part * C, E, a.wide, x);
         float inv = 1.0f, shift = 0.0f, least = INFINITY;
 #pragma unroll
-        for (int c = 0; c < C; ++c) least = min_nan(least, x[c]);
+        for (int c = 0; c < C; c += 2) least = min_nan(least, x[c], x[c + 1]);
         if constexpr (MODE == LOGITS) {
           shift = -INFINITY;
           float sum = 0.0f;
