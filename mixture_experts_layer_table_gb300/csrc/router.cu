@@ -18,6 +18,7 @@ namespace {
 
 constexpr int WARPS = 8;
 constexpr int THREADS = 32 * WARPS;
+
 template <int C, typename TL>
 __device__ __forceinline__ void load_row(const TL* row, int lane, int E, float (&x)[C]) {
 #pragma unroll
@@ -222,92 +223,11 @@ __device__ __forceinline__ void sigmoid_and_slope(float x, float& s, float& slop
   slope = e * f * f;
 }
 
-template <int C, typename TL>
-__global__ void __launch_bounds__(THREADS) route_backward_kernel(const RouteBackwardArgs a) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int E = a.E, k = a.k;
-  float d[C];
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int e = lane * C + c;
-    d[c] = a.dprob != nullptr && e < E ? a.dprob[e] : 0.0f;
-  }
-  for (int64_t t = (int64_t)blockIdx.x * WARPS + warp; t < a.T; t += (int64_t)gridDim.x * WARPS) {
-    const TL* row = static_cast<const TL*>(a.logits) + t * a.stride;
-    TL* out = static_cast<TL*>(a.dlogits) + t * a.out_stride;
-    float s[C];
-    load_row<C>(row, lane, E, s);
-    // the selected experts, one to a lane
-    int e = -1;
-    float xj = -INFINITY, dg = 0.0f, dj = 0.0f;
-    if (lane < k && a.dgates != nullptr) {
-      e = a.topk_idx[t * k + lane];
-      if (e < 0 || e >= E) {
-        report_status(a.status, MOK_DEV_INVALID_ROUTING, SITE_TOPK_INDEX);
-        e = -1;
-      } else {
-        xj = to_f32(row[e]);
-        dg = a.dgates[t * k + lane];
-        dj = a.dprob != nullptr ? a.dprob[e] : 0.0f;
-      }
-    }
-    float sj, slope_j = 0.0f, slope[C], inv = 1.0f;
-    if (a.router == 0) {
-      float m;
-      inv = softmax_row<C>(s, &m);
-      sj = e >= 0 ? expf(xj - m) * inv : 0.0f;
-    } else {
-#pragma unroll
-      for (int c = 0; c < C; ++c) sigmoid_and_slope(s[c], s[c], slope[c]);
-      sigmoid_and_slope(xj, sj, slope_j);
-    }
-    float ds = e >= 0 ? a.scale * dg : 0.0f;
-    if (a.renorm) {
-      const float S = warp_sum(sj), dot = warp_sum(dg * sj);
-      ds = e < 0 || S == 0.0f ? 0.0f : a.scale * (dg - dot / S) / S;
-    }
-    if (a.router == 0) {
-      float dot = 0.0f;
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        s[c] *= inv;
-        dot = fmaf(s[c], d[c], dot);
-      }
-      dot = warp_sum(fmaf(sj, ds, dot));
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-        if (lane * C + c < E) from_f32(s[c] * (d[c] - dot), out + lane * C + c);
-      __syncwarp();
-      if (e >= 0) from_f32(sj * (dj + ds - dot), out + e);
-    } else {
-      float total = 0.0f, dot = 0.0f;
-      if (a.dprob != nullptr) {
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          total += s[c];
-          dot = fmaf(s[c], d[c], dot);
-        }
-        total = warp_sum(total);
-        dot = warp_sum(dot);
-        inv = total == 0.0f ? 0.0f : 1.0f / total;
-        dot *= inv;
-      } else {
-        inv = 0.0f;
-      }
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-        if (lane * C + c < E) from_f32((d[c] - dot) * inv * slope[c], out + lane * C + c);
-      __syncwarp();
-      if (e >= 0) from_f32((ds + (dj - dot) * inv) * slope_j, out + e);
-    }
-  }
-}
-
-// The same for up to 256 experts, in words of 4: 8 lanes to a token, 4 tokens to a warp, lane p the words p, p + 8, ...
-// of the row, so that a warp's accesses are whole 128-byte (bf16: 64-byte) pieces of 4 rows, the sums over a token
-// take 3 exchanges for 4 tokens at once, and the lanes that hold the selected experts are all in use (k = 8).
-// Q: words of a lane; rows that are not aligned are read and written one expert at a time.  DENSE: the row's scores are needed (softmax, or dprob); without it the row is zero but for the
-// selected experts, whose logits alone are read.
+// LANES lanes to a token (8 up to 256 experts, 16 up to 512, 32), 32 / LANES tokens to a warp; a row is read and written
+// in words of 4 experts, lane p the words p, p + LANES, ..., so that a warp's accesses are whole 128-byte (bf16:
+// 64-byte) pieces of its rows and the sums over a token take 3 to 5 exchanges for all its tokens at once; rows that
+// are not aligned are read and written one expert at a time.  Q: words of a lane.  DENSE: the row's scores are needed
+// (softmax, or dprob); without it the row is zero but for the selected experts, whose logits alone are read.
 __device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
 __device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
   const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
@@ -345,9 +265,10 @@ __device__ __forceinline__ void store_word(TL* row, int e, int E, bool wide, flo
     if (e + 3 < E) from_f32(v.w, row + e + 3);
   }
 }
-__device__ __forceinline__ float sum_of_8(float x) {
+template <int LANES>
+__device__ __forceinline__ float token_sum(float x) {
 #pragma unroll
-  for (int o = 4; o > 0; o >>= 1) x += __shfl_xor_sync(ALL, x, o);
+  for (int o = LANES / 2; o > 0; o >>= 1) x += __shfl_xor_sync(ALL, x, o);
   return x;
 }
 // 4 experts as they lie in a row
@@ -371,24 +292,25 @@ __device__ __forceinline__ float4 unpack_word(uint2 v) {
 // 20%; with fewer registers for one more block 256 experts took 36 us instead of 27.
 constexpr int backward_blocks(int Q, bool dense) { return !dense ? 4 : Q <= 5 ? 3 : 2; }
 
-// Aligned rows come through shared memory, the next four tokens' under the arithmetic of these (cp.async), and the
+// Aligned rows come through shared memory, the next tokens' under the arithmetic of these (cp.async), and the
 // selected logits are read from there: no load waits for another.
-template <int Q, typename TL, int ROUTER, bool DENSE>
-__global__ void __launch_bounds__(THREADS, backward_blocks(Q, DENSE)) route_backward_words_kernel(const RouteBackwardArgs a) {
-  __shared__ float4 d[Q * 8];
+template <int LANES, int Q, typename TL, int ROUTER, bool DENSE>
+__global__ void __launch_bounds__(THREADS, backward_blocks(Q, DENSE)) route_backward_kernel(const RouteBackwardArgs a) {
+  constexpr int TOKENS = 32 / LANES, HELD = LANES == 8 ? 2 : 1;  // selected experts of a lane: at most 16 in all
+  __shared__ float4 d[Q * LANES];
   using W = typename Word<TL>::type;
   extern __shared__ __align__(16) unsigned char ring_bytes[];  // DENSE, aligned: [WARPS][2][Q][32] words
   W* ring = reinterpret_cast<W*>(ring_bytes) + (threadIdx.x >> 5) * (2 * Q * 32);
   const bool ringed = DENSE && a.wide;
-  const int lane = threadIdx.x & 31, row = lane >> 3, part = lane & 7;
+  const int lane = threadIdx.x & 31, row = lane / LANES, part = lane % LANES;
   const int E = a.E, k = a.k;
   if (DENSE) {
-    for (int e = threadIdx.x; e < Q * 32; e += THREADS)
+    for (int e = threadIdx.x; e < Q * LANES * 4; e += THREADS)
       reinterpret_cast<float*>(d)[e] = a.dprob != nullptr && e < E ? a.dprob[e] : 0.0f;
     __syncthreads();
   }
-  const int64_t step = (int64_t)gridDim.x * WARPS * 4;
-  int64_t base = ((int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5)) * 4;
+  const int64_t step = (int64_t)gridDim.x * WARPS * TOKENS;
+  int64_t base = ((int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5)) * TOKENS;
   const TL* logits = static_cast<const TL*>(a.logits);
   auto token = [&](int64_t first) { return min(first + row, a.T - 1); };
   auto fetch = [&](int64_t first, int stage) {
@@ -397,7 +319,7 @@ __global__ void __launch_bounds__(THREADS, backward_blocks(Q, DENSE)) route_back
       const uint32_t to = (uint32_t)__cvta_generic_to_shared(ring + stage * (Q * 32) + lane);
 #pragma unroll
       for (int i = 0; i < Q; ++i) {
-        const int e = 4 * (part + 8 * i);
+        const int e = 4 * (part + LANES * i);
         if (e < E)
           asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to + i * 32 * (int)sizeof(W)), "l"(from + e),
                        "n"(sizeof(W))
@@ -406,11 +328,11 @@ __global__ void __launch_bounds__(THREADS, backward_blocks(Q, DENSE)) route_back
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  // the selected experts, one to a lane, a second one where k > 8, and their gates' gradients
-  auto selected = [&](int64_t first, int (&e)[2], float (&dg)[2]) {
+  // the selected experts, one or two to a lane, and their gates' gradients
+  auto selected = [&](int64_t first, int (&e)[HELD], float (&dg)[HELD]) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int j = part + 8 * h;
+    for (int h = 0; h < HELD; ++h) {
+      const int j = part + LANES * h;
       e[h] = -1, dg[h] = 0.0f;
       if (j < k && a.dgates != nullptr && first < a.T) {
         e[h] = a.topk_idx[token(first) * k + j];
@@ -418,8 +340,8 @@ __global__ void __launch_bounds__(THREADS, backward_blocks(Q, DENSE)) route_back
       }
     }
   };
-  int e_next[2];
-  float dg_next[2];
+  int e_next[HELD];
+  float dg_next[HELD];
   fetch(base, 0);
   selected(base, e_next, dg_next);
   for (int stage = 0; base < a.T; base += step, stage ^= 1) {
@@ -427,8 +349,10 @@ __global__ void __launch_bounds__(THREADS, backward_blocks(Q, DENSE)) route_back
     const int64_t t = token(base);
     const TL* from = logits + t * a.stride;
     TL* out = static_cast<TL*>(a.dlogits) + t * a.out_stride;
-    int e[2] = {e_next[0], e_next[1]};
-    float x[2], dg[2] = {dg_next[0], dg_next[1]}, dj[2] = {0.0f, 0.0f};
+    int e[HELD];
+    float x[HELD], dg[HELD], dj[HELD];
+#pragma unroll
+    for (int h = 0; h < HELD; ++h) e[h] = e_next[h], dg[h] = dg_next[h], dj[h] = 0.0f;
     fetch(base + step, stage ^ 1);
     selected(base + step, e_next, dg_next);
     asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -438,35 +362,35 @@ __global__ void __launch_bounds__(THREADS, backward_blocks(Q, DENSE)) route_back
     if (DENSE) {
 #pragma unroll
       for (int i = 0; i < Q; ++i) {
-        const int at = 4 * (part + 8 * i);
+        const int at = 4 * (part + LANES * i);
         if (ringed) s[i] = at < E ? unpack_word(words[i * 32 + lane]) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
         else s[i] = load_word(from, at, E, false);
       }
     }
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < HELD; ++h) {
       x[h] = -INFINITY;
-      if (part + 8 * h < k && a.dgates != nullptr) {
+      if (part + LANES * h < k && a.dgates != nullptr) {
         if (e[h] < 0 || e[h] >= E) {
           report_status(a.status, MOK_DEV_INVALID_ROUTING, SITE_TOPK_INDEX);
           e[h] = -1, dg[h] = 0.0f;
         } else {
           const int q = e[h] >> 2;
           if (ringed)
-            x[h] = to_f32(reinterpret_cast<const TL*>(words + (q >> 3) * 32 + row * 8 + (q & 7))[e[h] & 3]);
+            x[h] = to_f32(reinterpret_cast<const TL*>(words + q / LANES * 32 + row * LANES + q % LANES)[e[h] & 3]);
           else
             x[h] = to_f32(from[e[h]]);
           if (DENSE) dj[h] = reinterpret_cast<const float*>(d)[e[h]];
         }
       }
     }
-    float shift = 0.0f, inv = 0.0f, sj[2], slope[2];
+    float shift = 0.0f, inv = 0.0f, sj[HELD], slope[HELD];
     if (ROUTER == 0) {
       shift = -INFINITY;
 #pragma unroll
       for (int i = 0; i < Q; ++i) shift = fmaxf(fmaxf(shift, fmaxf(s[i].x, s[i].y)), fmaxf(s[i].z, s[i].w));
 #pragma unroll
-      for (int o = 4; o > 0; o >>= 1) shift = fmaxf(shift, __shfl_xor_sync(ALL, shift, o));
+      for (int o = LANES / 2; o > 0; o >>= 1) shift = fmaxf(shift, __shfl_xor_sync(ALL, shift, o));
       if (shift == -INFINITY) shift = 0.0f;
       const float offset = -shift * LOG2E;
       float sum = 0.0f;
@@ -476,38 +400,46 @@ __global__ void __launch_bounds__(THREADS, backward_blocks(Q, DENSE)) route_back
                            exp2_fast(fmaf(s[i].z, LOG2E, offset)), exp2_fast(fmaf(s[i].w, LOG2E, offset)));
         sum += (s[i].x + s[i].y) + (s[i].z + s[i].w);
       }
-      sum = sum_of_8(sum);
+      sum = token_sum<LANES>(sum);
       inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) sj[h] = e[h] >= 0 ? expf(x[h] - shift) * inv : 0.0f;
+      for (int h = 0; h < HELD; ++h) sj[h] = e[h] >= 0 ? expf(x[h] - shift) * inv : 0.0f;
     } else {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < HELD; ++h) {
         sigmoid_and_slope(x[h], sj[h], slope[h]);
         if (e[h] < 0) sj[h] = slope[h] = 0.0f;
       }
     }
-    float ds[2] = {a.scale * dg[0], a.scale * dg[1]};
+    float ds[HELD], of_lane = 0.0f;
+#pragma unroll
+    for (int h = 0; h < HELD; ++h) ds[h] = a.scale * dg[h], of_lane += sj[h];
     if (a.renorm) {
-      const float S = sum_of_8(sj[0] + sj[1]), dot = sum_of_8(fmaf(dg[0], sj[0], dg[1] * sj[1]));
+      const float S = token_sum<LANES>(of_lane);
+      of_lane = 0.0f;
+#pragma unroll
+      for (int h = 0; h < HELD; ++h) of_lane = fmaf(dg[h], sj[h], of_lane);
+      const float dot = token_sum<LANES>(of_lane);
       const float inv_s = S == 0.0f ? 0.0f : 1.0f / S;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) ds[h] = e[h] >= 0 ? a.scale * (dg[h] - dot * inv_s) * inv_s : 0.0f;
+      for (int h = 0; h < HELD; ++h) ds[h] = e[h] >= 0 ? a.scale * (dg[h] - dot * inv_s) * inv_s : 0.0f;
     }
     float dot = 0.0f;
     if (ROUTER == 0) {
 #pragma unroll
       for (int i = 0; i < Q; ++i) {
-        const float4 di = d[part + 8 * i];
+        const float4 di = d[part + LANES * i];
         s[i].x *= inv, s[i].y *= inv, s[i].z *= inv, s[i].w *= inv;
         dot = fmaf(s[i].x, di.x, fmaf(s[i].y, di.y, fmaf(s[i].z, di.z, fmaf(s[i].w, di.w, dot))));
       }
-      dot = sum_of_8(fmaf(sj[0], ds[0], fmaf(sj[1], ds[1], dot)));
+#pragma unroll
+      for (int h = 0; h < HELD; ++h) dot = fmaf(sj[h], ds[h], dot);
+      dot = token_sum<LANES>(dot);
     } else if (DENSE) {
       float total = 0.0f;
 #pragma unroll
       for (int i = 0; i < Q; ++i) {  // the slopes in place of the logits
-        const float4 di = d[part + 8 * i];
+        const float4 di = d[part + LANES * i];
         float4 v;
         sigmoid_and_slope_fast(s[i].x, v.x, s[i].x);
         sigmoid_and_slope_fast(s[i].y, v.y, s[i].y);
@@ -516,14 +448,14 @@ __global__ void __launch_bounds__(THREADS, backward_blocks(Q, DENSE)) route_back
         total += (v.x + v.y) + (v.z + v.w);
         dot = fmaf(v.x, di.x, fmaf(v.y, di.y, fmaf(v.z, di.z, fmaf(v.w, di.w, dot))));
       }
-      total = sum_of_8(total);
+      total = token_sum<LANES>(total);
       inv = total == 0.0f ? 0.0f : 1.0f / total;
-      dot = sum_of_8(dot) * inv;
+      dot = token_sum<LANES>(dot) * inv;
     }
     if (on) {
 #pragma unroll
       for (int i = 0; i < Q; ++i) {
-        const int q = part + 8 * i;
+        const int q = part + LANES * i;
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (DENSE) {
           const float4 di = d[q];
@@ -536,7 +468,7 @@ __global__ void __launch_bounds__(THREADS, backward_blocks(Q, DENSE)) route_back
     }
     __syncwarp();  // the selected entries go over the row's
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < HELD; ++h) {
       if (on && e[h] >= 0)
         from_f32(ROUTER == 0 ? sj[h] * (dj[h] + ds[h] - dot) : (ds[h] + (dj[h] - dot) * inv) * slope[h], out + e[h]);
     }
@@ -544,35 +476,39 @@ __global__ void __launch_bounds__(THREADS, backward_blocks(Q, DENSE)) route_back
   }
 }
 
-template <int Q, typename TL>
-cudaError_t launch_backward_words(const RouteBackwardArgs& a, int n_sm, cudaStream_t st) {
-  auto kernel = route_backward_words_kernel<Q, TL, 1, false>;
-  if (a.router == 0) kernel = route_backward_words_kernel<Q, TL, 0, true>;
-  else if (a.dprob != nullptr) kernel = route_backward_words_kernel<Q, TL, 1, true>;
+template <int LANES, int Q, typename TL>
+cudaError_t launch_backward(const RouteBackwardArgs& a, int n_sm, cudaStream_t st) {
+  auto kernel = route_backward_kernel<LANES, Q, TL, 1, false>;
+  if (a.router == 0) kernel = route_backward_kernel<LANES, Q, TL, 0, true>;
+  else if (a.dprob != nullptr) kernel = route_backward_kernel<LANES, Q, TL, 1, true>;
   const bool dense = a.router == 0 || a.dprob != nullptr;
   const int smem = dense && a.wide ? WARPS * 2 * Q * 32 * 4 * (int)sizeof(TL) : 0;
   if (smem > 40 * 1024) {
     const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
   }
-  const int64_t want = (a.T + 4 * WARPS - 1) / (4 * WARPS);
+  constexpr int TOKENS = 32 / LANES * WARPS;  // of a block
+  const int64_t want = (a.T + TOKENS - 1) / TOKENS;
   const int most = dense ? backward_blocks(Q, true) : 8;
   kernel<<<(int)std::min<int64_t>(want, most * n_sm), THREADS, smem, st>>>(a);
   return cudaGetLastError();
 }
 template <typename TL>
-cudaError_t launch_backward_words(const RouteBackwardArgs& args, int n_sm, cudaStream_t st) {
+cudaError_t launch_backward(const RouteBackwardArgs& args, int n_sm, cudaStream_t st) {
   RouteBackwardArgs a = args;
   const size_t unit = 4 * sizeof(TL);
   a.wide = a.E % 4 == 0 && a.stride % 4 == 0 && a.out_stride % 4 == 0 &&
            reinterpret_cast<uintptr_t>(a.logits) % unit == 0 && reinterpret_cast<uintptr_t>(a.dlogits) % unit == 0;
-  const int q = (a.E + 31) / 32;
-  if (q <= 1) return launch_backward_words<1, TL>(a, n_sm, st);
-  if (q <= 2) return launch_backward_words<2, TL>(a, n_sm, st);
-  if (q <= 4) return launch_backward_words<4, TL>(a, n_sm, st);
-  if (q <= 5) return launch_backward_words<5, TL>(a, n_sm, st);
-  if (q <= 6) return launch_backward_words<6, TL>(a, n_sm, st);
-  return launch_backward_words<8, TL>(a, n_sm, st);
+  const int q = (a.E + 31) / 32;  // words of 8 lanes
+  if (q <= 1) return launch_backward<8, 1, TL>(a, n_sm, st);
+  if (q <= 2) return launch_backward<8, 2, TL>(a, n_sm, st);
+  if (q <= 4) return launch_backward<8, 4, TL>(a, n_sm, st);
+  if (q <= 5) return launch_backward<8, 5, TL>(a, n_sm, st);
+  if (q <= 6) return launch_backward<8, 6, TL>(a, n_sm, st);
+  if (q <= 8) return launch_backward<8, 8, TL>(a, n_sm, st);
+  if (q <= 12) return launch_backward<16, 6, TL>(a, n_sm, st);
+  if (q <= 16) return launch_backward<16, 8, TL>(a, n_sm, st);
+  return launch_backward<32, 8, TL>(a, n_sm, st);
 }
 
 template <int C, typename TL>
@@ -582,14 +518,6 @@ cudaError_t launch_route_c(const RouteArgs& a, int n_sm, cudaStream_t st) {
   route_kernel<C, TL><<<blocks, THREADS, (WARPS + 1) * a.E * 4, st>>>(a);
   return cudaGetLastError();
 }
-template <int C, typename TL>
-cudaError_t launch_route_backward_c(const RouteBackwardArgs& a, int n_sm, cudaStream_t st) {
-  const int64_t want = (a.T + WARPS - 1) / WARPS;
-  const int blocks = (int)(want > 6 * n_sm ? 6 * n_sm : want);
-  route_backward_kernel<C, TL><<<blocks, THREADS, 0, st>>>(a);
-  return cudaGetLastError();
-}
-
 }  // namespace
 
 // C experts to a lane: the least there is a kernel for.  3, 5, 6 and 12 keep groups whole lanes at 96, 160, 192
@@ -609,22 +537,20 @@ cudaError_t launch_route_backward_c(const RouteBackwardArgs& a, int n_sm, cudaSt
     return fn<32, TL>(a, n_sm, st);   \
   } while (0)
 
-// Two tokens to a warp from 2048 tokens on: 256 experts in 8 groups, without balance: 1024 tokens 4.7 us here and 4.9
-// there, 4096 tokens 9.7 and 7.4, 65536 tokens 95 and 42.
+// For many tokens, two of them to a warp: that kernel's steps for a token hardly grow with its experts, this one's do,
+// and a call needs tokens for all its warps.  Microseconds here and there, f32 logits, sigmoid with a bias, k = 8 in
+// 4 of 8 groups: 256 experts, 1024 tokens 4.7 and 6.0, 2048 tokens 6.0 and 6.0, 4096 tokens 9.9 and 7.3, 65536
+// tokens 95 and 38; 128 experts, 4096 tokens 5.9 and 5.8, 65536 tokens 60 and 30; ungrouped: 384 experts, 1024 tokens
+// 5.2 and 5.5, 4096 tokens 11.9 and 7.5; 64 experts, 4096 tokens 4.0 and 5.5, 16384 tokens 10.3 and 10.9, 65536
+// tokens 33 and 24; 32 experts, 16384 tokens 6.8 and 9.5, 65536 tokens 21 and 21.
 cudaError_t launch_route(const RouteArgs& a, bool bf16, int n_sm, cudaStream_t st) {
-  if (a.T >= 2048 && route_pairs_fit(a)) return launch_route_pairs(a, bf16, n_sm, st);
+  if (a.T * a.E * a.E >= int64_t{1} << 27 && route_pairs_fit(a)) return launch_route_pairs(a, bf16, n_sm, st);
   if (bf16) ROUTE_BY_C(launch_route_c, __nv_bfloat16);
   ROUTE_BY_C(launch_route_c, float);
 }
 
 cudaError_t launch_route_backward(const RouteBackwardArgs& a, bool bf16, int n_sm, cudaStream_t st) {
-  if (a.E <= 256) return bf16 ? launch_backward_words<__nv_bfloat16>(a, n_sm, st) : launch_backward_words<float>(a, n_sm, st);
-  if (bf16) {
-    if (a.E <= 512) return launch_route_backward_c<16, __nv_bfloat16>(a, n_sm, st);
-    return launch_route_backward_c<32, __nv_bfloat16>(a, n_sm, st);
-  }
-  if (a.E <= 512) return launch_route_backward_c<16, float>(a, n_sm, st);
-  return launch_route_backward_c<32, float>(a, n_sm, st);
+  return bf16 ? launch_backward<__nv_bfloat16>(a, n_sm, st) : launch_backward<float>(a, n_sm, st);
 }
 
 }  // namespace mok

@@ -1,17 +1,25 @@
-// Group-limited expert selection for many tokens: two tokens to a warp, 16 lanes to each.
+// Group-limited expert selection for many tokens: two tokens to a warp, 16 lanes to each (or one, where 16 lanes of 16
+// experts do not hold the groups: more than 256 experts, groups of 17 that take two lanes each, ...).
 //
 // With a warp to a token (router.cu) most of the instructions steer lanes: about 1,150 a token at 256 experts, k
 // rounds of "the best left" among them.  Here a warp's steps serve two tokens, and each token is selected in a few
-// steps (about 300 instructions):
-//   1. a lane holds C consecutive experts (16 C >= E) and finds the two largest of their rank values; lanes of a
-//      segment, a group or an equal part of one, merge theirs;
+// steps (about 400 instructions):
+//   1. a group lies on a power of two of lanes, C experts to a lane, the last ones fewer; a lane finds the two largest
+//      of its rank values; lanes of a segment, a group or an equal part of one, merge theirs;
 //   2. each group's lanes count the groups that are better;
 //   3. the least of the chosen segments' second largest values has at least 2 * topk_group * (segments of a group)
 //      >= k experts at or above it: a bound from below of the k-th largest value.  The experts that reach it (about
 //      11 of 128) are listed in shared memory;
 //   4. a lane to each listed expert counts how many are better: its place;
 //   5. the gates of the tokens of a few such steps are formed together, a lane to each selected expert.
-// A token for which this does not do (more than 64 experts listed, too few unmasked) is selected by the whole warp, one expert at a time, by the definition.
+// A token for which this does not do (more than 64 experts listed, too few unmasked) is selected by the whole warp, one
+// expert at a time, by the definition.
+//
+// 65,536 tokens of 256 experts (f32, sigmoid with a bias, 8 groups): 38 us, 1.8 TB/s; the row is read once, and the
+// bound is instructions (26.5 million of warps, issued in 62% of the cycles at 24 warps an SM, which wait on one
+// another's results: shared memory and shuffles between the steps).  4,096 tokens 7.3 us, with the balance outputs 10.
+// Of the instructions 30% place the listed experts, 27% load and score, 13% choose groups, 12% list, the rest merge
+// and form gates.
 #include <algorithm>
 #include <cstddef>
 
@@ -23,8 +31,9 @@ namespace {
 
 constexpr int WARPS = 8;
 constexpr int THREADS = 32 * WARPS;
-constexpr int MAX_EXPERTS = 256;  // 16 lanes of at most 16
-constexpr int BLOCKS_OF_SM = 3;  // 72 to 80 registers; 4 (64 registers) were 9% slower, 2 8%
+constexpr int MAX_EXPERTS = 512;  // 32 lanes of at most 16
+// 72 to 80 registers; 4 blocks (64 registers) took 46 us at 65,536 tokens of 256 experts instead of 42, 2 45
+constexpr int BLOCKS_OF_SM = 3;
 
 // How rank values are formed.  LOGITS: softmax without a bias, ranked by the logits.  FAST: a biased sigmoid by the
 // hardware's exponential and reciprocal, 4 instructions instead of about 18, with a check that the order is certain.
@@ -33,12 +42,10 @@ enum PairMode { LOGITS = 0, SIGMOID = 1, SIGMOID_FAST = 2 };
 // 1 / (1 + e^-x), off by less than 4e-7
 __device__ __forceinline__ float sigmoid_fast(float x) { return inverse_fast(1.0f + exp2_fast(x * -LOG2E)); }
 
-
 // One token by the definition, by the whole warp: lane j < k returns the j-th best expert, its score in *score.
-// `row` [E] is overwritten with the rank values; lane l holds those of the experts l, l + 32, ... (at most 256).
-template <typename TL>
+// `row` [E] is overwritten with the rank values; lane l holds those of the experts l, l + 32, ... (HELD of them).
+template <typename TL, int HELD>
 __device__ __noinline__ int select_by_warp(const RouteArgs& a, int64_t t, float* row, int lane, float* score) {
-  constexpr int HELD = MAX_EXPERTS / 32;
   const TL* from = static_cast<const TL*>(a.logits) + t * a.stride;
   const bool softmax = a.router == 0;  // without a bias: ranked by its logits
   float x[HELD], m = -INFINITY, inv = 1.0f;
@@ -139,38 +146,52 @@ constexpr int lane_stride() {
   return C == 8 || C == 16 ? C + 4 : C;
 }
 
-// A lane's experts of a row (-inf beyond E).
+// A lane's experts of a row, `held` of its C places from row on; -inf behind them.  WORDS: words of UNIT bytes can be
+// read, and none is held in part; ALL_OR_NONE: held is C or 0 in every lane.
+enum Rows { ALL_OR_NONE = 0, WORDS = 1, ELEMENTS = 2 };
 template <int C, typename TL>
-__device__ __forceinline__ void load_part(const TL* row, int first, int E, bool wide, float (&x)[C]) {
-  constexpr int BYTES = C * (int)sizeof(TL), UNIT = unit_of<C, TL>();
-  const bool in = first < E;
-  if (wide) {
+__device__ __forceinline__ void load_part(const TL* row, const TL* from, int held, int how, float (&x)[C]) {
+  constexpr int BYTES = C * (int)sizeof(TL), UNIT = unit_of<C, TL>(), OF_UNIT = UNIT / (int)sizeof(TL);
+  if (how != ELEMENTS) {
     uint32_t w[BYTES / 4];
-    const TL* from = row + (in ? first : 0);
-#pragma unroll
-    for (int j = 0; j < BYTES / UNIT; ++j) {
+    auto load = [&](const TL* p, int j) {
       if constexpr (UNIT == 16) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(from) + j);
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + j);
         w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
       } else if constexpr (UNIT == 8) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(from) + j);
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p) + j);
         w[2 * j] = v.x, w[2 * j + 1] = v.y;
       } else {
-        w[j] = __ldg(reinterpret_cast<const uint32_t*>(from) + j);
+        w[j] = __ldg(reinterpret_cast<const uint32_t*>(p) + j);
       }
+    };
+    if (how == ALL_OR_NONE) {
+      const TL* p = held > 0 ? from : row;
+#pragma unroll
+      for (int j = 0; j < BYTES / UNIT; ++j) load(p, j);
+    } else {
+      constexpr uint32_t NOTHING = sizeof(TL) == 4 ? 0xff800000u : 0xff80ff80u;
+#pragma unroll
+      for (int j = 0; j < BYTES / 4; ++j) w[j] = NOTHING;
+#pragma unroll
+      for (int j = 0; j < BYTES / UNIT; ++j)
+        if (j * OF_UNIT < held) load(from, j);
     }
 #pragma unroll
     for (int j = 0; j < BYTES / 4; ++j) {
       if constexpr (sizeof(TL) == 4) x[j] = __uint_as_float(w[j]);
       else x[2 * j] = __uint_as_float(w[j] << 16), x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
     }
-  } else if (in) {
+    if (how == ALL_OR_NONE && held == 0) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) x[c] = to_f32(row[first + c]);
-  }
-  if (!in) {
+      for (int c = 0; c < C; ++c) x[c] = -INFINITY;
+    }
+  } else {
 #pragma unroll
-    for (int c = 0; c < C; ++c) x[c] = -INFINITY;
+    for (int c = 0; c < C; ++c) {
+      x[c] = -INFINITY;
+      if (c < held) x[c] = to_f32(from[c]);
+    }
   }
 }
 
@@ -219,20 +240,23 @@ __device__ __forceinline__ void two_largest(const float (&v)[N], float& first, f
   }
 }
 
-// over the 16 lanes of a token
-__device__ __forceinline__ float half_max(float x) {
+// over the lanes of a token
+template <int LANES>
+__device__ __forceinline__ float token_max(float x) {
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(ALL, x, o));
+  for (int o = LANES / 2; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(ALL, x, o));
   return x;
 }
-__device__ __forceinline__ float half_min(float x) {
+template <int LANES>
+__device__ __forceinline__ float token_min(float x) {
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) x = fminf(x, __shfl_xor_sync(ALL, x, o));
+  for (int o = LANES / 2; o > 0; o >>= 1) x = fminf(x, __shfl_xor_sync(ALL, x, o));
   return x;
 }
-__device__ __forceinline__ float half_sum(float x) {
+template <int LANES>
+__device__ __forceinline__ float token_sum(float x) {
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(ALL, x, o);
+  for (int o = LANES / 2; o > 0; o >>= 1) x += __shfl_xor_sync(ALL, x, o);
   return x;
 }
 
@@ -265,34 +289,35 @@ __device__ __forceinline__ void store_selected(const RouteArgs& a, int64_t t, bo
   }
 }
 
-// How a block's tokens are cut up.
-struct PairShape {
-  int lanes, group;    // lanes of a group; this lane's
-  bool part_in;        // this lane has experts
+// How the experts lie on a token's lanes: a group on `lanes` of them, a power of two, C to a lane, the last ones fewer.
+struct Place {
+  int lanes, group;  // lanes of a group; this lane's
+  int first, held;   // this lane's experts
+  bool bounds;       // its segment has two experts or more
   bool choose, top2;
 };
 
-// The selection of a warp's two tokens from their lanes' rank values r (shift: of each softmax): the places of the
-// experts in pick.  Returns (on all 16 lanes of a token): 0 done; 1 not certain, with approximate values (FAST: off by
-// less than margin / 2); 2 more than the list holds, or too few experts.
-template <int C, bool LOGIT_VALUES, bool FAST>
-__device__ __forceinline__ int select_pair(const RouteArgs& a, const PairShape& p, const float (&r)[C], float shift,
+// The selection of a warp's tokens, one on each LANES lanes, from the lanes' rank values r (shift: of each softmax):
+// the experts in pick.  Returns (on all lanes of a token): 0 done; 1 not certain, with approximate values (FAST: off
+// by less than margin / 2); 2 more than the list holds, or too few experts.
+template <int LANES, int C, bool LOGIT_VALUES, bool FAST>
+__device__ __forceinline__ int select_pair(const RouteArgs& a, const Place& p, const float (&r)[C], float shift,
                                            float margin, int lane, float* mine, Scratch& w, int* pick) {
-  const int half = lane >> 4, part = lane & 15;
+  const int half = lane / LANES, part = lane % LANES;
   put(mine, r);
   // 1. the two largest of the lane, of its segment and of its group
   float m1, m2;
   two_largest(r, m1, m2);
   float low = m2;  // the segment's second largest
 #pragma unroll
-  for (int o = 1; o < 16; o <<= 1) {
+  for (int o = 1; o < LANES; o <<= 1) {
     if (o < p.lanes) {
       merge_top2(m1, m2, __shfl_xor_sync(ALL, m1, o), __shfl_xor_sync(ALL, m2, o));
       if (o < a.segment_lanes) low = m2;
     }
   }
   // 2. the groups
-  bool in_play = p.part_in, unsure = false;
+  bool in_play = p.held > 0, unsure = false;
   if (p.choose) {
     float value = m1;
     if (p.top2) {
@@ -303,7 +328,7 @@ __device__ __forceinline__ int select_pair(const RouteArgs& a, const PairShape& 
     int better = 0, near = 0;
 #pragma unroll 4
     for (int h = 0; h < a.n_group; ++h) {
-      const float o = __shfl_sync(ALL, value, (lane & 16) + h * p.lanes);
+      const float o = __shfl_sync(ALL, value, half * LANES + h * p.lanes);
       if (FAST) {
         better += o > value;
         near += o > reach;  // itself among them
@@ -311,11 +336,11 @@ __device__ __forceinline__ int select_pair(const RouteArgs& a, const PairShape& 
         better += h < p.group ? o >= value : o > value;
       }
     }
-    in_play = p.part_in && better < a.topk_group;
+    in_play = p.held > 0 && better < a.topk_group;
     if (FAST) unsure = in_play && near > better + 1;
   }
   // 3. the listed experts, in their order
-  float bound = half_min(in_play ? low : INFINITY);
+  float bound = token_min<LANES>(in_play && p.bounds ? low : INFINITY);
   const bool none = !(bound > -INFINITY);
   bound = in_play ? bound - margin : INFINITY;
   unsigned listed = 0u;
@@ -324,11 +349,11 @@ __device__ __forceinline__ int select_pair(const RouteArgs& a, const PairShape& 
   const int own = __popc(listed);
   int before = own;
 #pragma unroll
-  for (int o = 1; o < 16; o <<= 1) {
-    const int v = __shfl_up_sync(ALL, before, o, 16);
+  for (int o = 1; o < LANES; o <<= 1) {
+    const int v = __shfl_up_sync(ALL, before, o, LANES);
     if (part >= o) before += v;
   }
-  int n = __shfl_sync(ALL, before, lane | 15);
+  int n = __shfl_sync(ALL, before, lane | (LANES - 1));
   const bool out = none || n > LIST || n < a.k;  // the same on the token's lanes
   if (out) n = 0, listed = 0u;
   before -= own;
@@ -336,18 +361,18 @@ __device__ __forceinline__ int select_pair(const RouteArgs& a, const PairShape& 
     const int c = __ffs(listed) - 1;
     listed &= listed - 1u;
     w.value[half][before] = mine[c];
-    w.expert[half][before++] = part * C + c;
+    w.expert[half][before++] = p.first + c;
   }
   // 4. their places, 16 against 16; -inf behind the list, as far as the longer of the two lists is read
-  const int longest = max(n, __shfl_xor_sync(ALL, n, 16));
-  for (int at = part; at - part < longest; at += 16)
+  const int longest = LANES == 32 ? n : max(n, __shfl_xor_sync(ALL, n, 16));
+  for (int at = part; at - part < longest; at += LANES)
     if (at >= n) w.value[half][at] = -INFINITY;
   if (FAST) {
-    w.sorted[half][part] = part == n ? -INFINITY : INFINITY;
-    if (part == 0) w.sorted[half][16] = n == 16 ? -INFINITY : INFINITY;
+    if (part <= 16) w.sorted[half][part] = part == n ? -INFINITY : INFINITY;
+    if (LANES == 16 && part == 0) w.sorted[half][16] = n == 16 ? -INFINITY : INFINITY;
   }
   __syncwarp();
-  for (int at = part; at - part < longest; at += 16) {
+  for (int at = part; at - part < longest; at += LANES) {
     const float v = w.value[half][at];
     int better = 0;
     for (int block = 0; block < longest; block += 16) {
@@ -376,46 +401,52 @@ __device__ __forceinline__ int select_pair(const RouteArgs& a, const PairShape& 
     unsure = unsure || (part < a.k && !(w.sorted[half][part] - w.sorted[half][part + 1] >= margin));
   }
   const unsigned doubts = FAST ? __ballot_sync(ALL, unsure) : 0u;
-  return out ? 2 : (doubts >> (16 * half)) & 0xffffu ? 1 : 0;
+  return out ? 2 : doubts >> (half * LANES) & (ALL >> (32 - LANES)) ? 1 : 0;
 }
 
-template <int C, typename TL, int MODE>
+template <int LANES, int C, typename TL, int MODE>
 __global__ void __launch_bounds__(THREADS, BLOCKS_OF_SM) route_pairs_kernel(const RouteArgs a) {
-  // [16] lanes' bias, [WARPS][32] lanes' rank values; balance: [16 C] counts, [2 WARPS][16] lanes' sums
+  // [LANES] lanes' bias, [WARPS][32] lanes' rank values; balance: [LANES C] counts, [WARPS][32] lanes' sums
   extern __shared__ __align__(16) float sh[];
   constexpr int S = lane_stride<C>();
   __shared__ Scratch scratch[WARPS];
   constexpr bool FAST = MODE == SIGMOID_FAST;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = lane >> 4, part = lane & 15;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = lane / LANES, part = lane % LANES;
+  constexpr int TOKENS = 32 / LANES;
   const int E = a.E, k = a.k;
   const bool balance = a.ticket != nullptr;
-  float* rows = sh + 16 * S;
+  float* rows = sh + LANES * S;
   int* counts = balance ? reinterpret_cast<int*>(rows + WARPS * 32 * S) : nullptr;
-  float* sums = rows + WARPS * 32 * S + 16 * C;
+  float* sums = rows + WARPS * 32 * S + LANES * C;
   Scratch& w = scratch[warp];
   float* mine = rows + (warp * 32 + lane) * S;
   float* my_sums = sums + (warp * 32 + lane) * S;
   const float* bias = sh + part * S;
   float margin = 0.0f;
-  for (int e = threadIdx.x; e < 16 * C; e += THREADS)
-    sh[e / C * S + e % C] = e >= E ? -INFINITY : a.bias != nullptr ? fmaxf(a.bias[e], -INFINITY) : 0.0f;  // no NaN
+  const int size = a.group_size, lane_bits = a.n_group > 1 ? a.group_lane_bits : LANES == 32 ? 5 : 4, lanes = 1 << lane_bits;
+  for (int i = threadIdx.x; i < LANES * C; i += THREADS) {
+    const int l = i / C, c = i % C, group = l >> lane_bits, at = (l & (lanes - 1)) * C + c, e = group * size + at;
+    const bool in = group < a.n_group && at < size;
+    sh[l * S + c] = !in ? -INFINITY : a.bias != nullptr ? fmaxf(a.bias[e], -INFINITY) : 0.0f;  // no NaN
+  }
   if (balance) {
-    for (int e = threadIdx.x; e < 16 * C; e += THREADS) counts[e] = 0;
+    for (int e = threadIdx.x; e < LANES * C; e += THREADS) counts[e] = 0;
 #pragma unroll
     for (int c = 0; c < C; ++c) my_sums[c] = 0.0f;
   }
   __syncthreads();
   // Approximate rank values s + b are off by less than 4e-7 + 2^-23 |s + b|: their order is certain from twice that on.
   if (FAST) {
-    if (part * C < E) {
 #pragma unroll
-      for (int c = 0; c < C; ++c) margin = fmaxf(margin, fabsf(bias[c]));
-    }
+    for (int c = 0; c < C; ++c)
+      if (bias[c] > -INFINITY) margin = fmaxf(margin, fabsf(bias[c]));
     margin = fmaf(5e-7f, 1.0f + warp_max(margin), 1e-6f);
   }
-  const bool part_in = part * C < E;
-  const int lanes = a.n_group > 1 ? E / a.n_group / C : 16;
-  const PairShape shape = {lanes, part / lanes, part_in, a.topk_group < a.n_group, a.group_top2 != 0};
+  const int group = part >> lane_bits, in_group = (part & (lanes - 1)) * C;
+  const int held = group < a.n_group ? max(0, min(C, size - in_group)) : 0;
+  const Place place = {lanes, group, held > 0 ? group * size + in_group : 0, held,
+                       held > 0 && (part & (lanes - a.segment_lanes)) * C + 1 < size,
+                       a.topk_group < a.n_group, a.group_top2 != 0};
   const int slot = lane >> a.slot_bits, j_of = lane & ((1 << a.slot_bits) - 1);
   const int64_t step = (int64_t)gridDim.x * WARPS * a.batch;
   int64_t base = ((int64_t)blockIdx.x * WARPS + warp) * a.batch;
@@ -426,11 +457,11 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_OF_SM) route_pairs_kernel(cons
     for (; base < a.T && slow_count + a.batch <= SLOW_TOKENS; base += step) {
       const int count = (int)min((int64_t)a.batch, a.T - base);
       unsigned passed = 0u;  // tokens of the batch that are left over
-      for (int i = 0; i < count; i += 2) {
+      for (int i = 0; i < count; i += TOKENS) {
         const bool on = i + half < count;
         const int64_t t = base + (on ? i + half : i);
         float x[C], s[C], r[C];
-        load_part<C>(logits + t * a.stride, part * C, E, a.wide, x);
+        load_part<C>(logits + t * a.stride, logits + t * a.stride + place.first, held, a.rows, x);
         float inv = 1.0f, shift = 0.0f, least = INFINITY;
 #pragma unroll
         for (int c = 0; c < C; c += 2) least = min_nan(least, x[c], x[c + 1]);
@@ -439,7 +470,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_OF_SM) route_pairs_kernel(cons
           float sum = 0.0f;
 #pragma unroll
           for (int c = 0; c < C; ++c) shift = fmaxf(shift, x[c]);
-          shift = half_max(shift);
+          shift = token_max<LANES>(shift);
           if (shift == -INFINITY) shift = 0.0f;
           const float offset = -shift * LOG2E;
 #pragma unroll
@@ -448,7 +479,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_OF_SM) route_pairs_kernel(cons
             sum += s[c];
             r[c] = x[c];
           }
-          sum = half_sum(sum);
+          sum = token_sum<LANES>(sum);
           inv = sum == 0.0f ? 0.0f : 1.0f / sum;
           if (part == 0) w.shift[i + half] = shift, w.inv[i + half] = inv;
         } else {
@@ -459,37 +490,38 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_OF_SM) route_pairs_kernel(cons
             r[c] += s[c];
           }
         }
-        if (__any_sync(ALL, part_in && !(least > -INFINITY))) {  // masked experts, or NaN
+        if (__any_sync(ALL, held > 0 && !(least > -INFINITY))) {  // masked experts, or NaN
 #pragma unroll
           for (int c = 0; c < C; ++c) r[c] = x[c] > -INFINITY ? r[c] : -INFINITY;
         }
         int* pick = w.pick + ((i + half) << a.slot_bits);
-        int result = select_pair<C, MODE == LOGITS, FAST>(a, shape, r, shift, margin, lane, mine, w, pick);
+        int result = select_pair<LANES, C, MODE == LOGITS, FAST>(a, place, r, shift, margin, lane, mine, w, pick);
         if (FAST && __any_sync(ALL, result == 1)) {  // not certain: again, with the exact scores
           __syncwarp();
           get(bias, r);
 #pragma unroll
           for (int c = 0; c < C; ++c) r[c] = x[c] > -INFINITY ? r[c] + sigmoid(x[c]) : -INFINITY;
-          result = select_pair<C, false, false>(a, shape, r, 0.0f, 0.0f, lane, mine, w, pick);
+          result = select_pair<LANES, C, false, false>(a, place, r, 0.0f, 0.0f, lane, mine, w, pick);
         }
         const unsigned skips = __ballot_sync(ALL, result == 2 && on);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if ((skips >> (16 * h)) & 0xffffu) {
+        for (int h = 0; h < TOKENS; ++h) {
+          if (skips >> (h * LANES) & 1u) {
             passed |= 1u << (i + h);
             if (lane == 0) w.slow[slow_count] = base + i + h;
             ++slow_count;
           }
         }
-        if (a.scores != nullptr && on && part_in) {
-          float* to = a.scores + t * E + part * C;
+        if (a.scores != nullptr && on && held > 0) {
+          float* to = a.scores + t * E + place.first;
 #pragma unroll
           for (int c = 0; c < C; ++c) r[c] = s[c] * inv;
           if (a.wide_scores) {
             put(to, r);
           } else {
 #pragma unroll
-            for (int c = 0; c < C; ++c) to[c] = r[c];
+            for (int c = 0; c < C; ++c)
+              if (c < held) to[c] = r[c];
           }
         }
         if (balance) {
@@ -497,8 +529,8 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_OF_SM) route_pairs_kernel(cons
           if (MODE != LOGITS) {
             float total = 0.0f;
 #pragma unroll
-            for (int c = 0; c < C; ++c) total += s[c];  // 0 beyond E
-            total = half_sum(total);
+            for (int c = 0; c < C; ++c) total += s[c];  // 0 in places without an expert
+            total = token_sum<LANES>(total);
             q = total == 0.0f ? 0.0f : 1.0f / total;
           }
           if (on) {
@@ -522,7 +554,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_OF_SM) route_pairs_kernel(cons
     for (int i = 0; i < slow_count; ++i) {
       const int64_t t = w.slow[i];
       float score = 0.0f;
-      const int e = select_by_warp<TL>(a, t, rows + warp * 32 * S, lane, &score);
+      const int e = select_by_warp<TL, LANES * C / 32>(a, t, rows + warp * 32 * S, lane, &score);
       float sum = 0.0f;
       for (int j = 0; j < k; ++j) sum += __shfl_sync(ALL, score, j);
       if (lane < k) {
@@ -538,46 +570,63 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_OF_SM) route_pairs_kernel(cons
     __syncthreads();
     finish_balance(a, counts, [&](int e) {
       float p = 0.0f;
+      const int group = (int)(((float)e + 0.5f) * a.inv_group_size), at = e - group * size;
+      const int l = (group << lane_bits) + at / C, c = at % C;
 #pragma unroll
-      for (int h = 0; h < 2 * WARPS; ++h) p += sums[h * 16 * S + e / C * S + e % C];
+      for (int h = 0; h < TOKENS * WARPS; ++h) p += sums[(h * LANES + l) * S + c];
       return p;
     });
   }
 }
 
-// Experts of a lane for which there is a kernel; 0: none.
-int lane_experts(const RouteArgs& a) {
-  const int c = (a.E + 15) / 16;
-  const int C = c <= 4 ? 4 : c <= 8 ? 8 : c <= 10 ? 10 : c <= 16 ? 16 : 0;
-  if (C == 0 || a.E % C != 0 || (a.router == 0 && a.bias != nullptr)) return 0;
-  if (a.n_group == 1) return a.E / C * 2 >= a.k ? C : 0;
-  const int size = a.E / a.n_group, lanes = size / C;
-  if (size % C != 0 || (lanes & (lanes - 1)) != 0) return 0;
-  return 2 * a.topk_group * lanes >= a.k ? C : 0;
+// How the experts lie on lanes, if there is a kernel for it (token_lanes 0: there is none).  16 lanes for a token where
+// they hold its groups, else 32.
+struct Layout {
+  int token_lanes, per_lane, group_lanes, segment_lanes;
+};
+Layout layout_of(const RouteArgs& a) {
+  if (a.E > MAX_EXPERTS || (a.router == 0 && a.bias != nullptr)) return {};
+  const int size = a.E / a.n_group;
+  for (int token_lanes = 16; token_lanes <= 32; token_lanes *= 2) {
+    for (const int C : {4, 8, 10, 12, 16}) {
+      if (token_lanes == 32 && C < 12) continue;
+      const int used = (size + C - 1) / C;
+      int group_lanes = 1;
+      while (group_lanes < used) group_lanes *= 2;
+      if (group_lanes * a.n_group > token_lanes) continue;
+      // the longest segments, of which topk_group groups hold k experts in segments of two or more
+      for (int segment = group_lanes; segment > 0; segment /= 2) {
+        const int places = segment * C, segments = size / places + (size % places >= 2);
+        if (2 * a.topk_group * segments >= a.k) return {token_lanes, C, a.n_group > 1 ? group_lanes : token_lanes, segment};
+      }
+    }
+  }
+  return {};
 }
 
-template <int C, typename TL, int MODE>
-cudaError_t launch_pairs(const RouteArgs& args, int n_sm, cudaStream_t st) {
+template <int LANES, int C, typename TL, int MODE>
+cudaError_t launch_pairs(const RouteArgs& args, const Layout& layout, int n_sm, cudaStream_t st) {
   RouteArgs a = args;
   constexpr int UNIT = unit_of<C, TL>(), S = lane_stride<C>();
-  a.wide = reinterpret_cast<uintptr_t>(a.logits) % UNIT == 0 && a.stride * (int64_t)sizeof(TL) % UNIT == 0;
+  const int size = a.E / a.n_group;
+  a.group_size = size;
+  a.inv_group_size = 1.0f / (float)size;
+  a.group_lane_bits = 0;
+  while (1 << a.group_lane_bits < layout.group_lanes) ++a.group_lane_bits;
+  a.segment_lanes = layout.segment_lanes;
+  const bool words = reinterpret_cast<uintptr_t>(a.logits) % UNIT == 0 && a.stride * (int64_t)sizeof(TL) % UNIT == 0 &&
+                     size * (int)sizeof(TL) % UNIT == 0;
+  a.rows = !words ? ELEMENTS : size % C == 0 ? ALL_OR_NONE : WORDS;
   constexpr int SCORES_UNIT = C % 4 == 0 ? 16 : 8;
-  a.wide_scores = reinterpret_cast<uintptr_t>(a.scores) % SCORES_UNIT == 0 && a.E * 4 % SCORES_UNIT == 0;
+  a.wide_scores = reinterpret_cast<uintptr_t>(a.scores) % SCORES_UNIT == 0 && a.E * 4 % SCORES_UNIT == 0 && size % C == 0;
   a.slot_bits = 0;
   while ((1 << a.slot_bits) < a.k) ++a.slot_bits;
-  // the longest segments of which topk_group groups have k / 2
-  const int lanes = a.n_group > 1 ? a.E / a.n_group / C : 16;
-  a.segment_lanes = 1;
-  const int in_group = a.n_group > 1 ? lanes : a.E / C;
-  while (2 * a.segment_lanes <= in_group && in_group % (2 * a.segment_lanes) == 0 &&
-         2 * a.topk_group * (in_group / (2 * a.segment_lanes)) >= a.k)
-    a.segment_lanes *= 2;
   // tokens whose gates are formed together: as many as fill a warp, once every resident warp has a batch
   a.batch = 32 >> a.slot_bits;
-  while (a.batch > 2 && a.T < (int64_t)a.batch * WARPS * BLOCKS_OF_SM * n_sm) a.batch >>= 1;
+  while (a.batch > 32 / LANES && a.T < (int64_t)a.batch * WARPS * BLOCKS_OF_SM * n_sm) a.batch >>= 1;
   const bool balance = a.ticket != nullptr;
-  const int smem = (16 * S + WARPS * 32 * S + (balance ? 16 * C + WARPS * 32 * S : 0)) * 4;
-  auto kernel = route_pairs_kernel<C, TL, MODE>;
+  const int smem = (LANES * S + WARPS * 32 * S + (balance ? LANES * C + WARPS * 32 * S : 0)) * 4;
+  auto kernel = route_pairs_kernel<LANES, C, TL, MODE>;
   if (smem > 32 * 1024) {
     const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
@@ -588,28 +637,32 @@ cudaError_t launch_pairs(const RouteArgs& args, int n_sm, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-template <int C, typename TL>
-cudaError_t launch_mode(const RouteArgs& a, int n_sm, cudaStream_t st) {
-  if (a.router == 0) return launch_pairs<C, TL, LOGITS>(a, n_sm, st);
+template <int LANES, int C, typename TL>
+cudaError_t launch_mode(const RouteArgs& a, const Layout& l, int n_sm, cudaStream_t st) {
+  if (a.router == 0) return launch_pairs<LANES, C, TL, LOGITS>(a, l, n_sm, st);
   // without a bias ties are common (equal logits), and the scores that are handed out are the exact ones
-  if (a.bias != nullptr && a.scores == nullptr) return launch_pairs<C, TL, SIGMOID_FAST>(a, n_sm, st);
-  return launch_pairs<C, TL, SIGMOID>(a, n_sm, st);
+  if (a.bias != nullptr && a.scores == nullptr) return launch_pairs<LANES, C, TL, SIGMOID_FAST>(a, l, n_sm, st);
+  return launch_pairs<LANES, C, TL, SIGMOID>(a, l, n_sm, st);
 }
 
 template <typename TL>
 cudaError_t launch_type(const RouteArgs& a, int n_sm, cudaStream_t st) {
-  switch (lane_experts(a)) {
-    case 4: return launch_mode<4, TL>(a, n_sm, st);
-    case 8: return launch_mode<8, TL>(a, n_sm, st);
-    case 10: return launch_mode<10, TL>(a, n_sm, st);
-    case 16: return launch_mode<16, TL>(a, n_sm, st);
+  const Layout l = layout_of(a);
+  switch (l.token_lanes * 100 + l.per_lane) {
+    case 1604: return launch_mode<16, 4, TL>(a, l, n_sm, st);
+    case 1608: return launch_mode<16, 8, TL>(a, l, n_sm, st);
+    case 1610: return launch_mode<16, 10, TL>(a, l, n_sm, st);
+    case 1612: return launch_mode<16, 12, TL>(a, l, n_sm, st);
+    case 1616: return launch_mode<16, 16, TL>(a, l, n_sm, st);
+    case 3212: return launch_mode<32, 12, TL>(a, l, n_sm, st);
+    case 3216: return launch_mode<32, 16, TL>(a, l, n_sm, st);
     default: return cudaErrorInvalidValue;
   }
 }
 
 }  // namespace
 
-bool route_pairs_fit(const RouteArgs& a) { return lane_experts(a) != 0; }
+bool route_pairs_fit(const RouteArgs& a) { return layout_of(a).token_lanes != 0; }
 
 cudaError_t launch_route_pairs(const RouteArgs& a, bool bf16, int n_sm, cudaStream_t st) {
   return bf16 ? launch_type<__nv_bfloat16>(a, n_sm, st) : launch_type<float>(a, n_sm, st);

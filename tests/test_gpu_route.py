@@ -105,24 +105,36 @@ def test_sum_of_two_ties_on_equal_rows():
     assert out["topk_idx"].cpu().tolist() == [[0, 1, 2, 3, 4, 5]] * 4
 
 
-# shapes that many tokens are routed with two to a warp (4, 8, 10 and 16 experts to a lane, groups of one to 16
-# lanes, groups in segments, all groups in play), and ones that are not (a group of part of a lane, 512 experts)
+def _many(E):
+    """Tokens from which on the kernel for many takes them."""
+    return -(-2 ** 27 // E ** 2)
+
+
+# shapes that many tokens are routed with two to a warp (4 to 16 experts to a lane, groups of one to 16 lanes, groups
+# in segments, all groups in play)
 MANY = [(64, 6, 8, 3, MAX), (64, 6, 1, 1, MAX), (60, 5, 1, 1, TOP2), (96, 8, 3, 1, TOP2), (128, 8, 4, 2, TOP2),
         (128, 16, 4, 2, MAX), (160, 6, 8, 3, MAX), (160, 3, 8, 8, TOP2), (256, 8, 8, 4, TOP2), (256, 1, 16, 2, MAX),
         (256, 12, 4, 3, TOP2), (240, 7, 15, 5, TOP2), (252, 9, 9, 4, TOP2), (512, 8, 8, 4, TOP2), (16, 4, 4, 2, TOP2)]
 
 
+# groups that do not fill their lanes, sizes that are no whole words, tokens on 32 lanes
+MANY += [(222, 8, 6, 3, TOP2), (57, 5, 3, 2, TOP2), (33, 3, 3, 1, MAX), (35, 4, 5, 2, MAX), (17, 2, 1, 1, MAX),
+         (225, 12, 1, 1, MAX), (144, 6, 1, 1, MAX), (192, 8, 8, 3, TOP2), (320, 16, 5, 3, MAX), (272, 7, 16, 6, TOP2),
+         (384, 8, 1, 1, MAX), (384, 8, 8, 4, TOP2), (500, 9, 2, 1, MAX), (511, 8, 1, 1, MAX), (512, 8, 8, 4, TOP2)]
+
+
 @pytest.mark.parametrize("shape", MANY, ids=lambda s: "E%d_k%d_G%d_kg%d_s%d" % s)
 @pytest.mark.parametrize("router,with_bias", [(SIGMOID, True), (SIGMOID, False), (SOFTMAX, False), (SOFTMAX, True)])
 def test_route_many_tokens(shape, router, with_bias):
-    """40 tokens, over and over to 2,500 and then 5,001 of them: every copy is routed as the oracle's."""
+    """40 tokens, over and over to 2,500, then 5,001 and then enough for the kernel for many: every copy is routed as
+    the oracle's."""
     E, k, G, kg, score = shape
     bias = _bias(E, 15, with_bias)
     x, x64 = _logits(40, E, 17, torch.bfloat16 if k % 2 else torch.float32, router, bias, k, G, kg, score)
     idx, _ = O.select(x64, bias, router, k, G, kg, score)
     s = O.scores(x64, router)
     gates = O.gates(s, idx, True, 2.5)
-    for T in (2500, 5001):
+    for T in (2500, 5001, _many(E) + 3):
         of = np.arange(T) % 40
         desc = mok.make_route_desc(T, E, k, router, True, route_scale=2.5, n_group=G, topk_group=kg, group_score=score,
                                    balance_coef=0.3, bias_rate=0.01)
@@ -144,12 +156,13 @@ def test_route_many_tokens(shape, router, with_bias):
         assert torch.equal(again["topk_idx"], plain["topk_idx"]) and torch.equal(again["counts"], full["counts"])
 
 
-@pytest.mark.parametrize("E,k,G,kg,score", [(256, 8, 8, 4, MAX), (64, 6, 1, 1, MAX), (160, 6, 8, 3, MAX)])
+@pytest.mark.parametrize("E,k,G,kg,score", [(256, 8, 8, 4, MAX), (64, 6, 1, 1, MAX), (160, 6, 8, 3, MAX), (222, 7, 6, 3, MAX),
+                                            (35, 4, 5, 2, MAX), (384, 8, 1, 1, MAX), (500, 9, 2, 1, MAX)])
 @pytest.mark.parametrize("router,with_bias", [(SIGMOID, False), (SIGMOID, True), (SOFTMAX, False)])
 def test_many_tokens_with_ties_and_masks(E, k, G, kg, score, router, with_bias):
     """Exact ties (with a bias of zeros too), rows of one value, masked experts and groups, rows with too few experts
     left and with none: rank values here are equal or far apart in f32 as in f64."""
-    T = 3000
+    T, times = 3000, -(-_many(E) // 3000)  # over and over
     rng = np.random.default_rng(5)
     x = rng.integers(-4, 5, (T, E)) * 0.25
     x[:3] = [[0.0], [-1.0], [2.0]]
@@ -158,8 +171,9 @@ def test_many_tokens_with_ties_and_masks(E, k, G, kg, score, router, with_bias):
     x[900:950] = np.where(np.isin(np.arange(E), (3, E - 2)), x[900:950], -np.inf)
     x[950:1000] = -np.inf
     bias = np.zeros(E, np.float32) if with_bias else None
-    out = mok.Router(mok.make_route_desc(T, E, k, router, True, n_group=G, topk_group=kg, group_score=score)).forward(
-        torch.tensor(x).float().cuda(), _cuda(bias))
+    desc = mok.make_route_desc(T * times, E, k, router, True, n_group=G, topk_group=kg, group_score=score)
+    out = mok.Router(desc).forward(torch.tensor(x).float().cuda().repeat(times, 1), _cuda(bias))
+    out = {n: t[-T:] for n, t in out.items()}
     got = out["topk_idx"].cpu().numpy()
     want, _ = O.select(x, bias, router, k, G, kg, score)
     assert np.array_equal(got, want)
@@ -239,9 +253,10 @@ def test_nan_logits_rank_last():
         assert torch.allclose(again["prob_sum"], torch.full((24,), 16 / 24).cuda(), rtol=1e-6)
 
 
-def test_nan_logits_among_many_tokens():
+@pytest.mark.parametrize("T,E", [(2500, 64), (40000, 64), (2500, 256), (1500, 384)])
+def test_nan_logits_among_many_tokens(T, E):
     """As above where two tokens share a warp; the other tokens are routed as without the NaN."""
-    T, E, k = 2500, 64, 4
+    k = 4
     x = torch.randn(T, E, generator=torch.Generator().manual_seed(1)).cuda()
     y = x.clone()
     y[7, 3] = float("nan")
@@ -336,7 +351,7 @@ def test_route_backward(shape, router, use):
 
 
 @pytest.mark.parametrize("router", [SIGMOID, SOFTMAX])
-@pytest.mark.parametrize("E", [24, 300])
+@pytest.mark.parametrize("E", [24, 300, 600])
 def test_backward_against_differences_of_the_forward(router, E):
     """Central differences of f = sum dgates * gates + sum dprob * prob_sum, of the forward kernel's scores and sums.  The step
     is 2^-5: f in f32 (a sum of about 30 terms near 1 in f64, each off by 2^-21) is off by 30 * 2^-21, over twice the
@@ -389,9 +404,10 @@ def test_no_tokens():
     assert r.backward(x, torch.empty(0, 2, dtype=torch.int32).cuda(), torch.empty(0, 2).cuda()).shape == (0, 16)
 
 
-def test_rows_past_32_bit_offsets():
+@pytest.mark.parametrize("T,E", [(2 ** 21 + 3, 1024), (2 ** 23 + 3, 256)])
+def test_rows_past_32_bit_offsets(T, E):
     """More than 2^31 logits: the last tokens are routed, and their gradients written, as on their own."""
-    T, E, k, tail = 2 ** 21 + 3, 1024, 4, 100
+    k, tail = 4, 100
     x = torch.zeros(T, E, dtype=torch.bfloat16, device="cuda")
     x[-tail:] = torch.randn(tail, E, generator=torch.Generator().manual_seed(0)).bfloat16().cuda()
     x[-2 * tail:-tail] = x[-tail:]
@@ -490,19 +506,21 @@ def test_layer_routes_within_groups(router, score, mxfp8):
     assert torch.allclose(dl, layer.view("dlogits"), rtol=1e-4, atol=1e-6 * layer.view("dlogits").abs().max().item())
 
 
-def test_layer_with_groups_and_many_tokens():
-    """From 2,048 tokens on the layer's selection is the many-token kernel's, with the scores it hands out."""
-    shape = GROUPED.scaled(T=2100)
+@pytest.mark.parametrize("E", [32, 256])
+def test_layer_with_groups_and_many_tokens(E):
+    """With 256 experts, from 2,048 tokens on, the layer's selection is the many-token kernel's, with the scores it
+    hands out."""
+    shape = GROUPED.scaled(T=2100, E=E)
     inp = {n: t.cuda() for n, t in W.make_inputs(shape, seed=3).items() if t is not None}
-    bias = _cuda(_bias(32, 4, True))
+    bias = _cuda(_bias(E, 4, True))
     layer = mok.MoELayer(mok.desc_from_shape(shape, n_group=8, topk_group=3, group_score=TOP2))
     layer.forward(inp["x"], inp["w_router"], inp["w13"], inp["w2"], router_bias=bias)
     assert layer.status() == (0, 0)
     logits = layer.view("logits")
-    out = mok.Router(mok.make_route_desc(2100, 32, 4, SIGMOID, True, n_group=8, topk_group=3), scores=True).forward(logits, bias)
+    out = mok.Router(mok.make_route_desc(2100, E, 4, SIGMOID, True, n_group=8, topk_group=3), scores=True).forward(logits, bias)
     for n in ("topk_idx", "gates", "scores"):
         assert torch.equal(out[n], layer.view(n)), n
-    first = mok.Router(mok.make_route_desc(100, 32, 4, SIGMOID, True, n_group=8, topk_group=3), scores=True).forward(logits[:100], bias)
+    first = mok.Router(mok.make_route_desc(100, E, 4, SIGMOID, True, n_group=8, topk_group=3), scores=True).forward(logits[:100], bias)
     for n in ("topk_idx", "gates", "scores"):
         assert torch.equal(first[n], out[n][:100]), n
 
