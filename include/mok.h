@@ -394,8 +394,9 @@ typedef struct {
  *              mok_route_backward
  *   bias_next  f32 [E]: bias + bias_rate * sign(T k / E - counts), may be bias itself
  * The five from counts on need ws: at least MOK_ROUTE_WS_BYTES, 256-byte aligned, zero-filled once
- * before its first use (each call leaves it ready for the next); otherwise ws may be NULL.  With
- * them T stays below 2^31.  A logit that makes a token's scores NaN makes prob_sum and loss NaN. */
+ * before its first use (each call leaves it ready for the next; calls that may overlap need one
+ * each); otherwise ws may be NULL.  With them T stays below 2^31.  A logit that makes a token's
+ * scores NaN makes prob_sum and loss NaN. */
 #define MOK_ROUTE_WS_BYTES 98560
 mok_status mok_route(const mok_route_desc* desc, const void* logits, const float* bias, int32_t* topk_idx,
                      float* gates, float* scores, int32_t* counts, float* prob_sum, float* loss, float* dprob,
@@ -427,9 +428,9 @@ typedef struct {
 /* out[0] = the 2-norm of all gradients together, out[1] = min(1, max_norm / (out[0] + 1e-6)), the
  * factor that clips them to max_norm (> 0, may be infinite), or NaN where the norm is not finite.
  * out is f32 [2] on the device.  ws: at least MOK_GRAD_NORM_WS_BYTES, 16-byte aligned, zero-filled
- * once before its first use (each call leaves it ready for the next).  The
- * squares are formed and added in f32, a block's sums in f64, in a fixed order; a gradient above
- * 1.8e19 in magnitude makes the norm infinite. */
+ * once before its first use (each call leaves it ready for the next; calls that may overlap need one
+ * each).  The squares are formed and added in f32, the blocks' sums in f64, in a fixed order; a
+ * gradient above 1.8e19 in magnitude makes the norm infinite. */
 #define MOK_GRAD_NORM_WS_BYTES 16640
 mok_status mok_grad_norm(const mok_grad_tensor* tensors, int32_t count, float max_norm, float* out, void* ws,
                          size_t ws_bytes, void* stream);
@@ -444,8 +445,10 @@ mok_status mok_grad_norm(const mok_grad_tensor* tensors, int32_t count, float ma
  *               MOK_STATE_MX8: m and v are E4M3 [n] holding m and sqrt(v) in blocks of 32 elements,
  *               m_scale and v_scale [ceil(n / 32)] E8M0 bytes b standing for 2^(b - 127): the OCP
  *               Microscaling layout the layer's MXFP8 operands have.  Elements are rounded at random,
- *               with the mean unchanged; a nonzero sqrt(v) never becomes zero.  All-zero states are
- *               zero bytes (scale bytes of any value).
+ *               with the mean unchanged; a nonzero sqrt(v) never becomes zero.  v below 2^-126
+ *               counts as 0.  Scale bytes are written from 1 to 254; a block under byte 0 reads as
+ *               zeros, one under byte 255 (the format's NaN) as not finite.  All-zero states: zero
+ *               elements with scale bytes 0 to 254.
  *   counter  multiple of 8: element i takes the rounding bits of number counter + i.  Tensors whose
  *            ranges [counter, counter + n) do not overlap are rounded independently
  * Pointers are aligned to their element; 16-byte aligned ones are accessed in 16 bytes. */
@@ -478,7 +481,9 @@ typedef struct {
  *   g' = c * grad, c = *grad_scale (f32 on the device, NULL = 1), e.g. out + 1 of mok_grad_norm
  *   m = beta1 m + (1 - beta1) g';  v = beta2 v + (1 - beta2) g'^2
  *   param -= lr * ((m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps) + weight_decay * param)
- * in f32.  Where c is NaN nothing is changed. */
+ * in f32.  Where c is NaN nothing is changed (the host does not see it: a caller that counts on has
+ * skipped that number).  The step's number and rates are in the launch: a captured graph repeats them
+ * and the rounding bits at each replay. */
 mok_status mok_adamw_step(const mok_adamw_tensor* tensors, int32_t count, const mok_adamw_hyper* hyper,
                           const float* grad_scale, void* stream);
 

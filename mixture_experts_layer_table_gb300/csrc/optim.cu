@@ -234,9 +234,13 @@ __device__ __forceinline__ void store_e4m3(uint8_t* q, uint32_t i, int left, con
 // A clip factor c that is NaN leaves the tensor as it is (grad_norm gives one for gradients that are not finite).
 //
 // 8 consecutive elements to a thread (16 bytes of bf16, 32 of f32; four threads hold a block of 32), 2048 to a
-// pass of the block.  With f32 states the step is bound by DRAM and keeps IEEE roots and divisions; with 8-bit
-// states it moves 10 to 18 bytes an element and issue decides, so it runs on packed f32 pairs with approximate
-// roots and reciprocals (2^-22) and rounds without conversions to and from integers.
+// pass of the block.  With f32 states the step is bound by DRAM and keeps IEEE roots and divisions: bf16 parameters
+// with masters and f32 gradients, 30 bytes an element, 354 million elements in 1.48 ms, 7.16 TB/s, issue slots 28%
+// full; 96 tensors of 1 to 30,011 elements (8 MB, from L2) 5.5 us.  With 8-bit states it moves 10 to 18 bytes an
+// element and issue decides (plain f32: 92 instructions an element, 0.98 ms for those 354 million elements at 10.1
+// bytes), so it runs on packed f32 pairs with approximate roots and reciprocals (2^-22; v below 2^-126 counts as 0)
+// and rounds without conversions to and from integers: 52 instructions an element, 81% of the issue slots, 0.573 ms,
+// 6.25 TB/s; with masters or f32 gradients 6.9 to 7.0 TB/s.
 struct AdamConstants {
   float c, beta1, one_minus_beta1, beta2, one_minus_beta2, eps, inv_bc1, inv_bc2_sqrt, lr, weight_decay;
   uint32_t seed;
@@ -280,7 +284,6 @@ __device__ __forceinline__ void store_param(const AdamTensor& T, uint32_t i, int
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
       if constexpr (PK == PARAM_BF16) b[j] = __float_as_uint(p[j]) + (z[j] & 0xffffu);
-
       else b[j] = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(p[j])) << 16;
     }
     store8<WIDE>(static_cast<__nv_bfloat16*>(T.param), i, left, b);
@@ -521,7 +524,9 @@ __global__ void __launch_bounds__(MX8_THREADS, 4)
 // ----------------------------------------------------------------------------- gradient norm
 // Each block sums its chunks' squares in f32, 8 sums to a thread and a tree over the threads; one warp of the
 // block that comes last in the call adds the blocks' sums in f64 in a fixed order, so that the result does not
-// depend on the order of arrival.
+// depend on the order of arrival.  Bound by DRAM reads: 354 million f32 gradients in 0.198 ms, 7.15 TB/s (64 warps an
+// SM in flight, no copy through shared memory); small sets by the launch and the last block's turn: 96 tensors of 1
+// to 30,011 elements 5.5 us (with f64 sums within the blocks 8.6).
 __device__ __forceinline__ float warp_total(float x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -624,7 +629,7 @@ cudaError_t launch_mx8(const AdamTensor* tensors, int count, const AdamHyper& h,
   // further apart at one time: 32 passes were up to 6% slower than 8, 4 passes 3% slower with bf16 gradients)
   int64_t total = 0;
   for (int i = 0; i < count; ++i) total += (tensors[i].n + MX8_PASS - 1) / MX8_PASS;
-    const int passes = (int)std::min<int64_t>(MX8_MAX_PASSES, std::max<int64_t>(1, total / (12 * n_sm)));
+  const int passes = (int)std::min<int64_t>(MX8_MAX_PASSES, std::max<int64_t>(1, total / (12 * n_sm)));
   const int64_t chunk = (int64_t)passes * MX8_PASS;
   Table<AdamTensor, CAP> tab;
   const int64_t chunks = fill_table(tab, tensors, count, [chunk](int64_t n) { return (n + chunk - 1) / chunk; });

@@ -204,7 +204,9 @@ class AdamW:
 
     def step(self, grad_scale: Optional[torch.Tensor] = None, stream=None):
         """One step on what the gradient buffers hold; ``grad_scale``: float32 [1] CUDA tensor, the
-        factor on every gradient (a NaN skips the update)."""
+        factor on every gradient (a NaN skips the update; the step is counted all the same, since the
+        host does not wait for the factor).  A captured graph repeats the step it was captured at,
+        with its number, rates and rounding bits."""
         scale = None
         if grad_scale is not None:
             if not (grad_scale.dtype is torch.float32 and grad_scale.is_cuda and grad_scale.numel() == 1):
