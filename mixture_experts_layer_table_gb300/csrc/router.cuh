@@ -24,11 +24,10 @@ struct RouteArgs {
   float dprob_unit;        // dprob[e] = dprob_unit * counts[e]
   float bias_rate;
   int sum_shift;           // probabilities are summed in units of 2^-sum_shift
-  // set by the launcher: how rows are read; scores can be written in words of 8 or 16 bytes; tokens whose gates are
+  // set by the launcher: rows can be read, scores can be written in words of 8 or 16 bytes; tokens whose gates are
   // formed together; log2 of the next power of two of k; experts of a group and their inverse, log2 of its lanes;
   // lanes of a segment
-  int rows;
-  bool wide_scores;
+  bool words, wide_scores;
   int batch, slot_bits, group_size, group_lane_bits, segment_lanes;
   float inv_group_size;
   unsigned* ticket;        // workspace: zero between calls

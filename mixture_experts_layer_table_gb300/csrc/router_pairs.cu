@@ -15,11 +15,16 @@
 // A token for which this does not do (more than 64 experts listed, too few unmasked) is selected by the whole warp, one
 // expert at a time, by the definition.
 //
-// 65,536 tokens of 256 experts (f32, sigmoid with a bias, 8 groups): 38 us, 1.8 TB/s; the row is read once, and the
-// bound is instructions (26.5 million of warps, issued in 62% of the cycles at 24 warps an SM, which wait on one
-// another's results: shared memory and shuffles between the steps).  4,096 tokens 7.3 us, with the balance outputs 10.
-// Of the instructions 30% place the listed experts, 27% load and score, 13% choose groups, 12% list, the rest merge
-// and form gates.
+// The next tokens' logits come to shared memory under the arithmetic of these (cp.async; 39 us below without).
+//
+// A biased sigmoid is ranked on approximate values, and what those leave open is settled exactly where it arises: on
+// the listed experts if it is an order among them, from the groups on if it is a group (in the whole warp's way, as
+// at first, the code of 10 such tokens in 65,536, cold, was 10 us of a call's 38: a single warp's at the end).
+//
+// 65,536 tokens of 256 experts (f32, sigmoid with a bias, 8 groups): 37 us, 1.9 TB/s; the row is read once, and the
+// bound is instructions (25 million of warps, issued in 62% of the cycles at 24 warps an SM, which wait on one
+// another's results: shared memory and shuffles between the steps; the SMs' ends lie 15% apart).  4,096 tokens 6 us,
+// with the balance outputs 9.4.
 #include <algorithm>
 #include <cstddef>
 
@@ -32,15 +37,15 @@ namespace {
 constexpr int WARPS = 8;
 constexpr int THREADS = 32 * WARPS;
 constexpr int MAX_EXPERTS = 512;  // 32 lanes of at most 16
-// 72 to 80 registers; 4 blocks (64 registers) took 46 us at 65,536 tokens of 256 experts instead of 42, 2 45
-constexpr int BLOCKS_OF_SM = 3;
 
 // How rank values are formed.  LOGITS: softmax without a bias, ranked by the logits.  FAST: a biased sigmoid by the
 // hardware's exponential and reciprocal, 4 instructions instead of about 18, with a check that the order is certain.
 enum PairMode { LOGITS = 0, SIGMOID = 1, SIGMOID_FAST = 2 };
 
-// 1 / (1 + e^-x), off by less than 4e-7
-__device__ __forceinline__ float sigmoid_fast(float x) { return inverse_fast(1.0f + exp2_fast(x * -LOG2E)); }
+// The logits' mode does with 64 registers (12,345 tokens of 160 experts: 4 blocks 11.3 us, 3 12.1), the others with 80
+// (65,536 tokens of 256 experts: 3 blocks 37 us, 4 41; more and smaller blocks 38.5 to 41; a grid of twice as many,
+// for SMs that are done first, 40).
+constexpr int blocks_of_sm(PairMode mode) { return mode == LOGITS ? 4 : 3; }
 
 // One token by the definition, by the whole warp: lane j < k returns the j-th best expert, its score in *score.
 // `row` [E] is overwritten with the rank values; lane l holds those of the experts l, l + 32, ... (HELD of them).
@@ -120,13 +125,13 @@ __device__ __noinline__ int select_by_warp(const RouteArgs& a, int64_t t, float*
   return my_e;
 }
 
-constexpr int SLOW_TOKENS = 32;
+constexpr int SM_SHARED = 228 * 1024, BLOCK_RESERVED = 1024 + 256;  // shared memory of an SM; of a block, beside ours
+constexpr int SLOW_TOKENS = 32;  // at least a batch
 constexpr int LIST = 64;
 // A warp's shared memory, but for its rank values and sums.
 struct __align__(16) Scratch {
   float value[2][LIST];      // rank values of the two tokens' listed experts, -inf behind them (read four at a time)
-  int expert[2][LIST];
-  float sorted[2][20];        // the best k and the next
+  uint16_t expert[2][LIST];
   int pick[32];               // selected experts of the tokens of a batch
   float shift[32], inv[32];   // of the softmax of each
   int64_t slow[SLOW_TOKENS];  // tokens left over
@@ -146,52 +151,55 @@ constexpr int lane_stride() {
   return C == 8 || C == 16 ? C + 4 : C;
 }
 
-// A lane's experts of a row, `held` of its C places from row on; -inf behind them.  WORDS: words of UNIT bytes can be
-// read, and none is held in part; ALL_OR_NONE: held is C or 0 in every lane.
-enum Rows { ALL_OR_NONE = 0, WORDS = 1, ELEMENTS = 2 };
+// Bytes from one lane's logits to the next lane's in shared memory, with the same effect.
 template <int C, typename TL>
-__device__ __forceinline__ void load_part(const TL* row, const TL* from, int held, int how, float (&x)[C]) {
+constexpr int slot_bytes() {
+  return sizeof(TL) == 4 ? lane_stride<C>() * 4 : C == 16 ? 48 : C * 2;
+}
+// A lane's copies of its experts' logits, `held` of C places, to shared memory (cp.async) and the reading of them.
+template <int C, typename TL>
+__device__ __forceinline__ void copy_part(uint32_t to, const TL* from, int held) {
   constexpr int BYTES = C * (int)sizeof(TL), UNIT = unit_of<C, TL>(), OF_UNIT = UNIT / (int)sizeof(TL);
-  if (how != ELEMENTS) {
-    uint32_t w[BYTES / 4];
-    auto load = [&](const TL* p, int j) {
-      if constexpr (UNIT == 16) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + j);
-        w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
-      } else if constexpr (UNIT == 8) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p) + j);
-        w[2 * j] = v.x, w[2 * j + 1] = v.y;
-      } else {
-        w[j] = __ldg(reinterpret_cast<const uint32_t*>(p) + j);
-      }
-    };
-    if (how == ALL_OR_NONE) {
-      const TL* p = held > 0 ? from : row;
 #pragma unroll
-      for (int j = 0; j < BYTES / UNIT; ++j) load(p, j);
+  for (int j = 0; j < BYTES / UNIT; ++j) {
+    if (j * OF_UNIT < held) {
+      if constexpr (UNIT == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + j * UNIT), "l"(from + j * OF_UNIT) : "memory");
+      else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to + j * UNIT), "l"(from + j * OF_UNIT), "n"(UNIT)
+                     : "memory");
+    }
+  }
+}
+template <int C, typename TL>
+__device__ __forceinline__ void read_part(const unsigned char* slot, float (&x)[C]) {
+  constexpr int BYTES = C * (int)sizeof(TL), UNIT = unit_of<C, TL>();
+  uint32_t w[BYTES / 4];
+#pragma unroll
+  for (int j = 0; j < BYTES / UNIT; ++j) {
+    if constexpr (UNIT == 16) {
+      const uint4 v = reinterpret_cast<const uint4*>(slot)[j];
+      w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
+    } else if constexpr (UNIT == 8) {
+      const uint2 v = reinterpret_cast<const uint2*>(slot)[j];
+      w[2 * j] = v.x, w[2 * j + 1] = v.y;
     } else {
-      constexpr uint32_t NOTHING = sizeof(TL) == 4 ? 0xff800000u : 0xff80ff80u;
-#pragma unroll
-      for (int j = 0; j < BYTES / 4; ++j) w[j] = NOTHING;
-#pragma unroll
-      for (int j = 0; j < BYTES / UNIT; ++j)
-        if (j * OF_UNIT < held) load(from, j);
+      w[j] = reinterpret_cast<const uint32_t*>(slot)[j];
     }
+  }
 #pragma unroll
-    for (int j = 0; j < BYTES / 4; ++j) {
-      if constexpr (sizeof(TL) == 4) x[j] = __uint_as_float(w[j]);
-      else x[2 * j] = __uint_as_float(w[j] << 16), x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-    }
-    if (how == ALL_OR_NONE && held == 0) {
+  for (int j = 0; j < BYTES / 4; ++j) {
+    if constexpr (sizeof(TL) == 4) x[j] = __uint_as_float(w[j]);
+    else x[2 * j] = __uint_as_float(w[j] << 16), x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+  }
+}
+// The same from global memory, one at a time; -inf behind them.
+template <int C, typename TL>
+__device__ __forceinline__ void load_part(const TL* from, int held, float (&x)[C]) {
 #pragma unroll
-      for (int c = 0; c < C; ++c) x[c] = -INFINITY;
-    }
-  } else {
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      x[c] = -INFINITY;
-      if (c < held) x[c] = to_f32(from[c]);
-    }
+  for (int c = 0; c < C; ++c) {
+    x[c] = -INFINITY;
+    if (c < held) x[c] = to_f32(from[c]);
   }
 }
 
@@ -229,6 +237,36 @@ __device__ __forceinline__ float min_nan(float a, float b, float c) {  // NaN if
   return r;
 }
 
+// Two f32 in a register pair: one instruction for both.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void split(F2 x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// bits with x's sign behind them
+__device__ __forceinline__ uint32_t push_sign(uint32_t bits, float x) {
+  return __funnelshift_l(__float_as_uint(x), bits, 1);
+}
+
 // The two largest of N values, none of them NaN.
 template <int N>
 __device__ __forceinline__ void two_largest(const float (&v)[N], float& first, float& second) {
@@ -263,7 +301,7 @@ __device__ __forceinline__ float token_sum(float x) {
 // Writes the selected expert e of token t (`on`: this lane has one) and its gate, as the layer's ungrouped top-k
 // forms it: the sum over the token's lanes, from `first` on, in the order of the selection (a lane without an expert
 // adds 0).
-template <typename TL, int MODE>
+template <typename TL, PairMode MODE>
 __device__ __forceinline__ void store_selected(const RouteArgs& a, int64_t t, bool on, int j_of, int first, int e,
                                                float shift, float inv, int* counts) {
   float sel = 0.0f;
@@ -298,46 +336,69 @@ struct Place {
 };
 
 // The selection of a warp's tokens, one on each LANES lanes, from the lanes' rank values r (shift: of each softmax):
-// the experts in pick.  Returns (on all lanes of a token): 0 done; 1 not certain, with approximate values (FAST: off
-// by less than margin / 2); 2 more than the list holds, or too few experts.
-template <int LANES, int C, bool LOGIT_VALUES, bool FAST>
-__device__ __forceinline__ int select_pair(const RouteArgs& a, const Place& p, const float (&r)[C], float shift,
-                                           float margin, int lane, float* mine, Scratch& w, int* pick) {
+// the experts in pick.  FAST: r is off by less than margin / 2; what that leaves open is settled on exact values,
+// of the token's logits `own` from this lane's first on and their bias.  False (on all lanes of a token): more than the
+// list holds, or too few experts.
+template <int LANES, int C, bool LOGIT_VALUES, bool FAST, typename TL>
+__device__ __forceinline__ bool select_pair(const RouteArgs& a, const Place& p, const TL* own, const float* bias,
+                                            float (&r)[C], float shift, float margin, int lane, float* mine, Scratch& w,
+                                            int* pick) {
   const int half = lane / LANES, part = lane % LANES;
-  put(mine, r);
-  // 1. the two largest of the lane, of its segment and of its group
-  float m1, m2;
-  two_largest(r, m1, m2);
-  float low = m2;  // the segment's second largest
+  if (part < 16) w.value[half][part] = -INFINITY;
+  if (FAST && part < a.k) pick[part] = -1;
+  bool in_play = p.held > 0;
+  float low;  // the segment's second largest
+  for (bool exact = !FAST;; exact = true) {
+    put(mine, r);
+    // 1. the two largest of the lane, of its segment and of its group
+    float m1, m2;
+    two_largest(r, m1, m2);
+    low = m2;
 #pragma unroll
-  for (int o = 1; o < LANES; o <<= 1) {
-    if (o < p.lanes) {
-      merge_top2(m1, m2, __shfl_xor_sync(ALL, m1, o), __shfl_xor_sync(ALL, m2, o));
-      if (o < a.segment_lanes) low = m2;
+    for (int o = 1; o < LANES; o <<= 1) {
+      if (o < p.lanes) {
+        merge_top2(m1, m2, __shfl_xor_sync(ALL, m1, o), __shfl_xor_sync(ALL, m2, o));
+        if (o < a.segment_lanes) low = m2;
+      }
     }
-  }
-  // 2. the groups
-  bool in_play = p.held > 0, unsure = false;
-  if (p.choose) {
+    if (!p.choose) break;
+    // 2. the groups.  Each lane of a group counts the better ones among every lanes-th group
     float value = m1;
     if (p.top2) {
       if (LOGIT_VALUES) value = m1 > -INFINITY ? expf(m1 - shift) + expf(m2 - shift) : m1;
       else value = m2 > -INFINITY ? m1 + m2 : m1;
     }
-    const float reach = FAST ? value - fmaf(1e-6f, fabsf(value), 2e-6f) : 0.0f;
-    int better = 0, near = 0;
-#pragma unroll 4
-    for (int h = 0; h < a.n_group; ++h) {
-      const float o = __shfl_sync(ALL, value, half * LANES + h * p.lanes);
-      if (FAST) {
-        better += o > value;
-        near += o > reach;  // itself among them
-      } else {
-        better += h < p.group ? o >= value : o > value;
+    const int first = part & (p.lanes - 1);
+    auto count = [&](auto better) {
+      int n = 0;
+#pragma unroll 2
+      for (int h = first; h - first < a.n_group; h += p.lanes) {
+        const float o = __shfl_sync(ALL, value, half * LANES + h * p.lanes);
+        n += h < a.n_group && better(h, o);
       }
+#pragma unroll
+      for (int o = 1; o < LANES; o <<= 1)
+        if (o < p.lanes) n += __shfl_xor_sync(ALL, n, o);
+      return n;
+    };
+    if (exact) {
+      const int better = count([&](int h, float o) { return h < p.group ? o >= value : o > value; });
+      in_play = p.held > 0 && better < a.topk_group;
+      break;
     }
-    in_play = p.held > 0 && better < a.topk_group;
-    if (FAST) unsure = in_play && near > better + 1;
+    // those that might be better, itself among them: up to topk_group of these, and it is chosen for certain
+    const float reach = value - fmaf(1e-6f, fabsf(value), 2e-6f);
+    const int near = count([&](int, float o) { return o > reach; });
+    in_play = near <= a.topk_group && value > -INFINITY;
+    const unsigned chosen = __ballot_sync(ALL, in_play) >> (half * LANES) & (ALL >> (32 - LANES));
+    if (!__any_sync(ALL, __popc(chosen) != a.topk_group * p.lanes)) break;
+    __syncwarp();
+#pragma unroll 1
+    for (int c = 0; c < C; ++c) {
+      const float x = c < p.held ? to_f32(own[c]) : -INFINITY;
+      mine[c] = x > -INFINITY ? sigmoid(x) + bias[c] : -INFINITY;
+    }
+    get(mine, r);
   }
   // 3. the listed experts, in their order
   float bound = token_min<LANES>(in_play && p.bounds ? low : INFINITY);
@@ -346,8 +407,8 @@ __device__ __forceinline__ int select_pair(const RouteArgs& a, const Place& p, c
   unsigned listed = 0u;
 #pragma unroll
   for (int c = 0; c < C; ++c) listed |= r[c] >= bound ? 1u << c : 0u;
-  const int own = __popc(listed);
-  int before = own;
+  const int of_lane = __popc(listed);
+  int before = of_lane;
 #pragma unroll
   for (int o = 1; o < LANES; o <<= 1) {
     const int v = __shfl_up_sync(ALL, before, o, LANES);
@@ -356,7 +417,8 @@ __device__ __forceinline__ int select_pair(const RouteArgs& a, const Place& p, c
   int n = __shfl_sync(ALL, before, lane | (LANES - 1));
   const bool out = none || n > LIST || n < a.k;  // the same on the token's lanes
   if (out) n = 0, listed = 0u;
-  before -= own;
+  before -= of_lane;
+  __syncwarp();  // behind the first values and picks
   while (listed != 0u) {
     const int c = __ffs(listed) - 1;
     listed &= listed - 1u;
@@ -365,48 +427,62 @@ __device__ __forceinline__ int select_pair(const RouteArgs& a, const Place& p, c
   }
   // 4. their places, 16 against 16; -inf behind the list, as far as the longer of the two lists is read
   const int longest = LANES == 32 ? n : max(n, __shfl_xor_sync(ALL, n, 16));
-  for (int at = part; at - part < longest; at += LANES)
-    if (at >= n) w.value[half][at] = -INFINITY;
-  if (FAST) {
-    if (part <= 16) w.sorted[half][part] = part == n ? -INFINITY : INFINITY;
-    if (LANES == 16 && part == 0) w.sorted[half][16] = n == 16 ? -INFINITY : INFINITY;
+  if (longest > 16) {
+    for (int at = 16 + part; at - part < longest; at += LANES)
+      if (at >= n && at < LIST) w.value[half][at] = -INFINITY;
   }
   __syncwarp();
+  if (FAST) {
+    for (int at = part; at - part < longest; at += LANES) {  // how many might be better, itself among them
+      const float v = w.value[half][at] - margin;
+      const F2 reach = f2(v, v);
+      int better = -1;
+      for (int block = 0; block < longest; block += 16) {
+        uint32_t signs = 0u;
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+          const float4 o = *reinterpret_cast<const float4*>(&w.value[half][block + j]);
+          float d0, d1, d2, d3;
+          split(fma2(f2(o.x, o.y), f2(-1.0f, -1.0f), reach), d0, d1);
+          split(fma2(f2(o.z, o.w), f2(-1.0f, -1.0f), reach), d2, d3);
+          signs = push_sign(push_sign(push_sign(push_sign(signs, d0), d1), d2), d3);
+        }
+        better += __popc(signs);
+      }
+      if (at < n && better < a.k) pick[better] = w.expert[half][at];
+    }
+    // Where each of the best k is at least the margin above the next, it has its place; else the first that is not
+    // leaves its own empty, and the places are counted again on the exact values.
+    __syncwarp();
+    if (!__any_sync(ALL, n > 0 && part < a.k && pick[part] < 0)) return !out;
+    for (int at = part; at < n; at += LANES) {
+      const int e = w.expert[half][at];
+      w.value[half][at] = sigmoid(to_f32(own[e - p.first])) + fmaxf(a.bias[e], -INFINITY);
+    }
+    __syncwarp();
+  }
   for (int at = part; at - part < longest; at += LANES) {
     const float v = w.value[half][at];
     int better = 0;
     for (int block = 0; block < longest; block += 16) {
 #pragma unroll
-      for (int j = 0; j < 16; j += 4) {
+      for (int j = 0; j < 16; j += 4) {  // ties to the expert before
         const float4 o = *reinterpret_cast<const float4*>(&w.value[half][block + j]);
-        if (FAST) {
-          better += o.x > v;
-          better += o.y > v;
-          better += o.z > v;
-          better += o.w > v;
-        } else {  // ties to the expert before
-          better += at > block + j ? o.x >= v : o.x > v;
-          better += at > block + j + 1 ? o.y >= v : o.y > v;
-          better += at > block + j + 2 ? o.z >= v : o.z > v;
-          better += at > block + j + 3 ? o.w >= v : o.w > v;
-        }
+        better += at > block + j ? o.x >= v : o.x > v;
+        better += at > block + j + 1 ? o.y >= v : o.y > v;
+        better += at > block + j + 2 ? o.z >= v : o.z > v;
+        better += at > block + j + 3 ? o.w >= v : o.w > v;
       }
     }
-    if (FAST && at < n && better <= a.k) w.sorted[half][better] = v;
     if (at < n && better < a.k) pick[better] = w.expert[half][at];
   }
-  if (FAST) {
-    // each of the best k is at least the margin above the next (equal values leave a place at infinity)
-    __syncwarp();
-    unsure = unsure || (part < a.k && !(w.sorted[half][part] - w.sorted[half][part + 1] >= margin));
-  }
-  const unsigned doubts = FAST ? __ballot_sync(ALL, unsure) : 0u;
-  return out ? 2 : doubts >> (half * LANES) & (ALL >> (32 - LANES)) ? 1 : 0;
+  return !out;
 }
 
-template <int LANES, int C, typename TL, int MODE>
-__global__ void __launch_bounds__(THREADS, BLOCKS_OF_SM) route_pairs_kernel(const RouteArgs a) {
-  // [LANES] lanes' bias, [WARPS][32] lanes' rank values; balance: [LANES C] counts, [WARPS][32] lanes' sums
+template <int LANES, int C, typename TL, PairMode MODE>
+__global__ void __launch_bounds__(THREADS, blocks_of_sm(MODE)) route_pairs_kernel(const RouteArgs a) {
+  // [LANES] lanes' bias, [WARPS][32] lanes' rank values, [WARPS][32] lanes' logits; balance: [LANES C] counts,
+  // [WARPS][32] lanes' sums
   extern __shared__ __align__(16) float sh[];
   constexpr int S = lane_stride<C>();
   __shared__ Scratch scratch[WARPS];
@@ -416,8 +492,10 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_OF_SM) route_pairs_kernel(cons
   const int E = a.E, k = a.k;
   const bool balance = a.ticket != nullptr;
   float* rows = sh + LANES * S;
-  int* counts = balance ? reinterpret_cast<int*>(rows + WARPS * 32 * S) : nullptr;
-  float* sums = rows + WARPS * 32 * S + LANES * C;
+  constexpr int SLOT = slot_bytes<C, TL>();
+  unsigned char* slots = reinterpret_cast<unsigned char*>(rows + WARPS * 32 * S);
+  int* counts = balance ? reinterpret_cast<int*>(slots + WARPS * 32 * SLOT) : nullptr;
+  float* sums = reinterpret_cast<float*>(slots + WARPS * 32 * SLOT) + LANES * C;
   Scratch& w = scratch[warp];
   float* mine = rows + (warp * 32 + lane) * S;
   float* my_sums = sums + (warp * 32 + lane) * S;
@@ -452,6 +530,17 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_OF_SM) route_pairs_kernel(cons
   int64_t base = ((int64_t)blockIdx.x * WARPS + warp) * a.batch;
   const TL* logits = static_cast<const TL*>(a.logits);
 
+  // The logits of the next tokens come under the arithmetic of these; a lane's own copies, so that there is no barrier.
+  unsigned char* my_slot = slots + (warp * 32 + lane) * SLOT;
+  const bool copied = a.words;
+  auto fetch = [&](int64_t first) {
+    if (copied && first < a.T)
+      copy_part<C, TL>((uint32_t)__cvta_generic_to_shared(my_slot),
+                       logits + min(first + half, a.T - 1) * a.stride + place.first, held);
+  };
+#pragma unroll
+  for (int c = 0; c < C; ++c) from_f32(-INFINITY, reinterpret_cast<TL*>(my_slot) + c);
+  fetch(base);
   while (base < a.T) {
     int slow_count = 0;
     for (; base < a.T && slow_count + a.batch <= SLOW_TOKENS; base += step) {
@@ -461,7 +550,13 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_OF_SM) route_pairs_kernel(cons
         const bool on = i + half < count;
         const int64_t t = base + (on ? i + half : i);
         float x[C], s[C], r[C];
-        load_part<C>(logits + t * a.stride, logits + t * a.stride + place.first, held, a.rows, x);
+        if (copied) {
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          read_part<C, TL>(my_slot, x);
+          fetch(i + TOKENS < count ? base + i + TOKENS : base + step);
+        } else {
+          load_part<C>(logits + t * a.stride + place.first, held, x);
+        }
         float inv = 1.0f, shift = 0.0f, least = INFINITY;
 #pragma unroll
         for (int c = 0; c < C; c += 2) least = min_nan(least, x[c], x[c + 1]);
@@ -484,10 +579,21 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_OF_SM) route_pairs_kernel(cons
           if (part == 0) w.shift[i + half] = shift, w.inv[i + half] = inv;
         } else {
           get(bias, r);
+          if constexpr (FAST) {
 #pragma unroll
-          for (int c = 0; c < C; ++c) {
-            s[c] = FAST ? sigmoid_fast(x[c]) : sigmoid(x[c]);
-            r[c] += s[c];
+            for (int c = 0; c < C; c += 2) {
+              float e0, e1;
+              split(mul2(f2(x[c], x[c + 1]), f2(-LOG2E, -LOG2E)), e0, e1);
+              split(add2(f2(exp2_fast(e0), exp2_fast(e1)), f2(1.0f, 1.0f)), e0, e1);
+              s[c] = inverse_fast(e0), s[c + 1] = inverse_fast(e1);
+              split(add2(f2(s[c], s[c + 1]), f2(r[c], r[c + 1])), r[c], r[c + 1]);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+              s[c] = sigmoid(x[c]);
+              r[c] += s[c];
+            }
           }
         }
         if (__any_sync(ALL, held > 0 && !(least > -INFINITY))) {  // masked experts, or NaN
@@ -495,15 +601,9 @@ __global__ void __launch_bounds__(THREADS, BLOCKS_OF_SM) route_pairs_kernel(cons
           for (int c = 0; c < C; ++c) r[c] = x[c] > -INFINITY ? r[c] : -INFINITY;
         }
         int* pick = w.pick + ((i + half) << a.slot_bits);
-        int result = select_pair<LANES, C, MODE == LOGITS, FAST>(a, place, r, shift, margin, lane, mine, w, pick);
-        if (FAST && __any_sync(ALL, result == 1)) {  // not certain: again, with the exact scores
-          __syncwarp();
-          get(bias, r);
-#pragma unroll
-          for (int c = 0; c < C; ++c) r[c] = x[c] > -INFINITY ? r[c] + sigmoid(x[c]) : -INFINITY;
-          result = select_pair<LANES, C, false, false>(a, place, r, 0.0f, 0.0f, lane, mine, w, pick);
-        }
-        const unsigned skips = __ballot_sync(ALL, result == 2 && on);
+        const bool done = select_pair<LANES, C, MODE == LOGITS, FAST>(a, place, logits + t * a.stride + place.first, bias,
+                                                                      r, shift, margin, lane, mine, w, pick);
+        const unsigned skips = __ballot_sync(ALL, !done && on);
 #pragma unroll
         for (int h = 0; h < TOKENS; ++h) {
           if (skips >> (h * LANES) & 1u) {
@@ -604,7 +704,7 @@ Layout layout_of(const RouteArgs& a) {
   return {};
 }
 
-template <int LANES, int C, typename TL, int MODE>
+template <int LANES, int C, typename TL, PairMode MODE>
 cudaError_t launch_pairs(const RouteArgs& args, const Layout& layout, int n_sm, cudaStream_t st) {
   RouteArgs a = args;
   constexpr int UNIT = unit_of<C, TL>(), S = lane_stride<C>();
@@ -616,23 +716,25 @@ cudaError_t launch_pairs(const RouteArgs& args, const Layout& layout, int n_sm, 
   a.segment_lanes = layout.segment_lanes;
   const bool words = reinterpret_cast<uintptr_t>(a.logits) % UNIT == 0 && a.stride * (int64_t)sizeof(TL) % UNIT == 0 &&
                      size * (int)sizeof(TL) % UNIT == 0;
-  a.rows = !words ? ELEMENTS : size % C == 0 ? ALL_OR_NONE : WORDS;
+  a.words = words;
   constexpr int SCORES_UNIT = C % 4 == 0 ? 16 : 8;
   a.wide_scores = reinterpret_cast<uintptr_t>(a.scores) % SCORES_UNIT == 0 && a.E * 4 % SCORES_UNIT == 0 && size % C == 0;
   a.slot_bits = 0;
   while ((1 << a.slot_bits) < a.k) ++a.slot_bits;
+  const bool balance = a.ticket != nullptr;
+  const int smem = (LANES * S + WARPS * 32 * S + (balance ? LANES * C + WARPS * 32 * S : 0)) * 4 +
+                   WARPS * 32 * slot_bytes<C, TL>();
+  const int resident = std::min<int>(blocks_of_sm(MODE), SM_SHARED / (smem + (int)sizeof(Scratch) * WARPS + BLOCK_RESERVED));
   // tokens whose gates are formed together: as many as fill a warp, once every resident warp has a batch
   a.batch = 32 >> a.slot_bits;
-  while (a.batch > 32 / LANES && a.T < (int64_t)a.batch * WARPS * BLOCKS_OF_SM * n_sm) a.batch >>= 1;
-  const bool balance = a.ticket != nullptr;
-  const int smem = (LANES * S + WARPS * 32 * S + (balance ? LANES * C + WARPS * 32 * S : 0)) * 4;
+  while (a.batch > 32 / LANES && a.T < (int64_t)a.batch * WARPS * resident * n_sm) a.batch >>= 1;
   auto kernel = route_pairs_kernel<LANES, C, TL, MODE>;
-  if (smem > 32 * 1024) {
+  if (smem > 36 * 1024) {
     const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
   }
   const int64_t want = (a.T + (int64_t)WARPS * a.batch - 1) / ((int64_t)WARPS * a.batch);
-  const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>(want, BLOCKS_OF_SM * n_sm));
+  const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>(want, resident * n_sm));
   kernel<<<blocks, THREADS, smem, st>>>(a);
   return cudaGetLastError();
 }

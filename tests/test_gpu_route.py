@@ -199,6 +199,34 @@ def test_selection_is_that_of_the_f32_scores_however_near():
     assert torch.equal(one["topk_idx"], out["topk_idx"][:100])
 
 
+@pytest.mark.parametrize("E,G,kg", [(256, 8, 4), (222, 6, 3), (384, 8, 3)])
+def test_near_experts_and_groups_among_many_tokens(E, G, kg):
+    """A group of each token is another one's copy in another order, off by a few f32 steps or not at all: which of
+    them is chosen, and the order of their experts, is that of s + b in f32; calls of few tokens agree in every bit."""
+    T, k, size = 6000, 8, E // G
+    g = torch.Generator(device="cuda").manual_seed(0)
+    x = torch.randn(T, G, size, generator=g, device="cuda")
+    token = torch.arange(T, device="cuda")
+    of = torch.randint(0, G, (T,), generator=g, device="cuda")
+    to = (of + torch.randint(1, G, (T,), generator=g, device="cuda")) % G
+    copy = x[token, of][:, torch.randperm(size, generator=g, device="cuda")]
+    x[token, to] = copy + torch.randint(-2, 3, (T, 1), generator=g, device="cuda") * 2.0 ** -22
+    x = x.view(T, E)
+    bias = torch.randint(-2, 3, (G,), generator=g, device="cuda").float().repeat_interleave(size) * 2.0 ** -23
+    desc = lambda n: mok.make_route_desc(n, E, k, SIGMOID, True, n_group=G, topk_group=kg)  # noqa: E731
+    out = mok.Router(desc(T)).forward(x, bias)
+    r = 1.0 / (1.0 + torch.exp(-x)) + bias
+    best = r.view(T, G, size).sort(dim=2, descending=True, stable=True).values
+    chosen = (best[:, :, 0] + best[:, :, 1]).sort(dim=1, descending=True, stable=True).indices[:, :kg]
+    keep = torch.zeros((T, G), dtype=torch.bool, device="cuda").scatter_(1, chosen, True).repeat_interleave(size, 1)
+    want = torch.where(keep, r, -float("inf")).sort(dim=1, descending=True, stable=True).indices[:, :k]
+    assert torch.equal(out["topk_idx"].long(), want)
+    few = mok.Router(desc(600))
+    for at in range(0, T, 600):
+        part = few.forward(x[at:at + 600], bias)
+        assert all(torch.equal(part[n], out[n][at:at + 600]) for n in part)
+
+
 @pytest.mark.parametrize("G,kg,score", [(1, 1, MAX), (8, 3, TOP2), (8, 3, MAX), (5, 2, TOP2)])
 @pytest.mark.parametrize("router", [SIGMOID, SOFTMAX])
 @pytest.mark.parametrize("with_bias", [False, True])
