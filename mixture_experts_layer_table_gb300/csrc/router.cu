@@ -544,12 +544,12 @@ cudaError_t launch_route_c(const RouteArgs& a, int n_sm, cudaStream_t st) {
 
 // For many tokens, two of them to a warp: that kernel's steps for a token hardly grow with its experts, this one's do,
 // and a call needs tokens for all its warps.  Microseconds here and there, f32 logits, sigmoid with a bias, k = 8 in
-// 4 of 8 groups: 256 experts, 1024 tokens 4.7 and 6.0, 2048 tokens 6.0 and 6.0, 4096 tokens 9.9 and 7.3, 65536
-// tokens 95 and 38; 128 experts, 4096 tokens 5.9 and 5.8, 65536 tokens 60 and 30; ungrouped: 384 experts, 1024 tokens
-// 5.2 and 5.5, 4096 tokens 11.9 and 7.5; 64 experts, 4096 tokens 4.0 and 5.5, 16384 tokens 10.3 and 10.9, 65536
-// tokens 33 and 24; 32 experts, 16384 tokens 6.8 and 9.5, 65536 tokens 21 and 21.
+// 4 of 8 groups: 256 experts, 1024 tokens 4.5 and 4.8, 2048 tokens 5.8 and 4.9, 4096 tokens 9.7 and 6.0, 65536
+// tokens 97 and 37; 128 experts, 4096 tokens 5.9 and 5.5, 65536 tokens 60 and 29; ungrouped: 384 experts, 1024 tokens
+// 5.2 and 4.7, 4096 tokens 12.0 and 8.0; 64 experts, 4096 tokens 4.0 and 4.8, 16384 tokens 11.0 and 10.3, 65536
+// tokens 33 and 23; 32 experts, 16384 tokens 6.8 and 8.7, 65536 tokens 21 and 20.
 cudaError_t launch_route(const RouteArgs& a, bool bf16, int n_sm, cudaStream_t st) {
-  if (a.T * a.E * a.E >= int64_t{1} << 27 && route_pairs_fit(a)) return launch_route_pairs(a, bf16, n_sm, st);
+  if (a.T * a.E * a.E >= int64_t{3} << 25 && route_pairs_fit(a)) return launch_route_pairs(a, bf16, n_sm, st);
   if (bf16) ROUTE_BY_C(launch_route_c, __nv_bfloat16);
   ROUTE_BY_C(launch_route_c, float);
 }

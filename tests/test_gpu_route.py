@@ -106,7 +106,7 @@ def test_sum_of_two_ties_on_equal_rows():
 
 
 def _many(E):
-    """Tokens from which on the kernel for many takes them."""
+    """Tokens that the kernel for many takes, at E experts."""
     return -(-2 ** 27 // E ** 2)
 
 
@@ -536,8 +536,7 @@ def test_layer_routes_within_groups(router, score, mxfp8):
 
 @pytest.mark.parametrize("E", [32, 256])
 def test_layer_with_groups_and_many_tokens(E):
-    """With 256 experts, from 2,048 tokens on, the layer's selection is the many-token kernel's, with the scores it
-    hands out."""
+    """With 256 experts 2,100 tokens are many: the layer's selection is that kernel's, with the scores it hands out."""
     shape = GROUPED.scaled(T=2100, E=E)
     inp = {n: t.cuda() for n, t in W.make_inputs(shape, seed=3).items() if t is not None}
     bias = _cuda(_bias(E, 4, True))
