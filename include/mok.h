@@ -438,7 +438,8 @@ mok_status mok_grad_norm(const mok_grad_tensor* tensors, int32_t count, float ma
 /* One tensor of an AdamW step, n contiguous elements:
  *   param    f32, or bf16; with bf16, master is its f32 copy (param becomes the rounded master) or
  *            NULL (param is then rounded at random, up or down, with the mean unchanged: a step is
- *            mostly smaller than half of a bf16 spacing, and rounded to nearest would be lost).
+ *            mostly smaller than half of a bf16 spacing, and rounded to nearest would be lost; an
+ *            infinity or NaN stays one).
  *            master must be NULL for an f32 param
  *   grad     f32 or bf16
  *   state_type  MOK_STATE_F32: m and v are f32 [n], v_scale and m_scale NULL.

@@ -85,16 +85,15 @@ __device__ __forceinline__ void store8(float* p, uint32_t i, int left, const flo
       if (j < left) p[i + j] = x[j];
   }
 }
-// 8 bf16 bit patterns, the high half of each word
+// 8 bf16, two to a word
 template <bool WIDE>
-__device__ __forceinline__ void store8(__nv_bfloat16* p, uint32_t i, int left, const uint32_t (&b)[VEC]) {
+__device__ __forceinline__ void store8(__nv_bfloat16* p, uint32_t i, int left, const uint32_t (&w)[VEC / 2]) {
   if constexpr (WIDE) {
-    *reinterpret_cast<uint4*>(p + i) = make_uint4(__byte_perm(b[0], b[1], 0x7632), __byte_perm(b[2], b[3], 0x7632),
-                                                  __byte_perm(b[4], b[5], 0x7632), __byte_perm(b[6], b[7], 0x7632));
+    *reinterpret_cast<uint4*>(p + i) = make_uint4(w[0], w[1], w[2], w[3]);
   } else {
 #pragma unroll
     for (int j = 0; j < VEC; ++j)
-      if (j < left) p[i + j] = __ushort_as_bfloat16((unsigned short)(b[j] >> 16));
+      if (j < left) p[i + j] = __ushort_as_bfloat16((unsigned short)(w[j >> 1] >> (16 * (j & 1))));
   }
 }
 
@@ -274,19 +273,30 @@ __device__ __forceinline__ void load_grad(const AdamTensor& T, uint32_t i, int l
   if constexpr (GK == GRAD_F32) load8<WIDE>(static_cast<const float*>(T.grad), i, left, g);
   else load8<WIDE>(static_cast<const __nv_bfloat16*>(T.grad), i, left, g);
 }
+// Two values to bf16, each up or down by 16 random bits (z's low half) added to its own bits and what lies below bf16
+// cut off.  The conversion keeps infinities and NaN, which the sum itself would carry over (0x7fffffff to -0).
+__device__ __forceinline__ uint32_t to_bf16_random(float lo, float hi, uint32_t z_lo, uint32_t z_hi) {
+  uint32_t r;
+  asm("cvt.rs.bf16x2.f32 %0, %1, %2, %3;" : "=r"(r) : "f"(hi), "f"(lo), "r"(__byte_perm(z_lo, z_hi, 0x5410)));
+  return r;
+}
+__device__ __forceinline__ uint32_t to_bf16(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
 template <int PK, bool WIDE>
 __device__ __forceinline__ void store_param(const AdamTensor& T, uint32_t i, int left, const float (&p)[VEC],
                                             const uint32_t (&z)[VEC]) {
   if constexpr (PK == PARAM_F32) {
     store8<WIDE>(static_cast<float*>(T.param), i, left, p);
   } else {
-    uint32_t b[VEC];
+    uint32_t w[VEC / 2];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      if constexpr (PK == PARAM_BF16) b[j] = __float_as_uint(p[j]) + (z[j] & 0xffffu);
-      else b[j] = (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(p[j])) << 16;
+    for (int j = 0; j < VEC; j += 2) {
+      if constexpr (PK == PARAM_BF16) w[j / 2] = to_bf16_random(p[j], p[j + 1], z[j], z[j + 1]);
+      else w[j / 2] = to_bf16(p[j], p[j + 1]);
     }
-    store8<WIDE>(static_cast<__nv_bfloat16*>(T.param), i, left, b);
+    store8<WIDE>(static_cast<__nv_bfloat16*>(T.param), i, left, w);
     if constexpr (PK == PARAM_BF16_MASTER) store8<WIDE>(T.master, i, left, p);
   }
 }

@@ -195,6 +195,38 @@ def test_adamw_infinite_gradient_shows():
     assert bad.nonzero().flatten().tolist() == [5]
 
 
+KINDS = [(pk, grad, state) for pk in ("f32", "master", "bf16") for grad in (torch.float32, torch.bfloat16)
+         for state in ("f32", "mx8")]
+
+
+def _with_and_without(pk, grad_dtype, state, at, n=2085, **kw):
+    """Two optimizers on the same tensors, but for the gradients at `at`, zero in the second's: what the others' rounding
+    and scales are held against.  2,085 elements: whole words, and a tail of single ones."""
+    made = []
+    for clean in (False, True):
+        params = _tensors((n,), torch.float32 if pk == "f32" else torch.bfloat16, 0.05, 71)
+        grads = _tensors((n,), grad_dtype, 1e-3, 72)
+        grads[0][list(at)] = 0.0
+        for i, x in at.items():
+            if not clean:
+                grads[0][i] = x
+        made.append(mok.AdamW(params, grads, state=state, masters=True if pk == "master" else None, seed=17, **HYPER, **kw))
+    return made
+
+
+@pytest.mark.parametrize("pk,grad,state", KINDS)
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+def test_adamw_gradients_that_are_not_finite_show_in_every_kind_of_parameter(pk, grad, state, bad):
+    """Their own parameters become NaN, whatever random bits round them, and stay so; no others do."""
+    at = {i: bad for i in (5, 700, 701, 2080, 2084)}
+    opt, _ = _with_and_without(pk, grad, state, at)
+    for _ in range(3):
+        opt.step()
+        assert torch.isnan(opt.params[0]).nonzero().flatten().tolist() == sorted(at)
+        assert torch.isfinite(opt.params[0]).sum().item() == 2085 - len(at)
+        opt.grads[0][list(at)] = 0.0
+
+
 def test_adamw_states_in_8_bits_follow_the_32_bit_ones():
     """With steps far below a grid spacing (beta2 = 0.999) the 8-bit states keep moving with the f32 ones: over
     4096 elements the mean of sqrt(v) and of m stay together.  sqrt(v) wanders by a random rounding of up to
