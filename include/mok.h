@@ -447,9 +447,11 @@ mok_status mok_grad_norm(const mok_grad_tensor* tensors, int32_t count, float ma
  *               m_scale and v_scale [ceil(n / 32)] E8M0 bytes b standing for 2^(b - 127): the OCP
  *               Microscaling layout the layer's MXFP8 operands have.  Elements are rounded at random,
  *               with the mean unchanged; a nonzero sqrt(v) never becomes zero.  v below 2^-126
- *               counts as 0.  Scale bytes are written from 1 to 254; a block under byte 0 reads as
- *               zeros, one under byte 255 (the format's NaN) as not finite.  All-zero states: zero
- *               elements with scale bytes 0 to 254.
+ *               counts as 0.  An m or sqrt(v) that is not finite (an infinite gradient, or one whose
+ *               square is beyond f32) is kept as a NaN; the other elements of its block and the
+ *               block's scale are what they would be with a zero in its place.  Scale bytes are written
+ *               from 1 to 254; a block under byte 0 reads as zeros, one under byte 255 (the format's
+ *               NaN) as not finite.  All-zero states: zero elements with scale bytes 0 to 254.
  *   counter  multiple of 8: element i takes the rounding bits of number counter + i.  Tensors whose
  *            ranges [counter, counter + n) do not overlap are rounded independently
  * Pointers are aligned to their element; 16-byte aligned ones are accessed in 16 bytes. */

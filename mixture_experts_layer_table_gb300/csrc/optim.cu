@@ -175,8 +175,14 @@ __device__ __forceinline__ F2 to_grid(F2 y, F2 w) {
 __device__ __forceinline__ float high_bits(uint32_t z) { return __uint_as_float(__funnelshift_r(z, 0x7cu, 9)); }
 __device__ __forceinline__ float low_bits(uint32_t z) { return __uint_as_float((z & 0x7fffffu) | 0x3e000000u); }
 
-// Largest magnitude of a block: this thread's 8 elements and those of the three threads next to it.
-__device__ __forceinline__ float block_max(const F2 (&x)[VEC / 2]) {
+// Infinities to NaN: E4M3 has none, and the least power of two that reaches one would leave nothing of the block's other
+// elements.
+__device__ __forceinline__ void infinities_to_nan(F2 (&x)[VEC / 2]) {
+#pragma unroll
+  for (int j = 0; j < VEC / 2; ++j) x[j] = fma2(x[j], f2(0.0f), x[j]);
+}
+// Largest magnitude, NaN aside, of this thread's 8 elements, and of a block: those of the three threads next to it too.
+__device__ __forceinline__ float thread_max(const F2 (&x)[VEC / 2]) {
   float a = 0.0f;
 #pragma unroll
   for (int j = 0; j < VEC / 2; ++j) {
@@ -184,6 +190,9 @@ __device__ __forceinline__ float block_max(const F2 (&x)[VEC / 2]) {
     split(x[j], lo, hi);
     a = fmaxf(a, fmaxf(fabsf(lo), fabsf(hi)));
   }
+  return a;
+}
+__device__ __forceinline__ float block_max(float a) {
   a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
   return fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
 }
@@ -362,7 +371,14 @@ __device__ __forceinline__ void step8_mx8(const AdamTensor& T, const Mx8Constant
     split(fma2(m[j], f2(fast_inverse(d0), fast_inverse(d1)), fma2(pj, decay, pj)), p[2 * j], p[2 * j + 1]);
   }
   store_param<PK, WIDE>(T, i, left, p, z);
-  const int bm = scale_byte(block_max(m)), br = scale_byte(block_max(r));
+  // (looked for once per thread: without the branch, in every element, the step was 4% slower)
+  float am = thread_max(m), ar = thread_max(r);
+  if (fmaxf(am, ar) == INFINITY) {
+    infinities_to_nan(m);
+    infinities_to_nan(r);
+    am = thread_max(m), ar = thread_max(r);
+  }
+  const int bm = scale_byte(block_max(am)), br = scale_byte(block_max(ar));
   const F2 im = f2(power_of_two(254 - bm)), ir = f2(power_of_two(254 - br));
 #pragma unroll
   for (int j = 0; j < VEC / 2; ++j) {
@@ -371,7 +387,7 @@ __device__ __forceinline__ void step8_mx8(const AdamTensor& T, const Mx8Constant
     float y0, y1, q0, q1;
     split(y, y0, y1);
     split(to_grid(y, f2(low_bits(z[2 * j]), low_bits(z[2 * j + 1]))), q0, q1);
-    // a nonzero root below the least E4M3 value becomes that value
+    // a nonzero root below the least E4M3 value becomes that value (and NaN, of which y > 0 is false, stays)
     if (y0 > 0.0f) q0 = fmaxf(q0, 0.001953125f);
     if (y1 > 0.0f) q1 = fmaxf(q1, 0.001953125f);
     r[j] = f2(q0, q1);

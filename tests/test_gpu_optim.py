@@ -227,6 +227,70 @@ def test_adamw_gradients_that_are_not_finite_show_in_every_kind_of_parameter(pk,
         opt.grads[0][list(at)] = 0.0
 
 
+def _same(a, b):
+    return torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("pk,grad,state", [k for k in KINDS if k[2] == "mx8"])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_adamw_gradients_that_are_not_finite_leave_the_rest_of_a_block_of_8_bit_states(pk, grad, state, bad):
+    """The other 31 elements of the block are stepped as if those gradients had been zero, state for state and bit for
+    bit, in this step and the ones after it; the elements' own states become NaN."""
+    at = {i: bad for i in (5, 700, 701, 2080, 2084)}
+    opt, clean = _with_and_without(pk, grad, state, at)
+    others = torch.ones(2085, dtype=torch.bool, device="cuda")
+    others[list(at)] = False
+    for _ in range(3):
+        opt.step()
+        clean.step()
+        assert _same(opt.params[0][others], clean.params[0][others])
+        for n in ("m", "v"):
+            assert _same(opt.states[n][0].view(torch.uint8)[others], clean.states[n][0].view(torch.uint8)[others])
+            assert torch.isnan(opt.states[n][0].float()[~others]).all()
+            assert _same(opt.states[n + "_scale"][0], clean.states[n + "_scale"][0])
+        opt.grads[0][list(at)] = 0.0
+
+
+@pytest.mark.parametrize("pk", ["f32", "bf16"])
+def test_adamw_gradients_whose_square_overflows_show_in_8_bit_states(pk):
+    """sqrt(v) is not finite then: it is kept as a NaN (E4M3 has no infinity), alone of its block, and shows in the
+    parameter at the next step.  m is finite, and its block's scale grows with it."""
+    at = {700: 1e25, 2084: 1e25}
+    opt, clean = _with_and_without(pk, torch.float32, "mx8", at)
+    for o in (opt, clean):
+        o.step()
+    others = torch.ones(2085, dtype=torch.bool, device="cuda")
+    others[list(at)] = False
+    v = opt.states["v"][0]
+    assert torch.isnan(v.float()).nonzero().flatten().tolist() == sorted(at)
+    assert _same(v.view(torch.uint8)[others], clean.states["v"][0].view(torch.uint8)[others])
+    assert _same(opt.states["v_scale"][0], clean.states["v_scale"][0])
+    assert _same(opt.params[0][others], clean.params[0][others])
+    assert torch.isfinite(opt.states["m"][0].float()).all()
+    opt.grads[0].zero_()
+    opt.step()
+    assert torch.isnan(opt.params[0]).nonzero().flatten().tolist() == sorted(at)
+
+
+def test_adamw_a_scale_byte_of_255_is_not_finite():
+    """The block under it becomes NaN, states and, a step later at most, parameters; the other blocks do not."""
+    opt, clean = _with_and_without("f32", torch.float32, "mx8", {})
+    for o in (opt, clean):
+        o.step()
+    for name in ("m_scale", "v_scale"):
+        opt.states[name][0][3] = 255
+        opt.states[name][0][65] = 255          # the last block, of 5 elements
+    for o in (opt, clean):
+        o.step()
+        o.step()
+    block = torch.arange(2085, device="cuda") // 32
+    hit = (block == 3) | (block == 65)
+    assert torch.isnan(opt.params[0][hit]).all() and _same(opt.params[0][~hit], clean.params[0][~hit])
+    for n in ("m", "v"):
+        assert torch.isnan(opt.states[n][0].float()[hit]).all()
+        assert _same(opt.states[n][0].view(torch.uint8)[~hit], clean.states[n][0].view(torch.uint8)[~hit])
+
+
 def test_adamw_states_in_8_bits_follow_the_32_bit_ones():
     """With steps far below a grid spacing (beta2 = 0.999) the 8-bit states keep moving with the f32 ones: over
     4096 elements the mean of sqrt(v) and of m stay together.  sqrt(v) wanders by a random rounding of up to
