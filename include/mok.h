@@ -367,7 +367,8 @@ mok_status mok_moe_backward(const mok_layer_desc* desc, const void* dy, const vo
  *   balance_coef, bias_rate  factors of the balance loss and of the bias step
  * With s the scores, an expert's rank value is s + bias (softmax without a bias: its logit, and
  * e^(logit - max) in a sum of two, the same order without the rounding of the softmax's sum).  An
- * expert whose logit is -inf (masked) or NaN ranks behind all others and counts in no group's value.
+ * expert whose logit or bias is -inf (masked) or NaN ranks behind all others and counts in no group's
+ * value; every other bias is added as it is, the type's lowest and largest values and +inf too.
  * The topk_group best groups stay, then the k best experts in them; ties go to the lower index. */
 typedef enum { MOK_GROUP_MAX = 0, MOK_GROUP_TOP2 = 1 } mok_group_score;
 typedef struct {

@@ -26,6 +26,7 @@
 // another's results: shared memory and shuffles between the steps; the SMs' ends lie 15% apart).  4,096 tokens 6 us,
 // with the balance outputs 9.4.
 #include <algorithm>
+#include <cfloat>
 #include <cstddef>
 
 #include "router_common.cuh"
@@ -336,12 +337,17 @@ struct Place {
 };
 
 // The selection of a warp's tokens, one on each LANES lanes, from the lanes' rank values r (shift: of each softmax):
-// the experts in pick.  FAST: r is off by less than margin / 2; what that leaves open is settled on exact values,
+// the experts in pick.  FAST: r is approximate; what that leaves open is settled on exact values,
 // of the token's logits `own` from this lane's first on and their bias.  False (on all lanes of a token): more than the
 // list holds, or too few experts.
+//
+// An approximate rank value v = s + b is off by less than 4e-7 + 2^-23 |v|: the order of two is certain from twice that
+// on, and more is taken.  The distance goes by the value itself: a far larger bias of another expert (the type's lowest
+// value, as a mask) leaves the order of the others certain.
+__device__ __forceinline__ float distance_of(float v) { return fmaf(5e-7f, fabsf(v), 1.5e-6f); }
 template <int LANES, int C, bool LOGIT_VALUES, bool FAST, typename TL>
 __device__ __forceinline__ bool select_pair(const RouteArgs& a, const Place& p, const TL* own, const float* bias,
-                                            float (&r)[C], float shift, float margin, int lane, float* mine, Scratch& w,
+                                            float (&r)[C], float shift, int lane, float* mine, Scratch& w,
                                             int* pick) {
   const int half = lane / LANES, part = lane % LANES;
   if (part < 16) w.value[half][part] = -INFINITY;
@@ -403,10 +409,12 @@ __device__ __forceinline__ bool select_pair(const RouteArgs& a, const Place& p, 
   // 3. the listed experts, in their order
   float bound = token_min<LANES>(in_play && p.bounds ? low : INFINITY);
   const bool none = !(bound > -INFINITY);
-  bound = in_play ? bound - margin : INFINITY;
+  // (never -inf, the value of masked experts and of places without one)
+  if (FAST) bound = fmaxf(bound - distance_of(bound), -FLT_MAX);
   unsigned listed = 0u;
 #pragma unroll
   for (int c = 0; c < C; ++c) listed |= r[c] >= bound ? 1u << c : 0u;
+  if (!in_play) listed = 0u;  // (with +inf among its values too)
   const int of_lane = __popc(listed);
   int before = of_lane;
 #pragma unroll
@@ -434,8 +442,8 @@ __device__ __forceinline__ bool select_pair(const RouteArgs& a, const Place& p, 
   __syncwarp();
   if (FAST) {
     for (int at = part; at - part < longest; at += LANES) {  // how many might be better, itself among them
-      const float v = w.value[half][at] - margin;
-      const F2 reach = f2(v, v);
+      const float v = w.value[half][at], far = v - distance_of(v);
+      const F2 reach = f2(far, far);
       int better = -1;
       for (int block = 0; block < longest; block += 16) {
         uint32_t signs = 0u;
@@ -449,9 +457,10 @@ __device__ __forceinline__ bool select_pair(const RouteArgs& a, const Place& p, 
         }
         better += __popc(signs);
       }
-      if (at < n && better < a.k) pick[better] = w.expert[half][at];
+      // (-1 for +inf, of which nothing is certain: a difference that is NaN counts nothing, itself neither)
+      if (at < n && (unsigned)better < (unsigned)a.k) pick[better] = w.expert[half][at];
     }
-    // Where each of the best k is at least the margin above the next, it has its place; else the first that is not
+    // Where each of the best k is at least the distance above the next, it has its place; else the first that is not
     // leaves its own empty, and the places are counted again on the exact values.
     __syncwarp();
     if (!__any_sync(ALL, n > 0 && part < a.k && pick[part] < 0)) return !out;
@@ -500,7 +509,6 @@ __global__ void __launch_bounds__(THREADS, blocks_of_sm(MODE)) route_pairs_kerne
   float* mine = rows + (warp * 32 + lane) * S;
   float* my_sums = sums + (warp * 32 + lane) * S;
   const float* bias = sh + part * S;
-  float margin = 0.0f;
   const int size = a.group_size, lane_bits = a.n_group > 1 ? a.group_lane_bits : LANES == 32 ? 5 : 4, lanes = 1 << lane_bits;
   for (int i = threadIdx.x; i < LANES * C; i += THREADS) {
     const int l = i / C, c = i % C, group = l >> lane_bits, at = (l & (lanes - 1)) * C + c, e = group * size + at;
@@ -513,13 +521,6 @@ __global__ void __launch_bounds__(THREADS, blocks_of_sm(MODE)) route_pairs_kerne
     for (int c = 0; c < C; ++c) my_sums[c] = 0.0f;
   }
   __syncthreads();
-  // Approximate rank values s + b are off by less than 4e-7 + 2^-23 |s + b|: their order is certain from twice that on.
-  if (FAST) {
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-      if (bias[c] > -INFINITY) margin = fmaxf(margin, fabsf(bias[c]));
-    margin = fmaf(5e-7f, 1.0f + warp_max(margin), 1e-6f);
-  }
   const int group = part >> lane_bits, in_group = (part & (lanes - 1)) * C;
   const int held = group < a.n_group ? max(0, min(C, size - in_group)) : 0;
   const Place place = {lanes, group, held > 0 ? group * size + in_group : 0, held,
@@ -602,7 +603,7 @@ __global__ void __launch_bounds__(THREADS, blocks_of_sm(MODE)) route_pairs_kerne
         }
         int* pick = w.pick + ((i + half) << a.slot_bits);
         const bool done = select_pair<LANES, C, MODE == LOGITS, FAST>(a, place, logits + t * a.stride + place.first, bias,
-                                                                      r, shift, margin, lane, mine, w, pick);
+                                                                      r, shift, lane, mine, w, pick);
         const unsigned skips = __ballot_sync(ALL, !done && on);
 #pragma unroll
         for (int h = 0; h < TOKENS; ++h) {

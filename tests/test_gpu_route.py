@@ -557,3 +557,91 @@ def test_layer_refuses_bad_groups():
                dict(n_group=8, topk_group=9), dict(n_group=32, topk_group=3), dict(n_group=8, topk_group=2, group_score=2)):
         with pytest.raises(mok.MokError):
             mok.get_layout(mok.desc_from_shape(GROUPED, **kw))
+
+
+def _f32_selection(x, bias, k, G, kg, top2=True):
+    """The selection by s + b in f32, s = 1 / (1 + e^-x) by steps rounded to f32, ties to the lower index: -inf ranks
+    (masked logits, biases of -inf or NaN) behind all others and in no group's value."""
+    T, E = x.shape
+    r = 1.0 / (1.0 + torch.exp(-x)) + bias
+    r = torch.where((x > -float("inf")) & ~torch.isnan(r), r, -float("inf"))
+    first = r.sort(dim=1, descending=True, stable=True).indices
+    if G > 1:
+        best = r.view(T, G, E // G).sort(dim=2, descending=True, stable=True).values
+        value = best[:, :, 0]
+        if top2 and E > G:
+            value = torch.where(best[:, :, 1] > -float("inf"), value + best[:, :, 1], value)
+        chosen = value.sort(dim=1, descending=True, stable=True).indices[:, :kg]
+        left_out = torch.ones((T, G), dtype=torch.int32, device=x.device).scatter_(1, chosen, 0).repeat_interleave(E // G, 1)
+        first = first.gather(1, left_out.gather(1, first).sort(dim=1, stable=True).indices)   # behind -inf
+    return first[:, :k]
+
+
+LOWEST, LARGEST, INF = torch.finfo(torch.float32).min, torch.finfo(torch.float32).max, float("inf")
+
+
+def _extreme_bias(kind, E, size, rng):
+    b = (rng.normal(size=E) * 0.1).astype(np.float32)
+    at = np.arange(E)
+    if kind == "lowest":
+        b[rng.random(E) < 0.2] = LOWEST
+    elif kind == "lowest_groups":                       # whole groups, and all but one expert of another
+        b[: size] = LOWEST
+        b[E - size + 1:] = LOWEST
+    elif kind == "lowest_but_three":
+        b[~np.isin(at, (1, E // 2, E - 1))] = LOWEST
+    elif kind == "minus_inf":
+        b[rng.random(E) < 0.3] = -np.inf
+    elif kind == "plus_inf":                            # in every group, and twice in some
+        b[at % size == 0] = np.inf
+        b[min(3, E - 1)] = np.inf
+    elif kind == "plus_inf_one":
+        b[E - 1] = np.inf
+    elif kind == "mixed":
+        for value in (LOWEST, LARGEST, -np.inf, np.nan, 1e30, -1e30, 2.0 ** 26, -2.0 ** 25, 1e5, -1e5, 30.0):
+            b[rng.random(E) < 0.03] = value
+    elif kind == "all_lowest":
+        b[:] = LOWEST
+    elif kind == "all_largest":
+        b[:] = LARGEST
+    return b
+
+
+@pytest.mark.parametrize("E,k,G,kg,score", [(256, 8, 8, 4, TOP2), (222, 8, 6, 3, TOP2), (222, 8, 6, 3, MAX), (35, 4, 5, 2, MAX),
+                                            (57, 5, 3, 2, TOP2), (511, 8, 1, 1, MAX), (384, 8, 8, 3, TOP2), (20, 4, 20, 6, TOP2)])
+@pytest.mark.parametrize("kind", ["lowest", "lowest_groups", "lowest_but_three", "minus_inf", "plus_inf", "plus_inf_one",
+                                  "mixed", "all_lowest", "all_largest"])
+def test_biases_at_the_ends_of_the_type(E, k, G, kg, score, kind):
+    """Masks by the type's lowest value or -inf, experts forced by +inf, in calls of many tokens and of few: the selection
+    of the f32 rank values, indices in range and distinct."""
+    T, rng = max(_many(E) + 3, 2500), np.random.default_rng(43)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    rows = torch.randn(500, E, generator=g, device="cuda")
+    rows[:100][torch.rand(100, E, generator=g, device="cuda") < 0.1] = -INF
+    x = rows[torch.arange(T, device="cuda") % 500]
+    bias = _cuda(_extreme_bias(kind, E, E // G, rng))
+    want = _f32_selection(rows, bias, k, G, kg, score == TOP2)[torch.arange(T, device="cuda") % 500]
+    desc = lambda n: mok.make_route_desc(n, E, k, SIGMOID, True, n_group=G, topk_group=kg, group_score=score)  # noqa: E731
+    first = mok.Router(desc(500)).forward(rows, bias)
+    assert torch.equal(first["topk_idx"].long(), want[:500])
+    for kw in (dict(), dict(scores=True), dict(balance=True)):
+        out = mok.Router(desc(T), **kw).forward(x, bias)
+        assert torch.equal(out["topk_idx"].long(), want), kw
+        assert torch.equal(out["gates"][-500:], first["gates"][torch.arange(T - 500, T, device="cuda") % 500])
+        if "counts" in out:
+            assert torch.equal(out["counts"].long(), torch.bincount(want.flatten(), minlength=E))
+
+
+@pytest.mark.parametrize("E,k,G,kg", [(256, 8, 8, 4), (222, 8, 6, 3), (35, 4, 5, 2), (384, 8, 8, 3)])
+def test_infinite_logits_in_groups_that_are_not_chosen(E, k, G, kg):
+    """Groups ranked by their best logit, +inf in more of them than are chosen: ties to the lower groups, and no expert of
+    the others."""
+    T, size = max(_many(E) + 3, 2500), E // G
+    rows = torch.randn(500, E, generator=torch.Generator().manual_seed(3))
+    rows[:, 1::size] = INF
+    x = rows.cuda()[torch.arange(T, device="cuda") % 500]
+    desc = lambda n: mok.make_route_desc(n, E, k, SOFTMAX, True, n_group=G, topk_group=kg, group_score=MAX)  # noqa: E731
+    idx, _ = O.select(rows.double().numpy(), None, SOFTMAX, k, G, kg, MAX)
+    assert np.array_equal(mok.Router(desc(500)).forward(rows.cuda())["topk_idx"].cpu().numpy(), idx)
+    out = mok.Router(desc(T)).forward(x)["topk_idx"]
+    assert torch.equal(out, _cuda(idx)[torch.arange(T, device="cuda") % 500])
