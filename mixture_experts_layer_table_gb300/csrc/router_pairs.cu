@@ -347,8 +347,8 @@ struct Place {
 __device__ __forceinline__ float distance_of(float v) { return fmaf(5e-7f, fabsf(v), 1.5e-6f); }
 template <int LANES, int C, bool LOGIT_VALUES, bool FAST, typename TL>
 __device__ __forceinline__ bool select_pair(const RouteArgs& a, const Place& p, const TL* own, const float* bias,
-                                            float (&r)[C], float shift, int lane, float* mine, Scratch& w,
-                                            int* pick) {
+                                            float (&r)[C], float shift, float group_distance, int lane, float* mine,
+                                            Scratch& w, int* pick) {
   const int half = lane / LANES, part = lane % LANES;
   if (part < 16) w.value[half][part] = -INFINITY;
   if (FAST && part < a.k) pick[part] = -1;
@@ -393,7 +393,7 @@ __device__ __forceinline__ bool select_pair(const RouteArgs& a, const Place& p, 
       break;
     }
     // those that might be better, itself among them: up to topk_group of these, and it is chosen for certain
-    const float reach = value - fmaf(1e-6f, fabsf(value), 2e-6f);
+    const float reach = value - fmaf(3e-7f, fabsf(value), group_distance);
     const int near = count([&](int, float o) { return o > reach; });
     in_play = near <= a.topk_group && value > -INFINITY;
     const unsigned chosen = __ballot_sync(ALL, in_play) >> (half * LANES) & (ALL >> (32 - LANES));
@@ -521,6 +521,15 @@ __global__ void __launch_bounds__(THREADS, blocks_of_sm(MODE)) route_pairs_kerne
     for (int c = 0; c < C; ++c) my_sums[c] = 0.0f;
   }
   __syncthreads();
+  // A group's value is the sum of two, each off as distance_of has it, whatever is left of them in the sum; biases from
+  // 2^26 on take every s without a trace, so that such a rank value is exact.
+  float group_distance = 0.0f;
+  if (FAST) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (fabsf(bias[c]) < 67108864.0f) group_distance = fmaxf(group_distance, fabsf(bias[c]));
+    group_distance = 2.0f * distance_of(1.0f + warp_max(group_distance));
+  }
   const int group = part >> lane_bits, in_group = (part & (lanes - 1)) * C;
   const int held = group < a.n_group ? max(0, min(C, size - in_group)) : 0;
   const Place place = {lanes, group, held > 0 ? group * size + in_group : 0, held,
@@ -603,7 +612,7 @@ __global__ void __launch_bounds__(THREADS, blocks_of_sm(MODE)) route_pairs_kerne
         }
         int* pick = w.pick + ((i + half) << a.slot_bits);
         const bool done = select_pair<LANES, C, MODE == LOGITS, FAST>(a, place, logits + t * a.stride + place.first, bias,
-                                                                      r, shift, lane, mine, w, pick);
+                                                                      r, shift, group_distance, lane, mine, w, pick);
         const unsigned skips = __ballot_sync(ALL, !done && on);
 #pragma unroll
         for (int h = 0; h < TOKENS; ++h) {

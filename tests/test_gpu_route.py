@@ -645,3 +645,24 @@ def test_infinite_logits_in_groups_that_are_not_chosen(E, k, G, kg):
     assert np.array_equal(mok.Router(desc(500)).forward(rows.cuda())["topk_idx"].cpu().numpy(), idx)
     out = mok.Router(desc(T)).forward(x)["topk_idx"]
     assert torch.equal(out, _cuda(idx)[torch.arange(T, device="cuda") % 500])
+
+
+@pytest.mark.parametrize("size_of_bias", [30.0, 1000.0])
+@pytest.mark.parametrize("E,G,kg", [(256, 8, 4), (222, 6, 3), (384, 8, 3)])
+def test_near_groups_whose_best_have_large_biases_of_opposite_sign(E, G, kg, size_of_bias):
+    """One expert of each group is favoured by a large bias and the others are held back by it: a group's sum of two is
+    small, its summands and what the approximate ones are off by are not.  The groups are copies of one another, off by a
+    few steps of their rank values' rounding."""
+    T, k, size = 6000, 8, E // G
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(T, 1, size, generator=g, device="cuda").repeat(1, G, 1)
+    x = x + torch.randint(-3, 4, (T, G, 1), generator=g, device="cuda") * (size_of_bias * 2.0 ** -25)
+    x = x.view(T, E)
+    bias = torch.where(torch.arange(E, device="cuda") % size == 0, size_of_bias, -size_of_bias)
+    desc = lambda n: mok.make_route_desc(n, E, k, SIGMOID, True, n_group=G, topk_group=kg)  # noqa: E731
+    out = mok.Router(desc(T)).forward(x, bias)
+    assert torch.equal(out["topk_idx"].long(), _f32_selection(x, bias, k, G, kg))
+    few = mok.Router(desc(600))
+    for at in range(0, T, 600):
+        part = few.forward(x[at:at + 600], bias)
+        assert all(torch.equal(part[n], out[n][at:at + 600]) for n in part)
