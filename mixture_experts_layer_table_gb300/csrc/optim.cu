@@ -8,6 +8,7 @@
 #include <cfloat>
 #include <type_traits>
 
+#include "f32x2.cuh"
 #include "optim.cuh"
 
 namespace mok {
@@ -111,25 +112,7 @@ __device__ __forceinline__ void rounding_bits(uint64_t group, uint32_t seed, uin
 }
 
 // ----------------------------------------------------------------------------- packed f32
-// Two f32 in a register pair: one instruction for both (the 8-bit step is bound by issued instructions).
-using F2 = unsigned long long;
-__device__ __forceinline__ F2 f2(float a, float b) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ F2 f2(float a) { return f2(a, a); }
-__device__ __forceinline__ void split(F2 x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
+// (the 8-bit step is bound by issued instructions)
 __device__ __forceinline__ F2 fma2_down(F2 a, F2 b, F2 c) {
   F2 r;
   asm("fma.rm.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));

@@ -397,12 +397,11 @@ __global__ void __launch_bounds__(THREADS, backward_blocks(Q, DENSE)) route_back
 #pragma unroll
       for (int o = LANES / 2; o > 0; o >>= 1) shift = fmaxf(shift, __shfl_xor_sync(ALL, shift, o));
       if (shift == -INFINITY) shift = 0.0f;
-      const float offset = -shift * LOG2E;
       float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < Q; ++i) {
-        s[i] = make_float4(exp2_fast(fmaf(s[i].x, LOG2E, offset)), exp2_fast(fmaf(s[i].y, LOG2E, offset)),
-                           exp2_fast(fmaf(s[i].z, LOG2E, offset)), exp2_fast(fmaf(s[i].w, LOG2E, offset)));
+        exp_pair(s[i].x, s[i].y, shift, s[i].x, s[i].y);
+        exp_pair(s[i].z, s[i].w, shift, s[i].z, s[i].w);
         sum += (s[i].x + s[i].y) + (s[i].z + s[i].w);
       }
       sum = token_sum<LANES>(sum);

@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "f32x2.cuh"
 #include "router.cuh"
 
 namespace mok {
@@ -42,6 +43,12 @@ __device__ __forceinline__ float inverse_fast(float x) {
   return r;
 }
 constexpr float LOG2E = 1.442695041f;
+// e^(a - shift) and e^(b - shift) by it.  The shift is taken off first: as a rounded product of its own in the exponent it
+// would skew all terms of a softmax's sum alike (4e-5 at a shift of 1000), but not a score that is formed apart from them.
+__device__ __forceinline__ void exp_pair(float a, float b, float shift, float& ea, float& eb) {
+  split(mul2(add2(f2(a, b), f2(-shift)), f2(LOG2E)), ea, eb);
+  ea = exp2_fast(ea), eb = exp2_fast(eb);
+}
 
 // Unsigned integers in the order of the floats (-inf is the least, above 0); -0 equals +0.
 __device__ __forceinline__ uint32_t ordered(float r) {

@@ -238,31 +238,6 @@ __device__ __forceinline__ float min_nan(float a, float b, float c) {  // NaN if
   return r;
 }
 
-// Two f32 in a register pair: one instruction for both.
-using F2 = unsigned long long;
-__device__ __forceinline__ F2 f2(float a, float b) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void split(F2 x, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 // bits with x's sign behind them
 __device__ __forceinline__ uint32_t push_sign(uint32_t bits, float x) {
   return __funnelshift_l(__float_as_uint(x), bits, 1);
@@ -577,12 +552,12 @@ __global__ void __launch_bounds__(THREADS, blocks_of_sm(MODE)) route_pairs_kerne
           for (int c = 0; c < C; ++c) shift = fmaxf(shift, x[c]);
           shift = token_max<LANES>(shift);
           if (shift == -INFINITY) shift = 0.0f;
-          const float offset = -shift * LOG2E;
 #pragma unroll
-          for (int c = 0; c < C; ++c) {
-            s[c] = exp2_fast(fmaf(x[c], LOG2E, offset));
+          for (int c = 0; c < C; c += 2) {
+            exp_pair(x[c], x[c + 1], shift, s[c], s[c + 1]);
             sum += s[c];
-            r[c] = x[c];
+            sum += s[c + 1];
+            r[c] = x[c], r[c + 1] = x[c + 1];
           }
           sum = token_sum<LANES>(sum);
           inv = sum == 0.0f ? 0.0f : 1.0f / sum;

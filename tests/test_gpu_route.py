@@ -666,3 +666,104 @@ def test_near_groups_whose_best_have_large_biases_of_opposite_sign(E, G, kg, siz
     for at in range(0, T, 600):
         part = few.forward(x[at:at + 600], bias)
         assert all(torch.equal(part[n], out[n][at:at + 600]) for n in part)
+
+
+def _spread(T, E, seed, std, offset, router, bias, k, G, kg, score):
+    """As _logits, of any spread and place, for the softmax."""
+    x = torch.tensor(np.random.default_rng(seed).normal(size=(8 * T + 40, E)) * std + offset).float()
+    keep = O.select(x.double().numpy(), bias, router, k, G, kg, score)[1] > 1e-5
+    x = x[torch.tensor(keep)][:T]
+    assert x.shape[0] == T
+    return x.contiguous().cuda(), x.double().numpy()
+
+
+SPREADS = [(1.5, 0.0), (3.0, 300.0), (8.0, 0.0), (1.5, -1000.0), (1.5, 20000.0)]
+
+
+@pytest.mark.parametrize("E,k,G,kg,score", [(64, 6, 8, 3, MAX), (160, 6, 8, 3, MAX), (222, 8, 6, 3, MAX), (256, 8, 1, 1, MAX),
+                                            (384, 8, 8, 4, MAX), (1024, 12, 8, 4, MAX)])
+@pytest.mark.parametrize("std,offset", SPREADS)
+@pytest.mark.parametrize("renorm", [False, True])
+def test_softmax_gates_of_wide_and_shifted_logits(E, k, G, kg, score, std, offset, renorm):
+    """Gates are e^(x - max) over one sum, whatever the largest logit is and however many tokens a call has.  A score's
+    exponent (x - max) log2 e is rounded twice on top: 2^-23 of its size."""
+    x, x64 = _spread(40, E, 23, std, offset, SOFTMAX, None, k, G, kg, score)
+    idx, _ = O.select(x64, None, SOFTMAX, k, G, kg, score)
+    s = O.scores(x64, SOFTMAX)
+    away = x64.max(axis=1, keepdims=True) - x64
+    for T in (40, _many(E) + 3):
+        of = np.arange(T) % 40
+        desc = mok.make_route_desc(T, E, k, SOFTMAX, renorm, route_scale=2.5, n_group=G, topk_group=kg, group_score=score,
+                                   balance_coef=0.3)
+        rows = x[torch.tensor(of).cuda()]
+        plain = mok.Router(desc).forward(rows)
+        full = mok.Router(desc, balance=True, scores=True).forward(rows)
+        for out in (plain, full):
+            assert np.array_equal(out["topk_idx"].cpu().numpy(), idx[of])
+            assert np.allclose(f64(out["gates"]), O.gates(s, idx, renorm, 2.5)[of], rtol=REL, atol=1e-37)
+        assert (np.abs(f64(full["scores"]) - s[of]) <= (REL + 2.0 ** -23 * away[of]) * s[of] + 1e-37).all()
+        prob = s[of].sum(axis=0)
+        assert (np.abs(f64(full["prob_sum"]) - prob) <= REL * prob + (2.0 ** -23 * away * s)[of].sum(axis=0) + T * 1e-37).all()
+
+
+@pytest.mark.parametrize("E,k,G,kg,score", [(64, 6, 8, 3, MAX), (222, 8, 6, 3, TOP2), (256, 8, 8, 4, TOP2), (384, 8, 8, 4, MAX)])
+def test_sigmoid_gates_of_many_tokens_without_renormalisation(E, k, G, kg, score):
+    for with_bias in (False, True):
+        bias = _bias(E, 15, with_bias)
+        x, x64 = _logits(40, E, 19, torch.float32, SIGMOID, bias, k, G, kg, score)
+        idx, _ = O.select(x64, bias, SIGMOID, k, G, kg, score)
+        T = _many(E) + 3
+        of = np.arange(T) % 40
+        desc = mok.make_route_desc(T, E, k, SIGMOID, False, route_scale=2.5, n_group=G, topk_group=kg, group_score=score)
+        for scores in (False, True):
+            out = mok.Router(desc, scores=scores).forward(x[torch.tensor(of).cuda()], _cuda(bias))
+            assert np.array_equal(out["topk_idx"].cpu().numpy(), idx[of])
+            assert np.allclose(f64(out["gates"]), O.gates(O.scores(x64, SIGMOID), idx, False, 2.5)[of], rtol=REL, atol=0)
+
+
+@pytest.mark.parametrize("E,k", [(24, 3), (61, 4), (160, 6), (256, 8), (500, 9), (1024, 16)])
+@pytest.mark.parametrize("std,offset", SPREADS)
+@pytest.mark.parametrize("renorm", [False, True])
+def test_softmax_backward_of_wide_and_shifted_logits(E, k, std, offset, renorm):
+    """f32 gradients at the selected experts and at the others, to 2^-18 of their terms, and 2^-23 more for each unit
+    that a logit lies below the largest."""
+    T = 50
+    rng = np.random.default_rng(29)
+    x = torch.tensor(rng.normal(size=(T, E)) * std + offset).float()
+    x64 = x.double().numpy()
+    idx = np.argsort(-x64, axis=1, kind="stable")[:, :k].astype(np.int32)
+    s, away = O.scores(x64, SOFTMAX), x64.max(axis=1, keepdims=True) - x64
+    S = np.take_along_axis(s, idx.astype(np.int64), 1).sum(1, keepdims=True)
+    r = mok.Router(mok.make_route_desc(T, E, k, SOFTMAX, renorm, route_scale=2.5))
+    for use in ("gates", "both"):
+        dg = rng.normal(size=(T, k)).astype(np.float32)
+        dp = rng.normal(size=E).astype(np.float32) if use == "both" else None
+        got = f64(r.backward(x.cuda(), _cuda(idx), _cuda(dg), _cuda(dp)))
+        want = O.backward(x64, idx, dg.astype(np.float64), None if dp is None else dp.astype(np.float64), SOFTMAX, renorm, 2.5)
+        both = np.zeros((T, E))
+        np.put_along_axis(both, idx.astype(np.int64), 2.5 * (np.abs(dg) + np.abs(dg).max(1, keepdims=True) * renorm) /
+                          (S if renorm else 1.0), 1)
+        both = both if dp is None else both + np.abs(dp) + np.abs(dp).max()
+        more = REL + 2.0 ** -23 * away
+        tol = s * (more * both + (s * more * both).sum(1, keepdims=True) + more * (s * both).sum(1, keepdims=True)) + 1e-36
+        assert (np.abs(got - want) <= tol).all(), (use, (np.abs(got - want) / tol).max())
+
+
+@pytest.mark.parametrize("E,k", [(24, 3), (160, 6), (256, 8), (500, 9)])
+def test_sigmoid_backward_without_renormalisation(E, k):
+    T = 50
+    rng = np.random.default_rng(31)
+    x = torch.tensor(rng.normal(size=(T, E)) * 1.5).float()
+    x64 = x.double().numpy()
+    idx = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    dg, dp = rng.normal(size=(T, k)).astype(np.float32), rng.normal(size=E).astype(np.float32)
+    s = O.scores(x64, SIGMOID)
+    for p in (None, dp):
+        got = f64(mok.Router(mok.make_route_desc(T, E, k, SIGMOID, False, route_scale=2.5)).backward(
+            x.cuda(), _cuda(idx), _cuda(dg), _cuda(p)))
+        want = O.backward(x64, idx, dg.astype(np.float64), None if p is None else p.astype(np.float64), SIGMOID, False, 2.5)
+        both = np.zeros((T, E))
+        np.put_along_axis(both, idx.astype(np.int64), 2.5 * np.abs(dg), 1)
+        if p is not None:
+            both += (np.abs(p) + np.abs(p).max()) / s.sum(1, keepdims=True)
+        assert (np.abs(got - want) <= REL * s * both + 1e-38).all()
