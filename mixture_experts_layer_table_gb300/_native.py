@@ -124,6 +124,13 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _settle(device):
+    """Waits until what the current stream was given so far is done: buffers that an object fills when it is made (a
+    workspace's zeros, first states) are then ready for calls on any stream.  Under capture the graph keeps the order."""
+    if torch.device(device).type == "cuda" and not torch.cuda.is_current_stream_capturing():
+        torch.cuda.current_stream(device).synchronize()
+
+
 def _check(fn: str, code: int):
     if code != MOK_OK:
         raise MokError(fn, code)

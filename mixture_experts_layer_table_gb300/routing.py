@@ -11,7 +11,7 @@ from typing import Dict, Optional
 
 import torch
 
-from ._native import _check, _expect, _stream, load
+from ._native import _check, _expect, _settle, _stream, load
 
 P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 
@@ -69,7 +69,8 @@ def _address(t, shape, dtype, name):
 
 
 class Router:
-    """One routing descriptor with its output buffers, which each call overwrites.
+    """One routing descriptor with its output buffers, which each call overwrites.  Making one with ``balance`` waits for
+    the current stream, so that its zero-filled workspace is ready on every stream.
 
     ``forward`` returns {"topk_idx", "gates"}, with ``scores`` also "scores", and with ``balance``
     also "counts", "prob_sum", "loss", "dprob" and, where a bias is given, "bias_next"."""
@@ -91,6 +92,7 @@ class Router:
         if balance:
             self.out |= {"counts": new((E,), torch.int32), "prob_sum": new((E,)), "loss": new((1,)), "dprob": new((E,))}
             self.ws = torch.zeros(ROUTE_WS_BYTES, dtype=torch.uint8, device=device)
+            _settle(device)
         self.bias_next = new((E,)) if balance else None
         address = lambda t: None if t is None else t.data_ptr()  # noqa: E731
         self._args = tuple(address(self.out.get(n))

@@ -4,7 +4,9 @@ factor, and AdamW over many tensors.
 As in ``_native``: argument marshalling only, every step runs in the library's CUDA kernels, the
 stream is PyTorch's current stream unless given, and there is no fallback.  ``GradNorm`` and
 ``AdamW`` are made once for a set of buffers that a training loop keeps (the parameters and the
-gradient buffers that ``MoELayer.backward(out=...)`` writes); they hold references to them.
+gradient buffers that ``MoELayer.backward(out=...)`` writes); they hold references to them.  Making one
+waits for the current stream, so that the buffers it fills (a workspace, first states, f32 copies) are
+ready on every stream.
 """
 from __future__ import annotations
 
@@ -13,7 +15,7 @@ from typing import Dict, List, Optional, Sequence
 
 import torch
 
-from ._native import _check, _stream, load
+from ._native import _check, _settle, _stream, load
 
 P, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
 
@@ -97,6 +99,7 @@ class GradNorm:
         device = self.grads[0].device if self.grads else torch.device("cuda")
         self.result = torch.empty(2, dtype=torch.float32, device=device)
         self.ws = torch.zeros(GRAD_NORM_WS_BYTES, dtype=torch.uint8, device=device)
+        _settle(device)
         self._call = _grad_norm_fn()
         self._out, self._ws = self.result.data_ptr(), self.ws.data_ptr()
 
@@ -167,6 +170,8 @@ class AdamW:
         lrs, decays = each(lr, "lr"), each(weight_decay, "weight_decay")
         if len(lrs) != count or len(decays) != count:
             raise ValueError("lr and weight_decay: one number, or one for each parameter")
+        if params:
+            _settle(params[0].device)
         self._table = (AdamWTensor * max(1, count))()
         ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
         for i, p in enumerate(params):

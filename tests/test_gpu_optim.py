@@ -380,3 +380,34 @@ def test_grad_norm_of_nothing_and_of_non_finite():
         g[777] = bad
         got = f64(mok.GradNorm([g], 1.0).compute())
         assert not np.isfinite(got[0]) and np.isnan(got[1])
+
+
+def test_what_the_constructors_fill_is_ready_on_another_stream():
+    """The current stream is busy when the objects are made, in memory that was not zero; their first calls go to another
+    stream at once."""
+    params, grads = _tensors((5000,), torch.bfloat16, 0.05, 91), _tensors((5000,), torch.float32, 1e-3, 92)
+    want_norm = mok.GradNorm(grads, 0.5).compute().clone()
+    want = {}
+    for state in ("f32", "mx8"):
+        p = [params[0].clone()]
+        opt = mok.AdamW(p, grads, state=state, masters=True, **HYPER)
+        opt.step()
+        want[state] = [p[0], opt.masters[0], *[s[0].view(torch.uint8) for s in opt.states.values()]]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for n in (16640, 5000 * 4, 5000, 157):
+        torch.full((n,), 0xff, dtype=torch.uint8, device="cuda")
+    copies = [params[0].clone() for _ in want]
+    torch.cuda._sleep(40_000_000)
+    norm = mok.GradNorm(grads, 0.5)
+    assert torch.cuda.current_stream().query()
+    norm.compute(side)
+    side.synchronize()
+    assert torch.equal(norm.result, want_norm)
+    for (state, w), copy in zip(want.items(), copies):
+        torch.cuda._sleep(40_000_000)
+        opt = mok.AdamW([copy], grads, state=state, masters=True, **HYPER)
+        assert torch.cuda.current_stream().query()
+        opt.step(stream=side)
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(w, [copy, opt.masters[0], *[s[0].view(torch.uint8) for s in opt.states.values()]]))

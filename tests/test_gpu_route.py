@@ -767,3 +767,20 @@ def test_sigmoid_backward_without_renormalisation(E, k):
         if p is not None:
             both += (np.abs(p) + np.abs(p).max()) / s.sum(1, keepdims=True)
         assert (np.abs(got - want) <= REL * s * both + 1e-38).all()
+
+
+def test_a_new_workspace_is_ready_on_another_stream():
+    """The current stream is busy when the router is made, in memory that was not zero; its first call goes to another."""
+    T, E, k = 300, 64, 4
+    x = torch.randn(T, E, generator=torch.Generator().manual_seed(6)).cuda()
+    desc = mok.make_route_desc(T, E, k, SIGMOID, True, n_group=8, topk_group=4, balance_coef=1.0)
+    want = {n: t.clone() for n, t in mok.Router(desc, balance=True).forward(x).items()}
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.full((98560,), 0xff, dtype=torch.uint8, device="cuda")
+    torch.cuda._sleep(40_000_000)
+    r = mok.Router(desc, balance=True)
+    assert torch.cuda.current_stream().query()
+    out = r.forward(x, stream=side)
+    side.synchronize()
+    assert all(torch.equal(out[n], want[n]) for n in want)
