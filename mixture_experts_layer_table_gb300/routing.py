@@ -49,21 +49,29 @@ def _route_backward_fn():
     return fn
 
 
-def _rows(t, T, E, dtype, name) -> int:
-    """Row stride of a [T][E] CUDA tensor whose rows are contiguous."""
+def _rows(t, T, E, dtype, name, device) -> int:
+    """Row stride of a [T][E] CUDA tensor on this device whose rows are contiguous."""
     if t.shape != (T, E) or t.dtype != dtype:
         raise ValueError(f"{name}: expected ({T}, {E}) {dtype}, got {tuple(t.shape)} {t.dtype}")
     if t.device.type != "cuda":
         raise ValueError(f"{name} must be a CUDA tensor")
+    _same_device(t, name, device)
     if T > 1 and (t.stride(1) != 1 and E > 1 or t.stride(0) < E) or T == 1 and E > 1 and t.stride(1) != 1:
         raise ValueError(f"{name}: rows must be contiguous and must not overlap, got strides {t.stride()}")
     return t.stride(0) if T > 1 else E
 
 
-def _address(t, shape, dtype, name):
-    """The address of a contiguous CUDA tensor of this shape and type."""
-    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.is_cuda and t.is_contiguous()):
+def _same_device(t, name, device):
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the router's buffers are not")
+
+
+def _address(t, shape, dtype, name, device):
+    """The address of a contiguous CUDA tensor of this shape and type on this device (its index)."""
+    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.get_device() == device and
+            t.is_contiguous()):
         _expect(t, shape, dtype, name)
+        _same_device(t, name, device)
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
@@ -99,6 +107,7 @@ class Router:
                            for n in ("topk_idx", "gates", "scores", "counts", "prob_sum", "loss", "dprob"))
         self._ws = address(self.ws)
         self._shape, self._sel, self._experts = (T, E), (T, k), (E,)
+        self._device = self.out["gates"].get_device() if self.out["gates"].is_cuda else None  # its index
         self.dlogits = None  # made by the first backward without `out`
         self._ref = ctypes.byref(self.desc)
         self._call = _route_fn()
@@ -110,10 +119,10 @@ class Router:
         self._take_logits(logits)
         out, moved, b = self.out, None, None
         if bias is not None:
-            b = _address(bias, self._experts, torch.float32, "bias")
+            b = _address(bias, self._experts, torch.float32, "bias", self._device)
             if self.balance:
                 to = self.bias_next if bias_next is None else bias_next
-                moved = _address(to, self._experts, torch.float32, "bias_next")
+                moved = _address(to, self._experts, torch.float32, "bias_next", self._device)
                 out = dict(out, bias_next=to)
         code = self._call(self._ref, logits.data_ptr(), b, *self._args, moved, self._ws, ROUTE_WS_BYTES,
                           _stream(stream))
@@ -129,19 +138,20 @@ class Router:
         self._take_logits(logits)
         idx = dg = dp = status = None
         if dgates is not None:
-            dg = _address(dgates, self._sel, torch.float32, "dgates")
-            idx = _address(topk_idx, self._sel, torch.int32, "topk_idx")
+            dg = _address(dgates, self._sel, torch.float32, "dgates", self._device)
+            idx = _address(topk_idx, self._sel, torch.int32, "topk_idx", self._device)
         if dprob is not None:
-            dp = _address(dprob, self._experts, torch.float32, "dprob")
+            dp = _address(dprob, self._experts, torch.float32, "dprob", self._device)
         if device_status is not None:
-            status = _address(device_status, (2,), torch.int32, "device_status")
+            status = _address(device_status, (2,), torch.int32, "device_status", self._device)
         stride = 0
         if out is None:  # 5 us of a call less than a new tensor
             if self.dlogits is None:
                 self.dlogits = torch.empty(self._shape, dtype=self.dtype, device=logits.device)
             out = self.dlogits
-        elif not (out.shape == self._shape and out.dtype is self.dtype and out.is_cuda and out.is_contiguous()):
-            stride = _rows(out, *self._shape, self.dtype, "out")
+        elif not (out.shape == self._shape and out.dtype is self.dtype and out.get_device() == self._device and
+                  out.is_contiguous()):
+            stride = _rows(out, *self._shape, self.dtype, "out", self._device)
         code = self._call_backward(self._ref, logits.data_ptr(), idx, dg, dp, out.data_ptr(), stride, status,
                                    _stream(stream))
         if code:
@@ -149,7 +159,8 @@ class Router:
         return out
 
     def _take_logits(self, logits):
-        if logits.shape == self._shape and logits.dtype is self.dtype and logits.is_cuda and logits.is_contiguous():
+        if (logits.shape == self._shape and logits.dtype is self.dtype and logits.get_device() == self._device and
+                logits.is_contiguous()):
             self.desc.logits_stride = 0
         else:
-            self.desc.logits_stride = _rows(logits, *self._shape, self.dtype, "logits")
+            self.desc.logits_stride = _rows(logits, *self._shape, self.dtype, "logits", self._device)

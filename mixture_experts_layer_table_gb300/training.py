@@ -172,6 +172,7 @@ class AdamW:
             raise ValueError("lr and weight_decay: one number, or one for each parameter")
         if params:
             _settle(params[0].device)
+            self._device = params[0].get_device()
         self._table = (AdamWTensor * max(1, count))()
         ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
         for i, p in enumerate(params):
@@ -216,6 +217,8 @@ class AdamW:
         if grad_scale is not None:
             if not (grad_scale.dtype is torch.float32 and grad_scale.is_cuda and grad_scale.numel() == 1):
                 _expect_tensor(grad_scale, "grad_scale", (torch.float32,), 1)
+            if self.params and grad_scale.get_device() != self._device:
+                raise ValueError(f"grad_scale is on {grad_scale.device}, the parameters are not")
             scale = grad_scale.data_ptr()
         self._hyper.step += 1
         code = self._call(self._table, len(self.params), self._hyper_ref, scale, _stream(stream))

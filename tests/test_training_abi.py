@@ -153,3 +153,39 @@ def test_the_router_binding_refuses_mismatches(lib):
         r.forward(torch.zeros(4, 8).bfloat16())
     with pytest.raises(ValueError, match="float32 or bfloat16"):
         mok.Router(mok.make_route_desc(4, 8, 2, 1, True), dtype=torch.float16, device="cpu")
+
+
+class _OnGpu:
+    """What the binding looks at of a CUDA tensor, with an address that is none."""
+
+    def __init__(self, shape, dtype=torch.float32, index=0):
+        self.shape, self.dtype, self.is_cuda, self.device = torch.Size(shape), dtype, True, torch.device("cuda", index)
+
+    def get_device(self):
+        return self.device.index
+
+    def is_contiguous(self):
+        return True
+
+    def stride(self, i):
+        return self.shape[1] if i == 0 else 1
+
+    def data_ptr(self):
+        return 0x100000
+
+
+def test_the_router_binding_refuses_another_device_than_its_buffers(lib, monkeypatch):
+    """Buffers on the CPU or on another GPU, logits on this one: their addresses do not go to the kernel."""
+    from mixture_experts_layer_table_gb300 import routing as RT
+    monkeypatch.setattr(RT, "_stream", lambda s: None)
+    r = mok.Router(mok.make_route_desc(4, 8, 2, 1, True), device="cpu")
+    monkeypatch.setattr(r, "_call", lambda *a: pytest.fail("called"))
+    monkeypatch.setattr(r, "_call_backward", lambda *a: pytest.fail("called"))
+    for call in (lambda: r.forward(_OnGpu((4, 8))), lambda: r.backward(_OnGpu((4, 8)), None, None)):
+        with pytest.raises(ValueError, match="logits is on cuda:0"):
+            call()
+    r._device = 1                                            # as of buffers on a second GPU
+    with pytest.raises(ValueError, match="logits is on cuda:0"):
+        r.forward(_OnGpu((4, 8)))
+    with pytest.raises(ValueError, match="out is on cuda:0"):
+        r.backward(_OnGpu((4, 8), index=1), None, None, out=_OnGpu((4, 8)))
