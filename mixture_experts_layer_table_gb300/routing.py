@@ -115,7 +115,9 @@ class Router:
 
     def forward(self, logits: torch.Tensor, bias: Optional[torch.Tensor] = None,
                 bias_next: Optional[torch.Tensor] = None, stream=None) -> Dict[str, torch.Tensor]:
-        """``bias_next``: where the moved bias goes (with ``balance``), e.g. ``bias`` itself."""
+        """``bias_next``: where the moved bias goes (with ``balance`` and a bias), e.g. ``bias`` itself."""
+        if bias_next is not None and (bias is None or not self.balance):
+            raise ValueError("bias_next needs a bias and a router with balance")
         self._take_logits(logits)
         out, moved, b = self.out, None, None
         if bias is not None:

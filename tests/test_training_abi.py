@@ -189,3 +189,15 @@ def test_the_router_binding_refuses_another_device_than_its_buffers(lib, monkeyp
         r.forward(_OnGpu((4, 8)))
     with pytest.raises(ValueError, match="out is on cuda:0"):
         r.backward(_OnGpu((4, 8), index=1), None, None, out=_OnGpu((4, 8)))
+
+
+def test_the_router_binding_refuses_a_moved_bias_that_nothing_would_move(lib, monkeypatch):
+    from mixture_experts_layer_table_gb300 import routing as RT
+    monkeypatch.setattr(RT, "_stream", lambda s: None)
+    b = _OnGpu((8,))
+    for balance, bias in ((False, b), (True, None), (False, None)):
+        r = mok.Router(mok.make_route_desc(4, 8, 2, 1, True), balance=balance, device="cpu")
+        r._device = 0
+        monkeypatch.setattr(r, "_call", lambda *a: pytest.fail("called"))
+        with pytest.raises(ValueError, match="bias_next"):
+            r.forward(_OnGpu((4, 8)), bias, bias_next=b)
