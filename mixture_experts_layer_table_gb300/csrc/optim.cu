@@ -321,11 +321,13 @@ struct Mx8Constants {
   uint32_t seed;
 };
 __device__ __forceinline__ Mx8Constants mx8_constants_of(const AdamHyper& h, const AdamTensor& T, float c) {
-  // without a rate the divisor is as large as can be, and the quotient 0
+  // without a rate, or with one that f32 cannot divide by, the divisor is as large as can be, and the quotient 0 (an
+  // infinite one would make NaN of a root that is 0)
   const float rate = -T.lr * h.inv_bc1;
   const bool none = rate == 0.0f;
-  return {h.beta1, h.beta2_sqrt, c * h.one_minus_beta1, c * h.one_minus_beta2_sqrt, none ? FLT_MAX : h.inv_bc2_sqrt / rate,
-          none ? FLT_MAX : h.eps / rate, -T.lr * T.weight_decay, h.seed};
+  auto over_rate = [&](float x) { return none ? FLT_MAX : fminf(fmaxf(x / rate, -FLT_MAX), FLT_MAX); };
+  return {h.beta1, h.beta2_sqrt, c * h.one_minus_beta1, c * h.one_minus_beta2_sqrt, over_rate(h.inv_bc2_sqrt),
+          over_rate(h.eps), -T.lr * T.weight_decay, h.seed};
 }
 
 // The 8-bit-state step of elements i .. i + 7 (`left` of them in range) on values that were loaded: parameters,

@@ -291,6 +291,29 @@ def test_adamw_a_scale_byte_of_255_is_not_finite():
         assert _same(opt.states[n][0].view(torch.uint8)[~hit], clean.states[n][0].view(torch.uint8)[~hit])
 
 
+@pytest.mark.parametrize("state", ["f32", "mx8"])
+@pytest.mark.parametrize("pk", ["f32", "master"])
+@pytest.mark.parametrize("lr", [1e-30, 1e-37, 2e-38, 1e-39, 1e-44, 0.0])
+def test_adamw_rates_down_to_zero(state, pk, lr):
+    """The end of a schedule: rates near and below the least normal f32 number move a parameter by no more than its last
+    place, and one of zero by as little as themselves (a step's quotient is at most 1 / sqrt(1 - beta2) < 5, doubled for
+    the roundings); nothing is divided by a rate that is too small for it."""
+    n = 100
+    params = [torch.zeros(n, device="cuda"), torch.full((n,), 0.75, device="cuda")]
+    if pk == "master":
+        params = [p.bfloat16() for p in params]
+    grads = [torch.zeros(n, device="cuda") for _ in params]
+    for g in grads:
+        g[50:] = torch.linspace(-1e-3, 1e-3, 50, device="cuda")
+    opt = mok.AdamW(params, grads, lr=lr, weight_decay=0.1, state=state, masters=True if pk == "master" else None, **HYPER)
+    for _ in range(3):
+        opt.step()
+    held = params if pk == "f32" else opt.masters
+    assert held[0].abs().max().item() <= 3 * 10 * lr + 1e-37
+    assert torch.equal(held[1], torch.full((n,), 0.75, device="cuda"))
+    assert all(torch.isfinite(opt.state_values(i)[s]).all() for i in (0, 1) for s in ("m", "v"))
+
+
 def test_adamw_states_in_8_bits_follow_the_32_bit_ones():
     """With steps far below a grid spacing (beta2 = 0.999) the 8-bit states keep moving with the f32 ones: over
     4096 elements the mean of sqrt(v) and of m stay together.  sqrt(v) wanders by a random rounding of up to
