@@ -430,8 +430,10 @@ typedef struct {
  * factor that clips them to max_norm (> 0, may be infinite), or NaN where the norm is not finite.
  * out is f32 [2] on the device.  ws: at least MOK_GRAD_NORM_WS_BYTES, 16-byte aligned, zero-filled
  * once before its first use (each call leaves it ready for the next; calls that may overlap need one
- * each).  The squares are formed and added in f32, the blocks' sums in f64, in a fixed order; a
- * gradient above 1.8e19 in magnitude makes the norm infinite. */
+ * each).  The squares are formed and added in f32, the blocks' sums in f64, in a fixed order; a block
+ * whose squares pass f32's range is taken again in a smaller unit, so that every norm below 3.4e38 is
+ * found.
+ * Squares have f32's lower end: below gradients of 1e-19 they lose bits, below 2.6e-23 they are 0. */
 #define MOK_GRAD_NORM_WS_BYTES 16640
 mok_status mok_grad_norm(const mok_grad_tensor* tensors, int32_t count, float max_norm, float* out, void* ws,
                          size_t ws_bytes, void* stream);

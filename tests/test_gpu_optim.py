@@ -405,6 +405,33 @@ def test_grad_norm_of_nothing_and_of_non_finite():
         assert not np.isfinite(got[0]) and np.isnan(got[1])
 
 
+@pytest.mark.parametrize("size,n", [(1e18, 100003), (5e18, 40), (1e19, 16384 * 3), (3e19, 100003), (1e25, 7), (1e30, 50000),
+                                    (3e38, 1)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_grad_norm_of_large_gradients(size, n, dtype):
+    """Finite gradients whose squares, or their sum, pass f32's range: the norm is theirs as long as it is below 3.4e38
+    itself.  As above within 2^-20: sums in f32 over at most a few thousand squares of a thread, one root rounded to f32."""
+    grads = _tensors((1000,), torch.float32, 1e-3, 81) + [torch.full((n,), size, dtype=dtype, device="cuda")]
+    grads[1][::3].neg_()
+    norm = mok.GradNorm(grads, 1.0)
+    want = O.grad_norm([f64(g) for g in grads], 1.0)
+    first = norm.compute().clone()
+    got = f64(first)
+    assert abs(got[0] - want[0]) <= 2.0 ** -20 * want[0]
+    assert abs(got[1] - want[1]) <= 2.0 ** -20 * want[1] + 2.0 ** -149
+    assert torch.equal(norm.compute(), first)
+    grads[1][n // 2] = float("nan")
+    assert torch.isnan(norm.compute()).all()
+    grads[1][n // 2] = -float("inf")
+    got = f64(norm.compute())
+    assert np.isposinf(got[0]) and np.isnan(got[1])
+
+
+def test_grad_norm_past_f32_is_infinite():
+    got = f64(mok.GradNorm([torch.full((2,), 3e38, device="cuda")], 1.0).compute())
+    assert np.isposinf(got[0]) and np.isnan(got[1])
+
+
 def test_what_the_constructors_fill_is_ready_on_another_stream():
     """The current stream is busy when the objects are made, in memory that was not zero; their first calls go to another
     stream at once."""
