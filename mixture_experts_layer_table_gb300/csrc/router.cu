@@ -233,12 +233,6 @@ __device__ __forceinline__ void sigmoid_and_slope(float x, float& s, float& slop
 // four sums over the lanes) that 16 to 24 warps an SM cover in 58% of the cycles; 4,096 tokens of 256: 3.7 us.
 // Q: words of a lane.  DENSE: the row's scores are needed (softmax, or dprob); without it the row is zero but for the
 // selected experts, whose logits alone are read.
-__device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-  const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-  return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
-                     __uint_as_float(v.y & 0xffff0000u));
-}
 __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
 __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
   const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
@@ -252,10 +246,9 @@ __device__ __forceinline__ void sigmoid_and_slope_fast(float x, float& s, float&
   slope = e * f * f;
 }
 
-// Experts e .. e + 3 of a row, -inf beyond E.
+// Experts e .. e + 3 of a row that is not aligned, -inf beyond E.
 template <typename TL>
-__device__ __forceinline__ float4 load_word(const TL* row, int e, int E, bool wide) {
-  if (wide && e < E) return load4(row + e);
+__device__ __forceinline__ float4 load_word(const TL* row, int e, int E) {
   return make_float4(e < E ? to_f32(row[e]) : -INFINITY, e + 1 < E ? to_f32(row[e + 1]) : -INFINITY,
                      e + 2 < E ? to_f32(row[e + 2]) : -INFINITY, e + 3 < E ? to_f32(row[e + 3]) : -INFINITY);
 }
@@ -369,7 +362,7 @@ __global__ void __launch_bounds__(THREADS, backward_blocks(Q, DENSE)) route_back
       for (int i = 0; i < Q; ++i) {
         const int at = 4 * (part + LANES * i);
         if (ringed) s[i] = at < E ? unpack_word(words[i * 32 + lane]) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-        else s[i] = load_word(from, at, E, false);
+        else s[i] = load_word(from, at, E);
       }
     }
 #pragma unroll
