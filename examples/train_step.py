@@ -1,10 +1,12 @@
-"""A training loop of one group-limited mixture-of-experts layer, every step on the library's kernels.
+"""A training loop of one group-limited mixture-of-experts layer on the library's kernels.
 
     python examples/train_step.py [--steps N] [--state f32|mx8]
 
 Each step: the layer's forward (experts chosen within the best groups, selection moved by a bias), its
 backward, the balance loss and its gradient through the router logits, the global gradient norm, and one
-AdamW step of all weights on the clipped gradients.  The layer learns to reproduce another layer of the
+AdamW step of all weights on the clipped gradients.  The balance loss is not the layer's: its gradient comes as
+that of the logits, and two products of PyTorch's add it to the gradients of the router's weights and of the
+layer's input (which a layer below this one would take).  The layer learns to reproduce another layer of the
 same shape (random weights); the expert loads are kept together by the balance loss and by the bias that
 moves after each step.
 """
@@ -52,11 +54,13 @@ class Trainer:
         diff = y.float() - target.float()
         dy = (diff * (2.0 / diff.numel())).bfloat16()
         self.layer.backward(dy, x, w["w_router"], w["w13"], w["w2"], out=self.grads)
-        # balance: loads and probabilities of the layer's own logits; its gradient joins the router's weights
+        # balance: loads and probabilities of the layer's own logits; its gradient joins that of the router's weights and
+        # that of the input
         logits = self.layer.view("logits")
         stats = self.router.forward(logits, self.bias, bias_next=self.bias)
         dlogits = self.router.backward(logits, None, None, stats["dprob"])
         self.grads["dw_router"] += dlogits.T @ x.float()
+        self.grads["dx"].copy_(self.grads["dx"].float() + dlogits @ w["w_router"].float())
         norm = self.norm.compute()
         self.opt.step(norm[1:])
         return {"mse": diff.square().mean(), "balance": stats["loss"][0].clone(), "norm": norm[0].clone(),

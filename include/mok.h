@@ -408,7 +408,10 @@ mok_status mok_route(const mok_route_desc* desc, const void* logits, const float
  * prob_sum; either gradient may be NULL (topk_idx too without dgates), not both.  The selection is
  * held fixed, the bias gets no gradient.  An index outside [0, E) is left out and reported as
  * (MOK_ERR_INVALID_ROUTING, site) in device_status, a DEVICE buffer of 2 int32 that the caller has
- * cleared, or NULL. */
+ * cleared, or NULL.
+ * With the layer: mok_moe_backward's router gradient is that of its gates alone.  The balance loss's
+ * gradient of the logits (dgates NULL) is added to its outputs by the caller: dw_router += dlogits^T x and
+ * dx += dlogits w_router (examples/train_step.py). */
 mok_status mok_route_backward(const mok_route_desc* desc, const void* logits, const int32_t* topk_idx,
                               const float* dgates, const float* dprob, void* dlogits, int64_t dlogits_stride,
                               int32_t* device_status, void* stream);
