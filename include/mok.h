@@ -34,6 +34,9 @@
  *     counters from which the expert GEMMs and weight-gradient kernels take their tiles
  *     (cleared by each call); two overlapping calls on one `ws` would share them and skip
  *     tiles.
+ *   - The descriptors carry neither their size nor a version, and grow at their ends: a caller is
+ *     compiled with the header of the library that it loads, and zero-fills what it does not set
+ *     (the last fields of mok_layer_desc are n_group, topk_group and group_score).
  *   - No C++ exception crosses this boundary.  No global mutable state besides per-device
  *     caches of the SM count and of how many CTA pairs of each pair kernel fit at once, the
  *     driver entry point used to encode TMA descriptors, the optional per-kernel trace

@@ -99,7 +99,7 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, uint32_t i, int left, c
 }
 
 // 32 bits for each of the 8 elements of a counter group: MurmurHash3's 32-bit finaliser (A. Appleby) of the
-// group's number and the step's seed, times one odd number each.
+// group's number and the step's seed, times one odd number each (the first five are the primes of XXH32, Y. Collet).
 __device__ __forceinline__ void rounding_bits(uint64_t group, uint32_t seed, uint32_t (&z)[VEC]) {
   uint32_t x = (uint32_t)group ^ ((uint32_t)(group >> 32) * 0x9E3779B1u) ^ seed;
   x = (x ^ (x >> 16)) * 0x85EBCA6Bu;
@@ -222,16 +222,18 @@ __device__ __forceinline__ void store_e4m3(uint8_t* q, uint32_t i, int left, con
 // grid is 6% to 12% wide: rounded to nearest, a state would never move again, so both are rounded up or down
 // at random with the mean unchanged.  sqrt(v) > 0 never becomes 0, so that no step divides by eps alone.
 // bf16 parameters without an f32 master are rounded the same way (their updates are below half a spacing too).
+// What is not finite shows in its own element: NaN stays NaN in a bf16 parameter, and an m or sqrt(v) that is not finite
+// is an E4M3 NaN that its block's scale does not see.
 // A clip factor c that is NaN leaves the tensor as it is (grad_norm gives one for gradients that are not finite).
 //
 // 8 consecutive elements to a thread (16 bytes of bf16, 32 of f32; four threads hold a block of 32), 2048 to a
 // pass of the block.  With f32 states the step is bound by DRAM and keeps IEEE roots and divisions: bf16 parameters
 // with masters and f32 gradients, 30 bytes an element, 354 million elements in 1.48 ms, 7.16 TB/s, issue slots 28%
-// full; 96 tensors of 1 to 30,011 elements (8 MB, from L2) 5.5 us.  With 8-bit states it moves 10 to 18 bytes an
+// full; 96 tensors of 1 to 30,011 elements (8 MB, from L2) 5.7 us.  With 8-bit states it moves 10 to 18 bytes an
 // element and issue decides (plain f32: 92 instructions an element, 0.98 ms for those 354 million elements at 10.1
 // bytes), so it runs on packed f32 pairs with approximate roots and reciprocals (2^-22; v below 2^-126 counts as 0)
-// and rounds without conversions to and from integers: 52 instructions an element, 81% of the issue slots, 0.573 ms,
-// 6.25 TB/s; with masters or f32 gradients 6.9 to 7.0 TB/s.
+// and rounds without conversions to and from integers: 53 instructions an element, 83% of the issue slots, 0.567 ms,
+// 6.32 TB/s; with masters or f32 gradients 6.9 to 7.1 TB/s.
 struct AdamConstants {
   float c, beta1, one_minus_beta1, beta2, one_minus_beta2, eps, inv_bc1, inv_bc2_sqrt, lr, weight_decay;
   uint32_t seed;
@@ -537,7 +539,7 @@ __global__ void __launch_bounds__(MX8_THREADS, 4)
 // block that comes last in the call adds the blocks' sums in f64 in a fixed order, so that the result does not
 // depend on the order of arrival.  Squares below 2^-149, of gradients below 2.6e-23, count as 0.
 // Bound by DRAM reads: 354 million f32 gradients in 0.198 ms, 7.15 TB/s (64 warps an SM in flight, no copy through
-// shared memory); small sets by the launch and the last block's turn: 96 tensors of 1 to 30,011 elements 5.5 us (with
+// shared memory); small sets by the launch and the last block's turn: 96 tensors of 1 to 30,011 elements 5.7 us (with
 // f64 sums within the blocks 8.6).
 __device__ __forceinline__ float warp_total(float x) {
 #pragma unroll

@@ -8,7 +8,9 @@
 //   without a bias); the topk_group best groups stay, then the k best experts in them; ties to the lower index.
 //   gate = scale * s, or scale * s / (the sum of the k selected s), 0 where that sum is 0.
 // A warp keeps its row in registers, so that each round of the top-k is C maxima, one reduction over the warp and one
-// ballot.  Few tokens are bound by the chain of these steps: 1 token of 256 experts 3.6 us, 1,024 tokens 4.7 us.
+// ballot.  Few tokens are bound by the chain of these steps: 1 token of 256 experts 3.8 us, 8 tokens 4.3, 1,024 tokens
+// 4.7.  Many tokens come here only where the other kernel has no form: a softmax with a bias (65,536 tokens of 256: 95 us)
+// and more than 512 experts (16,384 tokens of 1,024: 190 us).
 #include <algorithm>
 
 #include "router_common.cuh"
@@ -229,7 +231,7 @@ __device__ __forceinline__ void sigmoid_and_slope(float x, float& s, float& slop
 // in words of 4 experts, lane p the words p, p + LANES, ..., so that a warp's accesses are whole 128-byte (bf16:
 // 64-byte) pieces of its rows and the sums over a token take 3 to 5 exchanges for all its tokens at once; rows that
 // are not aligned are read and written one expert at a time (222 experts, 65,536 tokens: 33 us; 256: 28).
-// 65,536 tokens of 160 experts, softmax: 17.5 us, 5.0 TB/s, bound by the latency of a warp's steps (exponentials and
+// 65,536 tokens of 160 experts, softmax: 17.7 us, 4.9 TB/s, bound by the latency of a warp's steps (exponentials and
 // four sums over the lanes) that 16 to 24 warps an SM cover in 58% of the cycles; 4,096 tokens of 256: 3.7 us.
 // Q: words of a lane.  DENSE: the row's scores are needed (softmax, or dprob); without it the row is zero but for the
 // selected experts, whose logits alone are read.

@@ -15,16 +15,17 @@
 // A token for which this does not do (more than 64 experts listed, too few unmasked) is selected by the whole warp, one
 // expert at a time, by the definition.
 //
-// The next tokens' logits come to shared memory under the arithmetic of these (cp.async; 39 us below without).
+// The next tokens' logits come to shared memory under the arithmetic of these (cp.async; without, the 37 us below are 39).
 //
 // A biased sigmoid is ranked on approximate values, and what those leave open is settled exactly where it arises: on
 // the listed experts if it is an order among them, from the groups on if it is a group (in the whole warp's way, as
 // at first, the code of 10 such tokens in 65,536, cold, was 10 us of a call's 38: a single warp's at the end).
 //
 // 65,536 tokens of 256 experts (f32, sigmoid with a bias, 8 groups): 37 us, 1.9 TB/s; the row is read once, and the
-// bound is instructions (25 million of warps, issued in 62% of the cycles at 24 warps an SM, which wait on one
+// bound is instructions (25 million of warps, issued in 64% of the cycles at 24 warps an SM, which wait on one
 // another's results: shared memory and shuffles between the steps; the SMs' ends lie 15% apart).  4,096 tokens 6 us,
-// with the balance outputs 9.4.
+// with the balance outputs 9.4.  With the scores written, and so formed exactly (as the layer asks for them): 65,536 tokens
+// 50 us, 4,096 tokens 7.8.
 #include <algorithm>
 #include <cfloat>
 #include <cstddef>
@@ -312,9 +313,9 @@ struct Place {
 };
 
 // The selection of a warp's tokens, one on each LANES lanes, from the lanes' rank values r (shift: of each softmax):
-// the experts in pick.  FAST: r is approximate; what that leaves open is settled on exact values,
-// of the token's logits `own` from this lane's first on and their bias.  False (on all lanes of a token): more than the
-// list holds, or too few experts.
+// the experts in pick.  FAST: r is approximate; what that leaves open is settled on exact values, of the token's logits
+// `own` from this lane's first on and their bias.  False (on all lanes of a token): more than the list holds, or too few
+// experts.
 //
 // An approximate rank value v = s + b is off by less than 4e-7 + 2^-23 |v|: the order of two is certain from twice that
 // on, and more is taken.  The distance goes by the value itself: a far larger bias of another expert (the type's lowest
