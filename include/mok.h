@@ -499,6 +499,111 @@ typedef struct {
 mok_status mok_adamw_step(const mok_adamw_tensor* tensors, int32_t count, const mok_adamw_hyper* hyper,
                           const float* grad_scale, void* stream);
 
+/* ------------------------------------------------------------------ experts outside the layer
+ * For experts that are not the layer's (another FFN, weights in 8 bits with a scale for each 128 x 128, a shared
+ * expert): the layer's table (mok_schedule) moves the rows, and the products run on E4M3 operands.  The pages have
+ * no counterpart: their experts are SwiGLU FFNs in BF16 or MXFP8.
+ *
+ * Rows by a table.
+ *   T  tokens, R  rows of the sorted order (mok_schedule: T k; fewer or more where assignments are dropped or rows
+ *   padded), both >= 0;  H  width >= 1;  k  assignments of a token, 1 .. 16
+ *   token_stride, row_stride  elements between tokens and between rows, >= H (0 = H)
+ *   type  mok_elem_type of tokens and rows
+ * src_of i32 [R]: the assignment a = t k + j in row r; row_of i32 [T k]: the row of assignment a.  -1 is an empty row
+ * and an assignment without a row (dropped); any other index out of range counts as -1 and is reported as
+ * (MOK_ERR_INVALID_ROUTING, site) in device_status, a DEVICE buffer of 2 int32 that the caller has cleared, or NULL.
+ * gates f32 [T][k], or NULL: all 1.  Outputs do not overlap inputs. */
+typedef struct {
+  int64_t T, R, H;
+  int64_t token_stride, row_stride;
+  int32_t k, type;
+} mok_rows_desc;
+
+/* x_g[r] = gates[a] x[a / k], a = src_of[r]: every row of x_g is written, empty ones with zeros.  Its gradient with
+ * respect to x is mok_merge_rows of dx_g with the same gates. */
+mok_status mok_gather_rows(const mok_rows_desc* desc, const void* x, const int32_t* src_of, const float* gates,
+                           void* x_g, int32_t* device_status, void* stream);
+
+/* y[t] = sum_j gates[t][j] o[row_of[t k + j]], j ascending, in f32, rounded once; zeros for a token without rows. */
+mok_status mok_merge_rows(const mok_rows_desc* desc, const void* o, const int32_t* row_of, const float* gates, void* y,
+                          int32_t* device_status, void* stream);
+
+/* d_o[row_of[t k + j]] = gates[t][j] dy[t]; dgates[t][j] = <dy[t], o[row_of[t k + j]]> (f32, NULL if not wanted), 0 for
+ * an assignment without a row.  Rows of d_o that no assignment names are left as they were; a row that two name
+ * holds either's. */
+mok_status mok_merge_rows_backward(const mok_rows_desc* desc, const void* dy, const void* o, const int32_t* row_of,
+                                   const float* gates, void* d_o, float* dgates, int32_t* device_status, void* stream);
+
+/* E4M3 with an f32 scale for each block of 128: scale = max(amax, 2^-110) / 448 over the block's finite elements,
+ * element = the E4M3 value nearest to 448 x / amax, ties to even; an element that is not finite becomes a NaN.  Rows
+ * of E4M3 elements start at multiples of 16 bytes.
+ *   R  rows, C  width of the quantised rows;  x_stride, grad_stride  elements between rows (0 = packed)
+ *   source   MOK_FP8_PLAIN: x [R][C]; with src_of, rows gates[a] x[a / k] of x [T][C] as in mok_gather_rows
+ *            (gates may be NULL)
+ *            MOK_FP8_SWIGLU: x [R][2C] = h | u; quantised is silu(h) u
+ *            MOK_FP8_SWIGLU_GRAD: x [R][C] = h | u, grad [R][C/2] = da; quantised is the gradient dh | du [R][C] of
+ *            a = silu(h) u
+ *   type     mok_elem_type of x and grad
+ * Outputs, either pair NULL if not wanted:
+ *   q [R][C], scale f32 [ceil(C/128)][R]: blocks along the row (q_stride bytes, a multiple of 16, 0 = C rounded up to
+ *     one; scale_stride floats, 0 = R)
+ *   qt [C][P], qt_scale f32 [P/128][C], P = 128 (R / 128 + E): blocks along the rows of each of E groups (offsets i32
+ *     [E+1], as of mok_schedule), transposed: group e's rows follow each other from 128 times the 128-row blocks of
+ *     the groups before it, with zeros behind its last up to a multiple of 128 (qt_stride bytes, 0 = P).  Blocks
+ *     behind the last group's are left as they were.  With it, q and scale too are written for the rows of the
+ *     groups only.
+ * Without columns E and offsets are not read.  An offset outside [0, R] or below the one before counts as the nearest
+ * that is not. */
+typedef enum { MOK_FP8_PLAIN = 0, MOK_FP8_SWIGLU = 1, MOK_FP8_SWIGLU_GRAD = 2 } mok_fp8_source;
+typedef struct {
+  int64_t R, C, T;
+  int64_t x_stride, grad_stride, q_stride, scale_stride, qt_stride;
+  int32_t E, k;
+  int32_t source, type;
+} mok_fp8_quantize_desc;
+mok_status mok_fp8_quantize(const mok_fp8_quantize_desc* desc, const void* x, const void* grad, const int32_t* src_of,
+                            const float* gates, const int32_t* offsets, uint8_t* q, float* scale, uint8_t* qt,
+                            float* qt_scale, int32_t* device_status, void* stream);
+
+/* Weights w [E][N][K] (contiguous) with a scale for each 128 x 128, by the same rule.  Outputs, either pair NULL if not
+ * wanted: q [E][N][K] and scale f32 [E][ceil(N/128)][ceil(K/128)] for x W^T, qt [E][K][N] and qt_scale f32
+ * [E][ceil(K/128)][ceil(N/128)] for dy W (the same elements and scales, transposed).  Strides in bytes between
+ * elements' rows, multiples of 16 (0 = the width rounded up to one). */
+typedef struct {
+  int64_t N, K;
+  int64_t q_stride, qt_stride;
+  int32_t E, type;
+} mok_fp8_weights_desc;
+mok_status mok_fp8_quantize_weights(const mok_fp8_weights_desc* desc, const void* w, uint8_t* q, float* scale,
+                                    uint8_t* qt, float* qt_scale, void* stream);
+
+/* out[r][n] = sum_b x_scale[b][r] w_scale[e][n/128][b] sum_{k in block b} x[r][k] w[e][n][k] for the rows r of group e,
+ * offsets[e] <= r < offsets[e+1] (as for mok_fp8_quantize; NULL with E = 1: all R rows).  x [R][K] and x_scale as q and
+ * scale of mok_fp8_quantize, w [E][N][K] and w_scale as of mok_fp8_quantize_weights: q and scale for x W^T, qt and
+ * qt_scale for dy W.  The sums of a block are formed by the tensor cores, the blocks are added in f32, in a fixed
+ * order.  out f32 or bf16 (out_type, rounded once), out_stride elements between rows (0 = N); rows of no group are
+ * left as they were.  device_status as for mok_gather_rows; it also takes a wait that ran out (MOK_ERR_TIMEOUT). */
+typedef struct {
+  int64_t R, N, K;
+  int64_t x_stride, x_scale_stride, w_stride, out_stride;
+  int32_t E, out_type;
+} mok_fp8_matmul_desc;
+mok_status mok_fp8_matmul(const mok_fp8_matmul_desc* desc, const uint8_t* x, const float* x_scale, const uint8_t* w,
+                          const float* w_scale, const int32_t* offsets, void* out, int32_t* device_status,
+                          void* stream);
+
+/* out[e][n][h] = sum over group e's blocks b of dy_scale[b][n] x_scale[b][h] sum_{r in b} dy[n][r] x[h][r]: the gradient
+ * of the weights, with dy [N][P], x [H][P] and their scales as qt and qt_scale of mok_fp8_quantize for the same R, E and
+ * offsets.  Zeros for a group without rows.  out f32 or bf16 [E][N][H], contiguous. */
+typedef struct {
+  int64_t R, N, H;
+  int64_t dy_stride, x_stride;
+  int32_t E, out_type;
+} mok_fp8_weight_grad_desc;
+mok_status mok_fp8_weight_grad(const mok_fp8_weight_grad_desc* desc, const uint8_t* dy, const float* dy_scale,
+                               const uint8_t* x, const float* x_scale, const int32_t* offsets, void* out,
+                               int32_t* device_status, void* stream);
+
 /* Synchronises `stream`, copies the device status word out of ws into
  * device_status[0] (code, a mok_status value) and device_status[1] (site), then clears it.
  * Host-blocking; not for use inside captured graphs. */

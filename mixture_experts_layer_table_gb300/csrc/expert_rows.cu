@@ -1,0 +1,294 @@
+// Rows by a schedule table, outside the layer (no counterpart on the pages beyond the layer's own gather and
+// merge: "把 MoE 通信延迟从 103μs 压到 18μs：Cursor 开源 GPU 内核 MoK", aientropygate.com, §03 ① and §04):
+//   gather          x_g[r] = g[a] x[a / k], a = src_of[r]; a zero row where a = -1
+//   merge           y[t] = sum_j g[t][j] o[row_of[t k + j]], j ascending, in f32, rounded once
+//   merge backward  do[row_of[t k + j]] = g[t][j] dy[t],  dg[t][j] = <dy[t], o[row_of[t k + j]]>
+// All three move rows and compute next to nothing: DRAM bounds them where there are many rows, the
+// chain index -> row -> store where there are few.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "expert_rows.cuh"
+#include "status.cuh"
+
+namespace mok {
+namespace {
+
+// A piece of a row: BYTES of T's, moved by one instruction.
+template <typename T, int BYTES>
+struct Piece {
+  static constexpr int N = BYTES / (int)sizeof(T);
+  T v[N];
+};
+template <typename T, int BYTES>
+struct Raw;
+template <typename T>
+struct Raw<T, 16> { using type = uint4; };
+template <typename T>
+struct Raw<T, 4> { using type = uint32_t; };
+template <typename T>
+struct Raw<T, 2> { using type = uint16_t; };
+
+__device__ __forceinline__ void load_raw(uint4& v, const void* p) {
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+}
+__device__ __forceinline__ void load_raw(uint32_t& v, const void* p) { v = __ldg(static_cast<const uint32_t*>(p)); }
+__device__ __forceinline__ void load_raw(uint16_t& v, const void* p) {
+  v = __ldg(static_cast<const unsigned short*>(p));
+}
+template <typename W>
+__device__ __forceinline__ void store_raw(void* p, const W& v) {
+  __stcs(static_cast<W*>(p), v);
+}
+__device__ __forceinline__ void store_raw(void* p, const uint16_t& v) {
+  __stcs(static_cast<unsigned short*>(p), (unsigned short)v);
+}
+
+__device__ __forceinline__ float widen(float v) { return v; }
+__device__ __forceinline__ float widen(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void narrow(float& d, float v) { d = v; }
+__device__ __forceinline__ void narrow(__nv_bfloat16& d, float v) { d = __float2bfloat16_rn(v); }
+
+template <typename T, int BYTES, typename W>
+__device__ __forceinline__ void unpack(const W& w, float (&f)[Piece<T, BYTES>::N]) {
+  const Piece<T, BYTES>& p = reinterpret_cast<const Piece<T, BYTES>&>(w);
+#pragma unroll
+  for (int i = 0; i < Piece<T, BYTES>::N; ++i) f[i] = widen(p.v[i]);
+}
+template <typename T, int BYTES, typename W>
+__device__ __forceinline__ void pack(W& w, const float (&f)[Piece<T, BYTES>::N]) {
+  Piece<T, BYTES>& p = reinterpret_cast<Piece<T, BYTES>&>(w);
+#pragma unroll
+  for (int i = 0; i < Piece<T, BYTES>::N; ++i) narrow(p.v[i], f[i]);
+}
+
+// The source of row r, or -1 for a zero row; an index outside [0, n) other than -1 is reported.
+__device__ __forceinline__ int64_t checked(int32_t i, int64_t n, int* status, int site) {
+  if (i >= 0 && i < n) return i;
+  if (i != -1) report_status(status, MOK_DEV_INVALID_ROUTING, site);
+  return -1;
+}
+
+// blockDim.x threads to a row, blockDim.y rows to a block; V pieces of a thread in flight at once.  Short-lived
+// blocks in row order, as the layer's own gather (rows.cu) found best.
+template <typename T, int BYTES, int V>
+__global__ void __launch_bounds__(128) expert_gather_kernel(const RowsArgs a, int pieces) {
+  using W = typename Raw<T, BYTES>::type;
+  const int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  if (r >= a.R) return;
+  const int64_t src = checked(a.index[r], a.T * a.k, a.status, SITE_ROWS_GATHER);
+  const float g = a.gates != nullptr && src >= 0 ? a.gates[src] : 1.0f;
+  const char* s = static_cast<const char*>(a.tokens) + (src < 0 ? 0 : src / a.k) * a.token_stride * (int64_t)sizeof(T);
+  char* d = static_cast<char*>(a.out) + r * a.row_stride * (int64_t)sizeof(T);
+  for (int base = threadIdx.x; base < pieces; base += blockDim.x * V) {
+    W v[V] = {};
+    if (src >= 0) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int i = base + j * blockDim.x;
+        if (i < pieces) load_raw(v[j], s + (int64_t)i * BYTES);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int i = base + j * blockDim.x;
+      if (i < pieces) {
+        if (a.gates != nullptr && src >= 0) {
+          float f[Piece<T, BYTES>::N];
+          unpack<T, BYTES>(v[j], f);
+#pragma unroll
+          for (int q = 0; q < Piece<T, BYTES>::N; ++q) f[q] *= g;
+          pack<T, BYTES>(v[j], f);
+        }
+        store_raw(d + (int64_t)i * BYTES, v[j]);
+      }
+    }
+  }
+}
+
+// One piece of one token to a thread, the token's k rows in flight at once.
+template <typename T, int BYTES, int KMAX>
+__global__ void __launch_bounds__(128) expert_merge_kernel(const RowsArgs a, int pieces) {
+  using W = typename Raw<T, BYTES>::type;
+  const int64_t n = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  const int64_t t = n / pieces;
+  if (t >= a.T) return;
+  const int i = (int)(n - t * pieces);
+  W v[KMAX];
+  float g[KMAX];
+  bool has[KMAX];
+#pragma unroll
+  for (int j = 0; j < KMAX; ++j) {
+    has[j] = false;
+    if (j < a.k) {
+      const int64_t row = checked(a.index[t * a.k + j], a.R, a.status, SITE_ROWS_MERGE);
+      has[j] = row >= 0;
+      if (has[j]) {
+        g[j] = a.gates != nullptr ? a.gates[t * a.k + j] : 1.0f;
+        load_raw(v[j], static_cast<const char*>(a.rows) + row * a.row_stride * (int64_t)sizeof(T) + (int64_t)i * BYTES);
+      }
+    }
+  }
+  float acc[Piece<T, BYTES>::N] = {};
+#pragma unroll
+  for (int j = 0; j < KMAX; ++j)
+    if (has[j]) {
+      float f[Piece<T, BYTES>::N];
+      unpack<T, BYTES>(v[j], f);
+#pragma unroll
+      for (int q = 0; q < Piece<T, BYTES>::N; ++q) acc[q] = fmaf(g[j], f[q], acc[q]);
+    }
+  W o;
+  pack<T, BYTES>(o, acc);
+  store_raw(static_cast<char*>(a.out) + t * a.token_stride * (int64_t)sizeof(T) + (int64_t)i * BYTES, o);
+}
+
+// One token to a block: dy is read once and meets the token's rows four at a time.  The dot products are added
+// over a thread's pieces, the lanes and the warps, in that fixed order.
+template <typename T, int BYTES, int KMAX>
+__global__ void __launch_bounds__(512) expert_merge_backward_kernel(const RowsArgs a, int pieces) {
+  using W = typename Raw<T, BYTES>::type;
+  constexpr int N = Piece<T, BYTES>::N, G = KMAX < 4 ? KMAX : 4;
+  __shared__ float part[16][KMAX];
+  const int64_t t = blockIdx.x;
+  int32_t row[KMAX];
+  float g[KMAX], dot[KMAX];
+#pragma unroll
+  for (int j = 0; j < KMAX; ++j) {
+    row[j] = -1;
+    dot[j] = 0.0f;
+    if (j < a.k) {
+      row[j] = (int32_t)checked(a.index[t * a.k + j], a.R, a.status, SITE_ROWS_MERGE);
+      g[j] = a.gates != nullptr ? a.gates[t * a.k + j] : 1.0f;
+    }
+  }
+  for (int i = threadIdx.x; i < pieces; i += blockDim.x) {
+    const int64_t at = (int64_t)i * BYTES;
+    W w;
+    load_raw(w, static_cast<const char*>(a.tokens) + t * a.token_stride * (int64_t)sizeof(T) + at);
+    float dy[N];
+    unpack<T, BYTES>(w, dy);
+#pragma unroll
+    for (int j0 = 0; j0 < KMAX; j0 += G) {
+      W v[G];
+#pragma unroll
+      for (int j = 0; j < G; ++j)
+        if (row[j0 + j] >= 0)
+          load_raw(v[j], static_cast<const char*>(a.rows) + row[j0 + j] * a.row_stride * (int64_t)sizeof(T) + at);
+#pragma unroll
+      for (int j = 0; j < G; ++j)
+        if (row[j0 + j] >= 0) {
+          float o[N], d[N];
+          unpack<T, BYTES>(v[j], o);
+#pragma unroll
+          for (int q = 0; q < N; ++q) {
+            dot[j0 + j] = fmaf(dy[q], o[q], dot[j0 + j]);
+            d[q] = g[j0 + j] * dy[q];
+          }
+          W out;
+          pack<T, BYTES>(out, d);
+          store_raw(static_cast<char*>(a.out) + row[j0 + j] * a.row_stride * (int64_t)sizeof(T) + at, out);
+        }
+    }
+  }
+  if (a.dgates == nullptr) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int j = 0; j < KMAX; ++j) {
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], s);
+    if (lane == 0) part[warp][j] = dot[j];
+  }
+  __syncthreads();
+  if (threadIdx.x < a.k) {
+    float sum = 0.0f;
+    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) sum += part[w][threadIdx.x];
+    a.dgates[t * a.k + threadIdx.x] = sum;
+  }
+}
+
+// The widest piece that the rows' starts, strides and width allow.
+int piece_bytes(const RowsArgs& a, int item) {
+  uint64_t bits = reinterpret_cast<uintptr_t>(a.tokens) | reinterpret_cast<uintptr_t>(a.rows) |
+                  reinterpret_cast<uintptr_t>(a.out) | (uint64_t)(a.H * item) | (uint64_t)(a.token_stride * item) |
+                  (uint64_t)(a.row_stride * item);
+  return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : item;
+}
+
+template <typename T, int BYTES>
+cudaError_t gather(const RowsArgs& a, cudaStream_t st) {
+  const int pieces = (int)(a.H * (int64_t)sizeof(T) / BYTES);
+  // narrow rows share a block
+  const int x = pieces <= 32 ? 32 : pieces <= 64 ? 64 : 128;
+  const dim3 block(x, 128 / x);
+  const int64_t blocks = (a.R + block.y - 1) / block.y;
+  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  expert_gather_kernel<T, BYTES, 8><<<(unsigned)blocks, block, 0, st>>>(a, pieces);
+  return cudaGetLastError();
+}
+
+template <typename T, int BYTES, int KMAX>
+cudaError_t merge_k(const RowsArgs& a, cudaStream_t st) {
+  const int pieces = (int)(a.H * (int64_t)sizeof(T) / BYTES);
+  const int64_t blocks = (a.T * pieces + 127) / 128;
+  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  expert_merge_kernel<T, BYTES, KMAX><<<(unsigned)blocks, 128, 0, st>>>(a, pieces);
+  return cudaGetLastError();
+}
+
+template <typename T, int BYTES>
+cudaError_t merge(const RowsArgs& a, cudaStream_t st) {
+  if (a.k <= 1) return merge_k<T, BYTES, 1>(a, st);
+  if (a.k <= 2) return merge_k<T, BYTES, 2>(a, st);
+  if (a.k <= 4) return merge_k<T, BYTES, 4>(a, st);
+  if (a.k <= 8) return merge_k<T, BYTES, 8>(a, st);
+  return merge_k<T, BYTES, 16>(a, st);
+}
+
+template <typename T, int BYTES, int KMAX>
+cudaError_t merge_backward_k(const RowsArgs& a, int n_sm, cudaStream_t st) {
+  const int pieces = (int)(a.H * (int64_t)sizeof(T) / BYTES);
+  // few tokens: a block of as many threads as shorten the row
+  const int most = a.T < 2 * n_sm ? 512 : 128;
+  const int threads = std::min(most, (pieces + 31) / 32 * 32);
+  if (a.T > INT32_MAX) return cudaErrorInvalidValue;
+  expert_merge_backward_kernel<T, BYTES, KMAX><<<(unsigned)a.T, threads, 0, st>>>(a, pieces);
+  return cudaGetLastError();
+}
+
+template <typename T, int BYTES>
+cudaError_t merge_backward(const RowsArgs& a, int n_sm, cudaStream_t st) {
+  if (a.k <= 1) return merge_backward_k<T, BYTES, 1>(a, n_sm, st);
+  if (a.k <= 2) return merge_backward_k<T, BYTES, 2>(a, n_sm, st);
+  if (a.k <= 4) return merge_backward_k<T, BYTES, 4>(a, n_sm, st);
+  if (a.k <= 8) return merge_backward_k<T, BYTES, 8>(a, n_sm, st);
+  return merge_backward_k<T, BYTES, 16>(a, n_sm, st);
+}
+
+}  // namespace
+
+cudaError_t launch_expert_gather(const RowsArgs& a, bool bf16, cudaStream_t st) {
+  const int bytes = piece_bytes(a, bf16 ? 2 : 4);
+  if (!bf16) return bytes == 16 ? gather<float, 16>(a, st) : gather<float, 4>(a, st);
+  if (bytes == 16) return gather<__nv_bfloat16, 16>(a, st);
+  return bytes == 4 ? gather<__nv_bfloat16, 4>(a, st) : gather<__nv_bfloat16, 2>(a, st);
+}
+
+cudaError_t launch_expert_merge(const RowsArgs& a, bool bf16, cudaStream_t st) {
+  const int bytes = piece_bytes(a, bf16 ? 2 : 4);
+  if (!bf16) return bytes == 16 ? merge<float, 16>(a, st) : merge<float, 4>(a, st);
+  if (bytes == 16) return merge<__nv_bfloat16, 16>(a, st);
+  return bytes == 4 ? merge<__nv_bfloat16, 4>(a, st) : merge<__nv_bfloat16, 2>(a, st);
+}
+
+cudaError_t launch_expert_merge_backward(const RowsArgs& a, bool bf16, int n_sm, cudaStream_t st) {
+  const int bytes = piece_bytes(a, bf16 ? 2 : 4);
+  if (!bf16) return bytes == 16 ? merge_backward<float, 16>(a, n_sm, st) : merge_backward<float, 4>(a, n_sm, st);
+  if (bytes == 16) return merge_backward<__nv_bfloat16, 16>(a, n_sm, st);
+  return bytes == 4 ? merge_backward<__nv_bfloat16, 4>(a, n_sm, st) : merge_backward<__nv_bfloat16, 2>(a, n_sm, st);
+}
+
+}  // namespace mok

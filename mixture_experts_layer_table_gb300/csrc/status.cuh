@@ -22,6 +22,10 @@ enum StatusSite : int {
   SITE_SCHEDULE_INDEX = 11,
   SITE_RING_WAIT = 20,
   SITE_TEST_WAIT = 30,
+  SITE_ROWS_GATHER = 40,
+  SITE_ROWS_MERGE = 41,
+  SITE_FP8_SOURCE = 42,
+  SITE_FP8_OFFSETS = 43,
 };
 
 // status[0] = code of the first error, status[1] = its site.
