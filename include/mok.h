@@ -552,8 +552,8 @@ mok_status mok_merge_rows_backward(const mok_rows_desc* desc, const void* dy, co
  *     the groups before it, with zeros behind its last up to a multiple of 128 (qt_stride bytes, 0 = P).  Blocks
  *     behind the last group's are left as they were.  With it, q and scale too are written for the rows of the
  *     groups only.
- * Without columns E and offsets are not read.  An offset outside [0, R] or below the one before counts as the nearest
- * that is not. */
+ * Without columns E and offsets are not read.  Offsets that do not ascend within [0, R] give results that are not
+ * defined; nothing outside the tensors is read or written. */
 typedef enum { MOK_FP8_PLAIN = 0, MOK_FP8_SWIGLU = 1, MOK_FP8_SWIGLU_GRAD = 2 } mok_fp8_source;
 typedef struct {
   int64_t R, C, T;

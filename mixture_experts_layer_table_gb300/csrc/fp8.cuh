@@ -68,13 +68,15 @@ struct Fp8WeightGradArgs {
 
 cudaError_t launch_fp8_quantize(const Fp8QuantizeArgs& a, int source, bool bf16, int n_sm, cudaStream_t st);
 cudaError_t launch_fp8_weights(const Fp8WeightsArgs& a, bool bf16, cudaStream_t st);
+// The product on CTA pairs (many rows a group); launch_fp8_matmul chooses.
+cudaError_t launch_fp8_product_pairs(const Fp8MatmulArgs& a, bool bf16_out, int n_sm, cudaStream_t st);
 cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, bool bf16_out, int n_sm, cudaStream_t st);
 cudaError_t launch_fp8_weight_grad(const Fp8WeightGradArgs& a, bool bf16_out, int n_sm, cudaStream_t st);
 
-// Row i of an offsets table as the kernels take it: inside [0, R], and not below its predecessor (the caller
-// carries `before`), so that a table that is wrong reads and writes nothing outside the tensors.
-__device__ __forceinline__ int fp8_offset(int32_t v, int before, int64_t R) {
-  const int r = v < before ? before : v;
+// An end of a group's rows as the kernels take it: in [least, R], with least 0 for the first row and the first row for
+// the end, so that a table that is wrong reads and writes nothing outside the tensors.
+__device__ __forceinline__ int fp8_offset(int32_t v, int least, int64_t R) {
+  const int r = v < least ? least : v;
   return r > R ? (int)R : r;
 }
 

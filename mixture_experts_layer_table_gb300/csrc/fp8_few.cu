@@ -131,77 +131,12 @@ cudaError_t few(const Fp8MatmulArgs& a, bool bf16_out, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-// dW[e][n][h] = sum over the 128-row blocks b of group e of ds[b][n] xs[b][h] sum_{r in b} dy[n][r] x[h][r]: a warp
-// has 16 rows of x as A and 32 rows of dy as B, so that 16 consecutive h of one n are stored together.
-template <typename OUT>
-__global__ void __launch_bounds__(32 * WARPS) fp8_weight_grad_kernel(const Fp8WeightGradArgs a) {
-  __shared__ int s_block[2];
-  const int e = blockIdx.z;
-  if (threadIdx.x == 0) {
-    int at = 0, before = 0;
-    for (int i = 0; i <= e; ++i) {
-      const int lo = fp8_offset(a.offsets[i], 0, a.R), hi = fp8_offset(a.offsets[i + 1], lo, a.R);
-      before = at;
-      at += (hi - lo + 127) >> 7;
-    }
-    const int most = (int)(a.R / 128 + a.E);
-    s_block[0] = min(before, most);
-    s_block[1] = min(at, most);
-  }
-  __syncthreads();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = lane >> 2, t = lane & 3;
-  const int64_t h0 = (int64_t)blockIdx.x * 16, n0 = ((int64_t)blockIdx.y * WARPS + warp) * 32;
-  if (n0 >= a.N) return;
-  const int64_t P = 128ll * (a.R / 128 + a.E);
-  const int64_t ha = min(h0 + g, a.H - 1), hb = min(h0 + g + 8, a.H - 1);
-  float sum[4][4] = {};
-  for (int kb = s_block[0]; kb < s_block[1]; ++kb) {
-    uint32_t wa[8], wb[8], x[8];
-    load_words(a.x + ha * a.x_stride, kb * 128ll, P, t, wa);
-    load_words(a.x + hb * a.x_stride, kb * 128ll, P, t, wb);
-    const float sa = a.x_scale[kb * a.H + ha], sb = a.x_scale[kb * a.H + hb];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      load_words(a.dy + min(n0 + 8 * j + g, a.N - 1) * a.dy_stride, kb * 128ll, P, t, x);
-      const float s0 = a.dy_scale[kb * a.N + min(n0 + 8 * j + 2 * t, a.N - 1)];
-      const float s1 = a.dy_scale[kb * a.N + min(n0 + 8 * j + 2 * t + 1, a.N - 1)];
-      float d[4] = {};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t f[4] = {wa[2 * i], wb[2 * i], wa[2 * i + 1], wb[2 * i + 1]};
-        mma_e4m3(d, f, x[2 * i], x[2 * i + 1]);
-      }
-      sum[j][0] = fmaf(d[0], sa * s0, sum[j][0]);
-      sum[j][1] = fmaf(d[1], sa * s1, sum[j][1]);
-      sum[j][2] = fmaf(d[2], sb * s0, sum[j][2]);
-      sum[j][3] = fmaf(d[3], sb * s1, sum[j][3]);
-    }
-  }
-  OUT* out = static_cast<OUT*>(a.out) + (int64_t)e * a.N * a.H;
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t n = n0 + 8 * j + 2 * t + (i & 1), h = h0 + g + 8 * (i >> 1);
-      if (n < a.N && h < a.H) put(out + n * a.H + h, sum[j][i]);
-    }
-}
-
 }  // namespace
 
 cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, bool bf16_out, int n_sm, cudaStream_t st) {
-  (void)n_sm;
   const int64_t each = (a.R + a.E - 1) / a.E;  // rows of a group, about
+  if (each > 32) return launch_fp8_product_pairs(a, bf16_out, n_sm, st);
   return each <= 8 ? few<1>(a, bf16_out, st) : each <= 16 ? few<2>(a, bf16_out, st) : few<4>(a, bf16_out, st);
-}
-
-cudaError_t launch_fp8_weight_grad(const Fp8WeightGradArgs& a, bool bf16_out, int n_sm, cudaStream_t st) {
-  (void)n_sm;
-  const dim3 grid((unsigned)((a.H + 15) / 16), (unsigned)((a.N + 255) / 256), (unsigned)a.E);
-  if (bf16_out) fp8_weight_grad_kernel<__nv_bfloat16><<<grid, 32 * WARPS, 0, st>>>(a);
-  else fp8_weight_grad_kernel<float><<<grid, 32 * WARPS, 0, st>>>(a);
-  return cudaGetLastError();
 }
 
 }  // namespace mok

@@ -1,0 +1,577 @@
+// E4M3 products with an f32 scale for each block of 128 on CTA pairs (include/mok.h: mok_fp8_matmul,
+// mok_fp8_weight_grad):
+//   product       out[r][n] = sum_b xs[b][r] ws[e][n / 128][b] (x_b w_b^T)[r][n]     over the rows r of group e
+//   weight grad   out[e][n][h] = sum_b ds[b][n] xs[b][h] (dy_b x_b^T)[n][h]        over the 128-row blocks b of group e
+// Both are out[col][lane] = sum_b s_b (A_b B_b^T) with A's rows the MMA's M (256 a pair tile, 128 a CTA: weights' rows, or
+// h) and B's rows its N (a multiple of 16 up to 256: the group's rows, or n), so that a group of few rows pads to 16
+// only and a warp's 32 lanes store 32 consecutive elements of out.
+//
+// The scales are arbitrary f32 numbers and change with each 128 of K, so a block's sum cannot stay in the tensor
+// cores: tcgen05.mma.kind::f8f6f4 forms it (four K = 32 steps) in one of two TMEM accumulators, and the epilogue warps
+// add it, scaled, to their f32 sums in registers while the next block's MMAs run into the other.  For 256 columns that
+// is 64 packed FMAs, 4 TMEM loads and 32 broadcast shared loads of a warp for each block, against 512 cycles of MMAs.
+//
+// Roles of both CTAs of a pair: warp 0 TMA producer, warp 1 MMA issuer (even CTA, one thread), warp 2 the scales, warps 4
+// to 11 epilogue (warp w reads TMEM lane quarter w % 4; the two warps of a quarter take alternate 32-column pieces).  The
+// scales' warp reads four blocks' scales at a time, multiplies the two where one is the same for a whole 128-row
+// tile (product) and puts them into a ring in shared memory.  Barriers: full[s] in the even CTA (one arrival with
+// both CTAs' bytes), empty[s] and pfull[a] in both (multicast commits), pempty[a] in the even CTA (16 arrivals),
+// sfull[q] and sempty[q] in each CTA.  Tiles (group, weight tile m, chunk c of the group's rows; c fastest, then m)
+// are dealt to the pairs round-robin; every output element is one tile's sum over its blocks in order, so results do not
+// depend on the deal.  Every wait is bounded.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "f32x2.cuh"
+#include "fp8.cuh"
+#include "ptx.cuh"
+#include "tmap.cuh"
+
+namespace mok {
+namespace {
+
+struct Fp8GemmArgs {
+  int E;
+  int nkb;                // product: blocks along K
+  int NM;                 // A rows of a group: weights' rows, or H
+  int NB;                 // weight grad: B rows (n)
+  int MT;                 // pair tiles along A's rows
+  int nmax;               // columns of a chunk at most (a multiple of 16 up to 256)
+  int64_t R;
+  int64_t blocks;         // weight grad: 128-row blocks that the operands have
+  const int32_t* offsets; // [E+1] or null: one group of R rows
+  const float* a_scale;   // product: [E][NM / 128][nkb]; weight grad: [blocks][NM]
+  const float* b_scale;   // product: [nkb][b_ld]; weight grad: [blocks][NB]
+  int64_t b_ld;
+  void* out;
+  int64_t ld;             // elements between out's rows
+  int* status;
+};
+
+constexpr int F8_STAGES = 6;
+constexpr int F8_SLOTS = 8;
+constexpr int F8_A_BYTES = 128 * 128;
+constexpr int F8_B_BYTES = 128 * 128;
+constexpr int F8_STAGE = F8_A_BYTES + F8_B_BYTES;
+constexpr int F8_SLOT = (256 + 128) * 4;  // the columns' scales, and (weight grad) the lanes'
+constexpr int F8_EPI_WARPS = 8;
+constexpr int F8_THREADS = 32 * (4 + F8_EPI_WARPS);
+// Registers of a thread: 168 at launch (384 threads of them are the register file); the epilogue's 128 f32 sums
+// need more: 128 x 88 + 256 x 208 = 64,512 = 384 x 168.
+constexpr int F8_REGS_FEW = 88, F8_REGS_EPI = 208;
+static_assert(128 * F8_REGS_FEW + 256 * F8_REGS_EPI <= F8_THREADS * 168, "register split");
+constexpr int F8_SMEM_BARS = 512;
+constexpr size_t f8_smem(int E) {
+  return 1024 + size_t(F8_STAGES) * F8_STAGE + size_t(F8_SLOTS) * F8_SLOT + F8_SMEM_BARS + size_t(3) * (E + 1) * 4;
+}
+static_assert(f8_smem(FP8_MAX_E) <= 232448, "shared memory");
+
+struct Fp8Tile {
+  int e, m;
+  int col0, cols, n;  // B's first row, how many there are, padded to the MMA's N
+  int kb0, nkb;       // first block of K, number of blocks
+};
+
+// Tile g: the groups' first tiles by binary search (product), or by division (weight grad).
+// s_at / s_cnt: product: first row and rows of each group, s_first: chunks before it; weight grad: first block, blocks.
+template <bool WGRAD>
+__device__ __forceinline__ Fp8Tile f8_tile(int g, const Fp8GemmArgs& a, const int* s_at, const int* s_cnt,
+                                           const int* s_first) {
+  Fp8Tile t;
+  int nc, c, rows;
+  if (WGRAD) {
+    nc = (a.NB + a.nmax - 1) / a.nmax;
+    const int per = nc * a.MT;
+    t.e = g / per;
+    const int l = g - t.e * per;
+    t.m = l / nc;
+    c = l - t.m * nc;
+    rows = a.NB;
+    t.kb0 = s_at[t.e];
+    t.nkb = s_cnt[t.e];
+    t.col0 = 0;
+  } else {
+    int lo = 0, hi = a.E;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_first[mid] * a.MT <= g) lo = mid; else hi = mid;
+    }
+    t.e = lo;
+    nc = s_first[lo + 1] - s_first[lo];
+    const int l = g - s_first[lo] * a.MT;
+    t.m = l / nc;
+    c = l - t.m * nc;
+    rows = s_cnt[lo];
+    t.kb0 = 0;
+    t.nkb = a.nkb;
+    t.col0 = s_at[lo];
+  }
+  const int each = ((rows + nc - 1) / nc + 15) & ~15;  // equal chunks
+  t.col0 += c * each;
+  t.cols = max(0, min(each, rows - c * each));
+  t.n = max(16, (t.cols + 15) & ~15);
+  return t;
+}
+
+__device__ __forceinline__ void f8_put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void f8_put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// tmA: A's rows, [groups][NM][K] bytes, boxes of 128 bytes x 128 rows; tmB: B's rows, boxes of 128 bytes x 32 rows.
+template <bool WGRAD, typename OUT>
+__global__ void __launch_bounds__(F8_THREADS, 1)
+    fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const Fp8GemmArgs args) {
+  constexpr int STAGES = F8_STAGES, SLOTS = F8_SLOTS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* slots = reinterpret_cast<float*>(smem + STAGES * F8_STAGE);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * F8_STAGE + SLOTS * F8_SLOT);
+  // bars: full, empty [STAGES], pfull, pempty [2], sfull, sempty [SLOTS], drain; the TMEM address; the abort flag
+  constexpr int NBARS = 2 * STAGES + 4 + 2 * SLOTS + 1;
+  static_assert(NBARS * 8 + 8 <= F8_SMEM_BARS, "barriers");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NBARS);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* s_at = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + F8_SMEM_BARS);
+  int* s_cnt = s_at + (args.E + 1);
+  int* s_first = s_cnt + (args.E + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int pair = (int)blockIdx.x >> 1;
+  const int npairs = (int)gridDim.x >> 1;
+  auto full_bar = [&](int s) { return smem_u32(&bars[s]); };
+  auto empty_bar = [&](int s) { return smem_u32(&bars[STAGES + s]); };
+  auto pfull_bar = [&](int a) { return smem_u32(&bars[2 * STAGES + a]); };
+  auto pempty_bar = [&](int a) { return smem_u32(&bars[2 * STAGES + 2 + a]); };
+  auto sfull_bar = [&](int q) { return smem_u32(&bars[2 * STAGES + 4 + q]); };
+  auto sempty_bar = [&](int q) { return smem_u32(&bars[2 * STAGES + 4 + SLOTS + q]); };
+  const uint32_t drain_bar = smem_u32(&bars[2 * STAGES + 4 + 2 * SLOTS]);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(pfull_bar(a), 1);
+      mbar_init(pempty_bar(a), 2 * F8_EPI_WARPS);
+    }
+    for (int q = 0; q < SLOTS; ++q) {
+      mbar_init(sfull_bar(q), 1);
+      mbar_init(sempty_bar(q), F8_EPI_WARPS);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), 512);
+    tmem_relinquish_pair();
+  }
+  if (warp == 0) {
+    // the groups' rows and the chunks (weight grad: 128-row blocks) before each: a scan, 32 groups at a time.  A group
+    // starts no earlier than those before it end, whatever the table says: the chunks are then at most as many as the
+    // host counted.
+    int before = 0, row = 0;
+    for (int e0 = 0; e0 < args.E; e0 += 32) {
+      const int e = e0 + lane;
+      int lo = 0, cnt = 0;
+      if (e < args.E) {
+        if (args.offsets == nullptr) {
+          cnt = (int)args.R;
+        } else {
+          lo = fp8_offset(args.offsets[e], 0, args.R);
+          cnt = fp8_offset(args.offsets[e + 1], lo, args.R);  // the end, for now
+        }
+      }
+      int end = max(row, cnt);
+#pragma unroll
+      for (int s = 1; s < 32; s <<= 1) end = max(end, __shfl_up_sync(0xffffffffu, end, s));
+      int start = __shfl_up_sync(0xffffffffu, end, 1);
+      if (lane == 0) start = row;
+      lo = max(lo, start);
+      cnt = max(0, cnt - lo);
+      row = __shfl_sync(0xffffffffu, end, 31);
+      const int mine = WGRAD ? (cnt + 127) >> 7 : (cnt + args.nmax - 1) / args.nmax;
+      int sum = mine;
+#pragma unroll
+      for (int s = 1; s < 32; s <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, sum, s);
+        if (lane >= s) sum += o;
+      }
+      const int first = before + sum - mine;
+      if (e < args.E) {
+        if (WGRAD) {  // a wrong table may count more blocks than there are
+          s_at[e] = min(first, (int)args.blocks);
+          s_cnt[e] = min(first + mine, (int)args.blocks) - s_at[e];
+        } else {
+          s_at[e] = lo;
+          s_cnt[e] = cnt;
+          s_first[e] = first;
+        }
+      }
+      before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    if (lane == 0) s_first[args.E] = before;
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers are initialised before either signals the other's
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int total = WGRAD ? args.E * args.MT * ((args.NB + args.nmax - 1) / args.nmax) : s_first[args.E] * args.MT;
+
+  if (warp < 4) {
+    reg_dec<F8_REGS_FEW>();
+    if (warp == 0) {
+      // ------------------------------------------------------------------ TMA producer (both CTAs)
+      if (lane == 0) {
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+        const uint64_t pol_a = l2_policy_evict_normal();
+        const uint64_t pol_once = l2_policy_evict_first();
+        const uint64_t pol_b = l2_policy_evict_last();  // read by every tile along A's rows
+        const uint32_t full0_cl = mapa_shared(full_bar(0), 0);
+        int stage = 0, issued = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int g = pair; g < total && ok; g += npairs) {
+          const Fp8Tile t = f8_tile<WGRAD>(g, args, s_at, s_cnt, s_first);
+          const int half = t.n >> 1;
+          const int nbox = (half + 31) >> 5;
+          const uint32_t pair_tx = 2u * (F8_A_BYTES + nbox * 32 * 128);
+          const uint64_t pa = !WGRAD && t.n == 16 ? pol_once : pol_a;
+          const int a_row = t.m * 256 + 128 * (int)rank;
+          const int b_row = t.col0 + (int)rank * half;
+          for (int kb = 0; kb < t.nkb; ++kb) {
+            if (!mbar_wait<true>(empty_bar(stage), phase ^ 1, abort_flag, args.status, SITE_GEMM_PRODUCER_EMPTY,
+                                 kWaitLimitNs, 32)) {
+              ok = false;
+              break;
+            }
+            const uint32_t fb = full0_cl + 8u * stage;
+            const uint32_t sa = smem_u32(smem + stage * F8_STAGE);
+            const uint32_t sb = sa + F8_A_BYTES;
+            if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), pair_tx);
+            const int k0 = (t.kb0 + kb) * 128;
+            tma_load_3d_pair(sa, &tmA, fb, k0, a_row, WGRAD ? 0 : t.e, pa);
+            for (int b = 0; b < nbox; ++b) tma_load_2d_pair(sb + b * 32 * 128, &tmB, fb, k0, b_row + 32 * b, pol_b);
+            ++issued;
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1;
+            }
+          }
+        }
+        if (!ok) {
+          if (rank == 0) {
+            // Aborted: wait for the stages that were armed, so that no copy is still landing when the pair exits.
+            const int outstanding = min(issued, STAGES);
+            int s = stage;
+            uint32_t ph = phase;
+            for (int i = 0; i < outstanding; ++i) {
+              if (--s < 0) {
+                s = STAGES - 1;
+                ph ^= 1;
+              }
+              volatile int no_abort = 0;
+              mbar_wait(full_bar(s), ph, &no_abort, args.status, SITE_GEMM_DRAIN);
+            }
+          } else {
+            // the peer cannot observe its own copies: give those in flight time to land
+            const uint64_t t0 = global_timer_ns();
+            while (global_timer_ns() - t0 < 100000ull) __nanosleep(1000);
+          }
+        }
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------------ MMA issuer (even CTA, one thread)
+      if (rank == 0 && lane == 0) {
+        int stage = 0, acc = 0;
+        uint32_t phase = 0, acc_phase = 0;
+        bool ok = true, any = false;
+        for (int g = pair; g < total && ok; g += npairs) {
+          const Fp8Tile t = f8_tile<WGRAD>(g, args, s_at, s_cnt, s_first);
+          const uint32_t idesc = idesc_e4m3_f32(256, t.n);
+          for (int kb = 0; kb < t.nkb; ++kb) {
+            if (!mbar_wait<true>(pempty_bar(acc), acc_phase ^ 1, abort_flag, args.status, SITE_GEMM_MMA_TMEM_EMPTY) ||
+                !mbar_wait<true>(full_bar(stage), phase, abort_flag, args.status, SITE_GEMM_MMA_FULL)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t sa = smem_u32(smem + stage * F8_STAGE);
+            const uint32_t sb = sa + F8_A_BYTES;
+  #pragma unroll
+            for (int k4 = 0; k4 < 4; ++k4)
+              umma_f8_pair(tmem_base + acc * 256, smem_desc_sw128(sa + k4 * 32, 16, 1024),
+                           smem_desc_sw128(sb + k4 * 32, 16, 1024), idesc, k4 != 0 ? 1u : 0u);
+            umma_commit_pair(empty_bar(stage), 0x3);
+            umma_commit_pair(pfull_bar(acc), 0x3);
+            any = true;
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1;
+            }
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1;
+          }
+        }
+        if (any) {
+          umma_commit_pair(drain_bar, 0x1);
+          volatile int no_abort = 0;
+          mbar_wait(drain_bar, 0, &no_abort, args.status, SITE_GEMM_DRAIN);
+        }
+      }
+      __syncwarp();
+    } else if (warp == 2) {
+      // ------------------------------------------------------------------ scales (both CTAs, each its own ring)
+      int q = 0;
+      uint32_t q_phase = 0;
+      bool ok = true;
+      for (int g = pair; g < total && ok; g += npairs) {
+        const Fp8Tile t = f8_tile<WGRAD>(g, args, s_at, s_cnt, s_first);
+        const int a_row = t.m * 256 + 128 * (int)rank;
+        for (int kb0 = 0; kb0 < t.nkb && ok; kb0 += 4) {
+          float b[4][8], a4[4][4];
+  #pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int64_t kb = t.kb0 + min(kb0 + j, t.nkb - 1);
+            if (WGRAD) {
+  #pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int r = a_row + i * 32 + lane;
+                a4[j][i] = r < args.NM ? __ldg(args.a_scale + kb * args.NM + r) : 0.0f;
+              }
+            } else {
+              const int tiles = (args.NM + 127) >> 7;
+              a4[j][0] = a_row < args.NM ? __ldg(args.a_scale + ((int64_t)t.e * tiles + (a_row >> 7)) * args.nkb + kb) : 0.0f;
+            }
+  #pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int c = i * 32 + lane;
+              b[j][i] = c < t.cols ? __ldg(args.b_scale + kb * args.b_ld + t.col0 + c) : 0.0f;
+            }
+          }
+  #pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (kb0 + j < t.nkb && ok) {
+              int w = 1;
+              if (lane == 0) w = mbar_wait(sempty_bar(q), q_phase ^ 1, abort_flag, args.status, SITE_FP8_SCALES, kWaitLimitNs, 32);
+              ok = __shfl_sync(0xffffffffu, w, 0);
+              if (ok) {
+                float* s = slots + q * (F8_SLOT / 4);
+  #pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  if (i * 32 < t.n) s[i * 32 + lane] = WGRAD ? b[j][i] : b[j][i] * a4[j][0];
+                if (WGRAD) {
+  #pragma unroll
+                  for (int i = 0; i < 4; ++i) s[256 + i * 32 + lane] = a4[j][i];
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sfull_bar(q));
+                if (++q == SLOTS) {
+                  q = 0;
+                  q_phase ^= 1;
+                }
+              }
+            }
+          }
+        }
+      }
+    }
+  } else {
+    reg_inc<F8_REGS_EPI>();
+    // ------------------------------------------------------------------ epilogue (both CTAs)
+    const int quarter = warp & 3;
+    const int side = (warp - 4) >> 2;  // 32-column pieces 2 i + side are this warp's
+    const uint32_t pempty0_cl = mapa_shared(pempty_bar(0), 0);
+    const uint32_t tlane = uint32_t(quarter * 32) << 16;
+    int acc = 0, q = 0;
+    uint32_t acc_phase = 0, q_phase = 0;
+    bool ok = true;
+    for (int g = pair; g < total && ok; g += npairs) {
+      const Fp8Tile t = f8_tile<WGRAD>(g, args, s_at, s_cnt, s_first);
+      F2 sum[4][16];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) sum[i][j] = f2(0.0f);
+      for (int kb = 0; kb < t.nkb; ++kb) {
+        int w = 1;
+        if (lane == 0)
+          w = mbar_wait(sfull_bar(q), q_phase, abort_flag, args.status, SITE_FP8_SCALES) &&
+              mbar_wait<true>(pfull_bar(acc), acc_phase, abort_flag, args.status, SITE_GEMM_EPI_TMEM_FULL);
+        if (!__shfl_sync(0xffffffffu, w, 0)) {
+          ok = false;
+          break;
+        }
+        __syncwarp();
+        tc_fence_after();
+        const float* s = slots + q * (F8_SLOT / 4);
+        F2 sa = 0;
+        if (WGRAD) sa = f2(s[256 + quarter * 32 + lane]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c0 = (2 * i + side) * 32;
+          if (c0 < t.n) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t v[16];
+              tmem_ld_32x32b_x16(tmem_base + acc * 256 + tlane + c0 + 16 * h, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float4 f = *reinterpret_cast<const float4*>(s + c0 + 16 * h + 4 * j);
+                F2 p0 = f2(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]));
+                F2 p1 = f2(__uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
+                if (WGRAD) {
+                  p0 = mul2(p0, sa);
+                  p1 = mul2(p1, sa);
+                }
+                F2* d = &sum[i][8 * h + 2 * j];
+                d[0] = fma2(p0, f2(f.x, f.y), d[0]);
+                d[1] = fma2(p1, f2(f.z, f.w), d[1]);
+              }
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_cluster_relaxed(pempty0_cl + 8u * acc);
+          mbar_arrive(sempty_bar(q));
+        }
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1;
+        if (++q == SLOTS) {
+          q = 0;
+          q_phase ^= 1;
+        }
+      }
+      if (!ok) break;
+      const int j = t.m * 256 + 128 * (int)rank + 32 * quarter + lane;
+      if (j < args.NM) {
+        OUT* out = static_cast<OUT*>(args.out) + (WGRAD ? ((int64_t)t.e * args.NB + t.col0) : (int64_t)t.col0) * args.ld + j;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c0 = (2 * i + side) * 32;
+          OUT* o = out + (int64_t)c0 * args.ld;
+          const int left = t.cols - c0;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            float a, b;
+            split(sum[i][k], a, b);
+            if (2 * k < left) f8_put(o, a);
+            o += args.ld;
+            if (2 * k + 1 < left) f8_put(o, b);
+            o += args.ld;
+          }
+        }
+      }
+      __syncwarp();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // neither CTA leaves while the pair's MMAs or signals may still touch it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+// E4M3 rows [groups][rows][K], `ld` bytes apart, in boxes of 128 bytes x box_rows; bytes behind K and rows behind
+// `rows` read as zero.
+bool tmap_e4m3_rows(CUtensorMap* m, const void* base, int64_t K, int64_t rows, int64_t groups, int64_t ld, uint32_t box_rows,
+                    bool grouped) {
+  const uint64_t dims[3] = {(uint64_t)K, (uint64_t)rows, (uint64_t)groups};
+  const uint64_t strides[2] = {(uint64_t)ld, (uint64_t)(ld * rows)};
+  const uint32_t box[3] = {128, box_rows, 1};
+  return make_tmap(m, base, grouped ? 3 : 2, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8);
+}
+
+template <bool WGRAD, typename OUT>
+cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const Fp8GemmArgs& args, int64_t tiles, int n_sm,
+                   cudaStream_t st) {
+  auto kern = fp8_gemm_kernel<WGRAD, OUT>;
+  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)f8_smem(FP8_MAX_E));
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(F8_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = f8_smem(args.E);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(tiles, std::max(1, n_sm / 2))), 1, 1);
+  err = cudaLaunchKernelEx(&cfg, kern, ta, tb, args);
+  return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_product_pairs(const Fp8MatmulArgs& a, bool bf16_out, int n_sm, cudaStream_t st) {
+  Fp8GemmArgs g = {};
+  g.E = a.E;
+  g.nkb = (int)((a.K + 127) / 128);
+  g.NM = (int)a.N;
+  g.MT = (int)((a.N + 255) / 256);
+  g.R = a.R;
+  g.offsets = a.offsets;
+  g.a_scale = a.w_scale;
+  g.b_scale = a.x_scale;
+  g.b_ld = a.x_scale_stride;
+  g.out = a.out;
+  g.ld = a.out_stride;
+  g.status = a.status;
+  // narrower chunks while the tiles of wider ones leave pairs without work
+  g.nmax = 256;
+  const int64_t pairs = std::max(1, n_sm / 2);
+  while (g.nmax > 32 && g.MT * std::max<int64_t>((a.R + g.nmax - 1) / g.nmax, std::min<int64_t>(a.E, a.R)) < pairs)
+    g.nmax /= 2;
+  const int64_t tiles = ((a.R + g.nmax - 1) / g.nmax + a.E) * g.MT;  // at most
+  if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+  CUtensorMap ta, tb;
+  if (!tmap_e4m3_rows(&ta, a.w, a.K, a.N, a.E, a.w_stride, 128, true) ||
+      !tmap_e4m3_rows(&tb, a.x, a.K, a.R, 1, a.x_stride, 32, false))
+    return cudaErrorInvalidValue;
+  return bf16_out ? launch<false, __nv_bfloat16>(ta, tb, g, tiles, n_sm, st) : launch<false, float>(ta, tb, g, tiles, n_sm, st);
+}
+
+cudaError_t launch_fp8_weight_grad(const Fp8WeightGradArgs& a, bool bf16_out, int n_sm, cudaStream_t st) {
+  Fp8GemmArgs g = {};
+  g.E = a.E;
+  g.NM = (int)a.H;
+  g.NB = (int)a.N;
+  g.MT = (int)((a.H + 255) / 256);
+  g.R = a.R;
+  g.blocks = a.R / 128 + a.E;
+  g.offsets = a.offsets;
+  g.a_scale = a.x_scale;
+  g.b_scale = a.dy_scale;
+  g.b_ld = a.N;
+  g.out = a.out;
+  g.ld = a.H;
+  g.status = a.status;
+  g.nmax = 256;
+  const int64_t pairs = std::max(1, n_sm / 2);
+  while (g.nmax > 32 && a.E * g.MT * ((a.N + g.nmax - 1) / g.nmax) < pairs) g.nmax /= 2;
+  const int64_t tiles = a.E * (int64_t)g.MT * ((a.N + g.nmax - 1) / g.nmax);
+  if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+  CUtensorMap ta, tb;
+  const int64_t P = 128 * g.blocks;
+  if (!tmap_e4m3_rows(&ta, a.x, P, a.H, 1, a.x_stride, 128, true) ||
+      !tmap_e4m3_rows(&tb, a.dy, P, a.N, 1, a.dy_stride, 32, false))
+    return cudaErrorInvalidValue;
+  return bf16_out ? launch<true, __nv_bfloat16>(ta, tb, g, tiles, n_sm, st) : launch<true, float>(ta, tb, g, tiles, n_sm, st);
+}
+
+}  // namespace mok

@@ -266,8 +266,8 @@ __global__ void __launch_bounds__(THREADS, 2) fp8_columns_kernel(const Fp8Quanti
     const int e = e0 + threadIdx.x;
     int lo = 0, hi = 0;
     if (e < a.E) {
-      lo = max(0, (int)min((int64_t)a.offsets[e], a.R));
-      hi = max(lo, (int)min((int64_t)a.offsets[e + 1], a.R));
+      lo = fp8_offset(a.offsets[e], 0, a.R);
+      hi = fp8_offset(a.offsets[e + 1], lo, a.R);
     }
     const int mine = (hi - lo + 127) >> 7;
     int sum = mine;
@@ -292,9 +292,9 @@ __global__ void __launch_bounds__(THREADS, 2) fp8_columns_kernel(const Fp8Quanti
     before += total;
     __syncthreads();
   }
-  const int rows = s_where[1];
-  if (rows == 0) return;  // behind the last expert's blocks
   const int64_t row0 = s_where[0];
+  const int rows = s_where[1] == 0 ? 0 : (int)min((int64_t)s_where[1], a.R - row0);  // whatever the table says
+  if (rows <= 0) return;  // behind the last expert's blocks
   const int w = threadIdx.x >> 4, l = threadIdx.x & 15;
   const int b_end = min(col_blocks, (int)(blockIdx.x % groups + 1) * group);
   for (int b = (blockIdx.x % groups) * group; b < b_end; ++b) {

@@ -25,7 +25,7 @@ enum StatusSite : int {
   SITE_ROWS_GATHER = 40,
   SITE_ROWS_MERGE = 41,
   SITE_FP8_SOURCE = 42,
-  SITE_FP8_OFFSETS = 43,
+  SITE_FP8_SCALES = 43,
 };
 
 // status[0] = code of the first error, status[1] = its site.

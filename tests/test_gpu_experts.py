@@ -466,7 +466,7 @@ def test_weight_grad(counts, N, H, dtype):
 
 
 def test_bad_offsets_stay_in_the_tensors():
-    """An offset out of range or below its predecessor counts as the nearest that is not."""
+    """Offsets out of range or out of order: nothing outside the tensors is touched; ends behind R count as R."""
     rng = np.random.default_rng(8)
     R, N, K, E = 100, 70, 200, 4
     x, xs = random_e4m3(rng, (R, K)), scales(rng, (2, R))
