@@ -22,6 +22,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "f32x2.cuh"
 #include "fp8.cuh"
@@ -46,21 +47,28 @@ struct Fp8GemmArgs {
   int64_t b_ld;
   void* out;
   int64_t ld;             // elements between out's rows
+  int mixed;              // TMEM lane 8 k + u of a quarter holds A's row 4 u + k, else the rows are in order
+  int wide_out;           // mixed, and out's rows take four neighbours at once
   int* status;
 };
 
 constexpr int F8_STAGES = 6;
-constexpr int F8_SLOTS = 8;
+constexpr int F8_SLOTS = 3;
+constexpr int F8_GROUP = 4;  // K blocks whose scales share a slot
 constexpr int F8_A_BYTES = 128 * 128;
 constexpr int F8_B_BYTES = 128 * 128;
 constexpr int F8_STAGE = F8_A_BYTES + F8_B_BYTES;
-constexpr int F8_SLOT = (256 + 128) * 4;  // the columns' scales, and (weight grad) the lanes'
+constexpr int F8_SLOT_BLOCK = 256 + 128;  // floats of a block in a slot: the columns' scales, and (weight grad) the lanes'
+constexpr int F8_SLOT = F8_GROUP * F8_SLOT_BLOCK * 4;
 constexpr int F8_EPI_WARPS = 8;
 constexpr int F8_THREADS = 32 * (4 + F8_EPI_WARPS);
 // Registers of a thread: 168 at launch (384 threads of them are the register file); the epilogue's 128 f32 sums
-// need more: 128 x 88 + 256 x 208 = 64,512 = 384 x 168.
-constexpr int F8_REGS_FEW = 88, F8_REGS_EPI = 208;
-static_assert(128 * F8_REGS_FEW + 256 * F8_REGS_EPI <= F8_THREADS * 168, "register split");
+// need more, and the scales' warp of the weight gradient too: 128 x 72 + 256 x 216 = 128 x 88 + 256 x 208 = 384 x 168.
+template <bool WGRAD>
+struct F8Regs {
+  static constexpr int FEW = WGRAD ? 88 : 72, EPI = WGRAD ? 208 : 216;
+  static_assert(128 * FEW + 256 * EPI <= F8_THREADS * 168, "register split");
+};
 constexpr int F8_SMEM_BARS = 512;
 constexpr size_t f8_smem(int E) {
   return 1024 + size_t(F8_STAGES) * F8_STAGE + size_t(F8_SLOTS) * F8_SLOT + F8_SMEM_BARS + size_t(3) * (E + 1) * 4;
@@ -114,6 +122,43 @@ __device__ __forceinline__ Fp8Tile f8_tile(int g, const Fp8GemmArgs& a, const in
   return t;
 }
 
+// A bounded wait by all lanes of a warp together.  The timer is read only once a wait has gone on for a while: reading
+// it takes longer than most waits here do.
+__device__ __forceinline__ bool f8_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status, int site) {
+  if (mbar_try_wait(bar, parity)) return true;
+  uint64_t t0 = 0;
+  uint32_t spins = 0;
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity)) {
+    if ((++spins & 63u) == 0) {
+      if (*abort_flag) return false;
+      const uint64_t now = global_timer_ns();
+      if (t0 == 0) {
+        t0 = now;
+      } else if (now - t0 > kWaitLimitNs) {
+        *abort_flag = 1;
+        report_status(status, MOK_DEV_TIMEOUT, site);
+        return false;
+      }
+    }
+  }
+  return true;
+}
+
+// Blocks of K whose sums share an accumulator of 256 columns: narrow tiles hand over several at once, since handing
+// over costs the epilogue as much as 128 columns do.
+__device__ __forceinline__ int f8_blocks_at_once(int n) { return n <= 64 ? 4 : n <= 128 ? 2 : 1; }
+
+// Where column c (of 32) has its scale: the four columns 8 g + 2 t, + 1 of two neighbouring g that a lane (t = lane % 4) holds
+// follow each other.
+__device__ __forceinline__ int f8_scale_at(int c) { return (c >> 4) * 16 + ((c >> 1) & 3) * 4 + ((c >> 3) & 1) * 2 + (c & 1); }
+
+__device__ __forceinline__ void f8_put4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void f8_put4(__nv_bfloat16* p, float4 v) {
+  __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+}
+
 __device__ __forceinline__ void f8_put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void f8_put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
@@ -121,11 +166,12 @@ __device__ __forceinline__ void f8_put(__nv_bfloat16* p, float v) { *p = __float
 template <bool WGRAD, typename OUT>
 __global__ void __launch_bounds__(F8_THREADS, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ CUtensorMap tmB64, const __grid_constant__ CUtensorMap tmB32,
                     const Fp8GemmArgs args) {
   constexpr int STAGES = F8_STAGES, SLOTS = F8_SLOTS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* slots = reinterpret_cast<float*>(smem + STAGES * F8_STAGE);
+  const uint32_t slots0 = smem_u32(smem) + STAGES * F8_STAGE;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * F8_STAGE + SLOTS * F8_SLOT);
   // bars: full, empty [STAGES], pfull, pempty [2], sfull, sempty [SLOTS], drain; the TMEM address; the abort flag
   constexpr int NBARS = 2 * STAGES + 4 + 2 * SLOTS + 1;
@@ -136,18 +182,19 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
   int* s_cnt = s_at + (args.E + 1);
   int* s_first = s_cnt + (args.E + 1);
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);  // uniform, and known to be
   const int lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int pair = (int)blockIdx.x >> 1;
   const int npairs = (int)gridDim.x >> 1;
-  auto full_bar = [&](int s) { return smem_u32(&bars[s]); };
-  auto empty_bar = [&](int s) { return smem_u32(&bars[STAGES + s]); };
-  auto pfull_bar = [&](int a) { return smem_u32(&bars[2 * STAGES + a]); };
-  auto pempty_bar = [&](int a) { return smem_u32(&bars[2 * STAGES + 2 + a]); };
-  auto sfull_bar = [&](int q) { return smem_u32(&bars[2 * STAGES + 4 + q]); };
-  auto sempty_bar = [&](int q) { return smem_u32(&bars[2 * STAGES + 4 + SLOTS + q]); };
-  const uint32_t drain_bar = smem_u32(&bars[2 * STAGES + 4 + 2 * SLOTS]);
+  const uint32_t bars0 = smem_u32(bars);
+  auto full_bar = [&](int s) { return bars0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bars0 + 8u * (STAGES + s); };
+  auto pfull_bar = [&](int a) { return bars0 + 8u * (2 * STAGES + a); };
+  auto pempty_bar = [&](int a) { return bars0 + 8u * (2 * STAGES + 2 + a); };
+  auto sfull_bar = [&](int q) { return bars0 + 8u * (2 * STAGES + 4 + q); };
+  auto sempty_bar = [&](int q) { return bars0 + 8u * (2 * STAGES + 4 + SLOTS + q); };
+  const uint32_t drain_bar = bars0 + 8u * (2 * STAGES + 4 + 2 * SLOTS);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -224,108 +271,124 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
   const int total = WGRAD ? args.E * args.MT * ((args.NB + args.nmax - 1) / args.nmax) : s_first[args.E] * args.MT;
 
   if (warp < 4) {
-    reg_dec<F8_REGS_FEW>();
+    reg_dec<F8Regs<WGRAD>::FEW>();
     if (warp == 0) {
       // ------------------------------------------------------------------ TMA producer (both CTAs)
-      if (lane == 0) {
+      const bool leader = elect_one();
+      if (leader) {
         tma_prefetch_desc(&tmA);
         tma_prefetch_desc(&tmB);
-        const uint64_t pol_a = l2_policy_evict_normal();
-        const uint64_t pol_once = l2_policy_evict_first();
-        const uint64_t pol_b = l2_policy_evict_last();  // read by every tile along A's rows
-        const uint32_t full0_cl = mapa_shared(full_bar(0), 0);
-        int stage = 0, issued = 0;
-        uint32_t phase = 0;
-        bool ok = true;
-        for (int g = pair; g < total && ok; g += npairs) {
-          const Fp8Tile t = f8_tile<WGRAD>(g, args, s_at, s_cnt, s_first);
-          const int half = t.n >> 1;
-          const int nbox = (half + 31) >> 5;
-          const uint32_t pair_tx = 2u * (F8_A_BYTES + nbox * 32 * 128);
-          const uint64_t pa = !WGRAD && t.n == 16 ? pol_once : pol_a;
-          const int a_row = t.m * 256 + 128 * (int)rank;
-          const int b_row = t.col0 + (int)rank * half;
-          for (int kb = 0; kb < t.nkb; ++kb) {
-            if (!mbar_wait<true>(empty_bar(stage), phase ^ 1, abort_flag, args.status, SITE_GEMM_PRODUCER_EMPTY,
-                                 kWaitLimitNs, 32)) {
-              ok = false;
-              break;
-            }
+      }
+      const uint64_t pol_a = l2_policy_evict_normal();
+      const uint64_t pol_once = l2_policy_evict_first();
+      const uint64_t pol_b = l2_policy_evict_last();  // read by every tile along A's rows
+      const uint32_t full0_cl = mapa_shared(full_bar(0), 0);
+      const uint32_t smem0 = smem_u32(smem);
+      int stage = 0, issued = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int g = pair; g < total && ok; g += npairs) {
+        const Fp8Tile t = f8_tile<WGRAD>(g, args, s_at, s_cnt, s_first);
+        const int half = t.n >> 1;
+        // the CTA's rows of B in the fewest boxes of 128, 64 and 32 rows
+        const int b128 = half > 96, b64 = !b128 && half > 32, b32 = !b128 && (half <= 32 || half > 64);
+        const uint32_t pair_tx = 2u * (F8_A_BYTES + (b128 * 128 + b64 * 64 + b32 * 32) * 128);
+        const uint64_t pa = !WGRAD && t.n == 16 ? pol_once : pol_a;
+        const int a_row = t.m * 256 + 128 * (int)rank;
+        const int b_row = t.col0 + (int)rank * half;
+        for (int kb = 0; kb < t.nkb; ++kb) {
+          ok = __all_sync(0xffffffffu,
+                          f8_wait(empty_bar(stage), phase ^ 1, abort_flag, args.status, SITE_GEMM_PRODUCER_EMPTY));
+          if (!ok) break;
+          if (leader) {
             const uint32_t fb = full0_cl + 8u * stage;
-            const uint32_t sa = smem_u32(smem + stage * F8_STAGE);
+            const uint32_t sa = smem0 + stage * F8_STAGE;
             const uint32_t sb = sa + F8_A_BYTES;
             if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), pair_tx);
             const int k0 = (t.kb0 + kb) * 128;
-            tma_load_3d_pair(sa, &tmA, fb, k0, a_row, WGRAD ? 0 : t.e, pa);
-            for (int b = 0; b < nbox; ++b) tma_load_2d_pair(sb + b * 32 * 128, &tmB, fb, k0, b_row + 32 * b, pol_b);
-            ++issued;
-            if (++stage == STAGES) {
-              stage = 0;
-              phase ^= 1;
-            }
+            if (args.mixed) tma_load_5d_pair(sa, &tmA, fb, k0, 0, 0, a_row >> 5, WGRAD ? 0 : t.e, pa);
+            else tma_load_3d_pair(sa, &tmA, fb, k0, a_row, WGRAD ? 0 : t.e, pa);
+            if (b128) tma_load_2d_pair(sb, &tmB, fb, k0, b_row, pol_b);
+            if (b64) tma_load_2d_pair(sb, &tmB64, fb, k0, b_row, pol_b);
+            if (b32) tma_load_2d_pair(sb + b64 * 64 * 128, &tmB32, fb, k0, b_row + b64 * 64, pol_b);
           }
-        }
-        if (!ok) {
-          if (rank == 0) {
-            // Aborted: wait for the stages that were armed, so that no copy is still landing when the pair exits.
-            const int outstanding = min(issued, STAGES);
-            int s = stage;
-            uint32_t ph = phase;
-            for (int i = 0; i < outstanding; ++i) {
-              if (--s < 0) {
-                s = STAGES - 1;
-                ph ^= 1;
-              }
-              volatile int no_abort = 0;
-              mbar_wait(full_bar(s), ph, &no_abort, args.status, SITE_GEMM_DRAIN);
-            }
-          } else {
-            // the peer cannot observe its own copies: give those in flight time to land
-            const uint64_t t0 = global_timer_ns();
-            while (global_timer_ns() - t0 < 100000ull) __nanosleep(1000);
+          __syncwarp();
+          ++issued;
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1;
           }
         }
       }
+      if (!ok) {
+        if (rank == 0) {
+          // Aborted: wait for the stages that were armed, so that no copy is still landing when the pair exits.
+          const int outstanding = min(issued, STAGES);
+          int s = stage;
+          uint32_t ph = phase;
+          for (int i = 0; i < outstanding; ++i) {
+            if (--s < 0) {
+              s = STAGES - 1;
+              ph ^= 1;
+            }
+            volatile int no_abort = 0;
+            f8_wait(full_bar(s), ph, &no_abort, args.status, SITE_GEMM_DRAIN);
+          }
+        } else {
+          // the peer cannot observe its own copies: give those in flight time to land
+          const uint64_t t0 = global_timer_ns();
+          while (global_timer_ns() - t0 < 100000ull) __nanosleep(1000);
+        }
+      }
     } else if (warp == 1) {
-      // ------------------------------------------------------------------ MMA issuer (even CTA, one thread)
-      if (rank == 0 && lane == 0) {
+      // ------------------------------------------------------------------ MMA issuer (even CTA)
+      // The whole warp goes through the loop, one thread issues: the descriptors then stay in uniform registers.
+      if (rank == 0) {
+        const bool leader = elect_one();
+        const uint64_t adesc0 = smem_desc_sw128(smem_u32(smem), 16, 1024);
+        const uint64_t bdesc0 = smem_desc_sw128(smem_u32(smem) + F8_A_BYTES, 16, 1024);
         int stage = 0, acc = 0;
         uint32_t phase = 0, acc_phase = 0;
         bool ok = true, any = false;
         for (int g = pair; g < total && ok; g += npairs) {
           const Fp8Tile t = f8_tile<WGRAD>(g, args, s_at, s_cnt, s_first);
           const uint32_t idesc = idesc_e4m3_f32(256, t.n);
+          const int per = f8_blocks_at_once(t.n), width = 256 / per;
           for (int kb = 0; kb < t.nkb; ++kb) {
-            if (!mbar_wait<true>(pempty_bar(acc), acc_phase ^ 1, abort_flag, args.status, SITE_GEMM_MMA_TMEM_EMPTY) ||
-                !mbar_wait<true>(full_bar(stage), phase, abort_flag, args.status, SITE_GEMM_MMA_FULL)) {
-              ok = false;
-              break;
-            }
+            const int sub = kb & (per - 1);
+            const bool last = sub == per - 1 || kb == t.nkb - 1;
+            ok = f8_wait(full_bar(stage), phase, abort_flag, args.status, SITE_GEMM_MMA_FULL) &&
+                 (sub != 0 || f8_wait(pempty_bar(acc), acc_phase ^ 1, abort_flag, args.status, SITE_GEMM_MMA_TMEM_EMPTY));
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
             tc_fence_after();
-            const uint32_t sa = smem_u32(smem + stage * F8_STAGE);
-            const uint32_t sb = sa + F8_A_BYTES;
-  #pragma unroll
-            for (int k4 = 0; k4 < 4; ++k4)
-              umma_f8_pair(tmem_base + acc * 256, smem_desc_sw128(sa + k4 * 32, 16, 1024),
-                           smem_desc_sw128(sb + k4 * 32, 16, 1024), idesc, k4 != 0 ? 1u : 0u);
-            umma_commit_pair(empty_bar(stage), 0x3);
-            umma_commit_pair(pfull_bar(acc), 0x3);
+            const uint64_t off = (uint64_t)(stage * (F8_STAGE >> 4));
+            if (leader) {
+#pragma unroll
+              for (int k4 = 0; k4 < 4; ++k4)
+                umma_f8_pair(tmem_base + acc * 256 + sub * width, adesc0 + off + 2 * k4, bdesc0 + off + 2 * k4, idesc, k4 != 0 ? 1u : 0u);
+              umma_commit_pair(empty_bar(stage), 0x3);
+              if (last) umma_commit_pair(pfull_bar(acc), 0x3);
+            }
+            __syncwarp();
             any = true;
             if (++stage == STAGES) {
               stage = 0;
               phase ^= 1;
             }
-            acc ^= 1;
-            if (acc == 0) acc_phase ^= 1;
+            if (last) {
+              acc ^= 1;
+              if (acc == 0) acc_phase ^= 1;
+            }
           }
         }
         if (any) {
-          umma_commit_pair(drain_bar, 0x1);
+          if (leader) umma_commit_pair(drain_bar, 0x1);
           volatile int no_abort = 0;
-          mbar_wait(drain_bar, 0, &no_abort, args.status, SITE_GEMM_DRAIN);
+          f8_wait(drain_bar, 0, &no_abort, args.status, SITE_GEMM_DRAIN);
         }
+        __syncwarp();
       }
-      __syncwarp();
     } else if (warp == 2) {
       // ------------------------------------------------------------------ scales (both CTAs, each its own ring)
       int q = 0;
@@ -334,10 +397,10 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
       for (int g = pair; g < total && ok; g += npairs) {
         const Fp8Tile t = f8_tile<WGRAD>(g, args, s_at, s_cnt, s_first);
         const int a_row = t.m * 256 + 128 * (int)rank;
-        for (int kb0 = 0; kb0 < t.nkb && ok; kb0 += 4) {
-          float b[4][8], a4[4][4];
+        for (int kb0 = 0; kb0 < t.nkb; kb0 += F8_GROUP) {
+          float b[F8_GROUP][8], a4[F8_GROUP][4];
   #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < F8_GROUP; ++j) {
             const int64_t kb = t.kb0 + min(kb0 + j, t.nkb - 1);
             if (WGRAD) {
   #pragma unroll
@@ -355,123 +418,170 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
               b[j][i] = c < t.cols ? __ldg(args.b_scale + kb * args.b_ld + t.col0 + c) : 0.0f;
             }
           }
-  #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (kb0 + j < t.nkb && ok) {
-              int w = 1;
-              if (lane == 0) w = mbar_wait(sempty_bar(q), q_phase ^ 1, abort_flag, args.status, SITE_FP8_SCALES, kWaitLimitNs, 32);
-              ok = __shfl_sync(0xffffffffu, w, 0);
-              if (ok) {
-                float* s = slots + q * (F8_SLOT / 4);
-  #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  if (i * 32 < t.n) s[i * 32 + lane] = WGRAD ? b[j][i] : b[j][i] * a4[j][0];
-                if (WGRAD) {
-  #pragma unroll
-                  for (int i = 0; i < 4; ++i) s[256 + i * 32 + lane] = a4[j][i];
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(sfull_bar(q));
-                if (++q == SLOTS) {
-                  q = 0;
-                  q_phase ^= 1;
-                }
-              }
+            ok = __all_sync(0xffffffffu, f8_wait(sempty_bar(q), q_phase ^ 1, abort_flag, args.status, SITE_FP8_SCALES));
+          if (!ok) break;
+#pragma unroll
+          for (int j = 0; j < F8_GROUP; ++j) {
+            const uint32_t s = slots0 + q * F8_SLOT + j * (F8_SLOT_BLOCK * 4);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (i * 32 < t.n) sts1(s + 4 * (i * 32 + f8_scale_at(lane)), WGRAD ? b[j][i] : b[j][i] * a4[j][0]);
+            if (WGRAD) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) sts1(s + 4 * (256 + i * 32 + lane), a4[j][i]);
             }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sfull_bar(q));
+          if (++q == SLOTS) {
+            q = 0;
+            q_phase ^= 1;
           }
         }
       }
     }
   } else {
-    reg_inc<F8_REGS_EPI>();
+    reg_inc<F8Regs<WGRAD>::EPI>();
     // ------------------------------------------------------------------ epilogue (both CTAs)
     const int quarter = warp & 3;
     const int side = (warp - 4) >> 2;  // 32-column pieces 2 i + side are this warp's
     const uint32_t pempty0_cl = mapa_shared(pempty_bar(0), 0);
-    const uint32_t tlane = uint32_t(quarter * 32) << 16;
+    const uint32_t tlane = tmem_base + (uint32_t(quarter * 32) << 16) + side * 32;
+    const uint32_t lane_slot = side * 128 + 16 * (lane & 3), lane_rows = 4 * (256 + quarter * 32 + (lane >> 2) * (args.mixed ? 4 : 1)), row_step = args.mixed ? 4 : 32;
+    const bool leader = elect_one();
     int acc = 0, q = 0;
     uint32_t acc_phase = 0, q_phase = 0;
-    bool ok = true;
+    bool ok = true, ready = false;
     for (int g = pair; g < total && ok; g += npairs) {
       const Fp8Tile t = f8_tile<WGRAD>(g, args, s_at, s_cnt, s_first);
-      F2 sum[4][16];
+      // sum[s]: piece s / 2, TMEM lanes 16 (s % 2) of the quarter: [g][row lane / 4, + 8], columns 2 t, 2 t + 1 of group g
+      float sum[8][4][2][2];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          sum[i][j >> 1][j & 1][0] = sum[i][j >> 1][j & 1][1] = 0.0f;
+        }
+      // G blocks at once, of which this warp has NP pieces each
+      auto run = [&](auto pieces, auto at_once) {
+        constexpr int NP = decltype(pieces)::value, G = decltype(at_once)::value, S = 2 * NP;
+        for (int kb = 0; kb < t.nkb; kb += G) {
+          if ((kb & (F8_GROUP - 1)) == 0)
+            ok = __all_sync(0xffffffffu, f8_wait(sfull_bar(q), q_phase, abort_flag, args.status, SITE_FP8_SCALES));
+          if (!ready)
+            ok = __all_sync(0xffffffffu,
+                            f8_wait(pfull_bar(acc), acc_phase, abort_flag, args.status, SITE_GEMM_EPI_TMEM_FULL) && ok);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t s0 = slots0 + q * F8_SLOT + (kb & (F8_GROUP - 1)) * (F8_SLOT_BLOCK * 4);
+          const int blocks = min(G, t.nkb - kb);
+#pragma unroll
+          for (int g8 = 0; g8 < G; ++g8) {
+            if (G == 1 || g8 < blocks) {
+              const bool final = G == 1 || g8 == blocks - 1;
+              const uint32_t s = s0 + g8 * (F8_SLOT_BLOCK * 4);
+              const uint32_t tacc = tlane + acc * 256 + g8 * (256 / G);
+              const uint32_t sl = s + lane_slot;
+              float sa[4];
+              if (WGRAD) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sa[i] = lds1(s + lane_rows + row_step * i);
+              }
+              uint32_t v[2][16];
+              float4 f[2];
+              if (S > 0) {
+                tmem_ld_16x256b_x4(tacc, v[0]);
+                f[0] = lds4(sl);
+                f[1] = lds4(sl + 64);
+                tmem_wait_ld();
+              }
+              auto done = [&]() {  // the accumulator is in registers
+                tc_fence_before();
+                const bool next = mbar_test_wait(pfull_bar(acc ^ 1), acc_phase ^ (uint32_t)acc);
+                __syncwarp();
+                if (leader) mbar_arrive_cluster_relaxed(pempty0_cl + 8u * acc);
+                ready = __all_sync(0xffffffffu, next);
+              };
+              if (S == 0 && final) done();
+#pragma unroll
+              for (int p = 0; p < S; ++p) {
+                if (p + 1 < S)
+                  tmem_ld_16x256b_x4(tacc + ((p + 1) >> 1) * 64 + ((p + 1) & 1) * (16u << 16), v[(p + 1) & 1]);
+                else if (final)
+                  done();
+                const float c[4][2] = {{f[0].x, f[0].y}, {f[0].z, f[0].w}, {f[1].x, f[1].y}, {f[1].z, f[1].w}};
+                if ((p & 1) && p + 1 < S) {
+                  f[0] = lds4(sl + ((p + 1) >> 1) * 256);
+                  f[1] = lds4(sl + ((p + 1) >> 1) * 256 + 64);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                  for (int r = 0; r < 2; ++r) {
+                    float x0 = __uint_as_float(v[p & 1][4 * j + 2 * r]), x1 = __uint_as_float(v[p & 1][4 * j + 2 * r + 1]);
+                    if (WGRAD) {
+                      x0 *= sa[2 * (p & 1) + r];
+                      x1 *= sa[2 * (p & 1) + r];
+                    }
+                    sum[p][j][r][0] = fmaf(x0, c[j][0], sum[p][j][r][0]);
+                    sum[p][j][r][1] = fmaf(x1, c[j][1], sum[p][j][r][1]);
+                  }
+                if (p + 1 < S) tmem_wait_ld();
+              }
+            }
+          }
+          if ((kb & (F8_GROUP - 1)) + G >= F8_GROUP || kb + G >= t.nkb) {
+            __syncwarp();
+            if (leader) mbar_arrive(sempty_bar(q));
+            if (++q == SLOTS) {
+              q = 0;
+              q_phase ^= 1;
+            }
+          }
+          acc ^= 1;
+          if (acc == 0) acc_phase ^= 1;
+        }
+      };
+      using one = std::integral_constant<int, 1>;
+      using two = std::integral_constant<int, 2>;
+      using three = std::integral_constant<int, 3>;
+      using four = std::integral_constant<int, 4>;
+      const int pieces = (t.n + 31) >> 5;
+      if (pieces > 6 + side) run(four{}, one{});
+      else if (pieces > 4) run(three{}, one{});
+      else if (pieces > 2) run(two{}, two{});
+      else run(one{}, four{});
+      if (!ok) break;
+      // out[column][row]: of a column a lane has four rows, neighbours where the rows are mixed
+      const int u = lane >> 2;
+      const int j0 = t.m * 256 + 128 * (int)rank + 32 * quarter + (args.mixed ? 4 * u : u);
+      const int jstep = args.mixed ? 1 : 8;
+      OUT* out = static_cast<OUT*>(args.out) + (WGRAD ? (int64_t)t.e * args.NB + t.col0 : (int64_t)t.col0) * args.ld + j0;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) sum[i][j] = f2(0.0f);
-      for (int kb = 0; kb < t.nkb; ++kb) {
-        int w = 1;
-        if (lane == 0)
-          w = mbar_wait(sfull_bar(q), q_phase, abort_flag, args.status, SITE_FP8_SCALES) &&
-              mbar_wait<true>(pfull_bar(acc), acc_phase, abort_flag, args.status, SITE_GEMM_EPI_TMEM_FULL);
-        if (!__shfl_sync(0xffffffffu, w, 0)) {
-          ok = false;
-          break;
-        }
-        __syncwarp();
-        tc_fence_after();
-        const float* s = slots + q * (F8_SLOT / 4);
-        F2 sa = 0;
-        if (WGRAD) sa = f2(s[256 + quarter * 32 + lane]);
+        for (int g8 = 0; g8 < 4; ++g8) {
+          const int c = (2 * i + side) * 32 + 8 * g8 + 2 * (lane & 3);
+          float x[2][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c0 = (2 * i + side) * 32;
-          if (c0 < t.n) {
+          for (int k = 0; k < 4; ++k) {
+            x[0][k] = sum[2 * i + (k >> 1)][g8][k & 1][0];
+            x[1][k] = sum[2 * i + (k >> 1)][g8][k & 1][1];
+          }
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t v[16];
-              tmem_ld_32x32b_x16(tmem_base + acc * 256 + tlane + c0 + 16 * h, v);
-              tmem_wait_ld();
+          for (int h = 0; h < 2; ++h) {
+            if (c + h < t.cols) {
+              OUT* o = out + (int64_t)(c + h) * args.ld;
+              if (args.wide_out) {
+                if (j0 < args.NM) f8_put4(o, make_float4(x[h][0], x[h][1], x[h][2], x[h][3]));
+              } else {
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float4 f = *reinterpret_cast<const float4*>(s + c0 + 16 * h + 4 * j);
-                F2 p0 = f2(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]));
-                F2 p1 = f2(__uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
-                if (WGRAD) {
-                  p0 = mul2(p0, sa);
-                  p1 = mul2(p1, sa);
-                }
-                F2* d = &sum[i][8 * h + 2 * j];
-                d[0] = fma2(p0, f2(f.x, f.y), d[0]);
-                d[1] = fma2(p1, f2(f.z, f.w), d[1]);
+                for (int k = 0; k < 4; ++k)
+                  if (j0 + k * jstep < args.NM) f8_put(o + k * jstep, x[h][k]);
               }
             }
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive_cluster_relaxed(pempty0_cl + 8u * acc);
-          mbar_arrive(sempty_bar(q));
-        }
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1;
-        if (++q == SLOTS) {
-          q = 0;
-          q_phase ^= 1;
-        }
-      }
-      if (!ok) break;
-      const int j = t.m * 256 + 128 * (int)rank + 32 * quarter + lane;
-      if (j < args.NM) {
-        OUT* out = static_cast<OUT*>(args.out) + (WGRAD ? ((int64_t)t.e * args.NB + t.col0) : (int64_t)t.col0) * args.ld + j;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c0 = (2 * i + side) * 32;
-          OUT* o = out + (int64_t)c0 * args.ld;
-          const int left = t.cols - c0;
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            float a, b;
-            split(sum[i][k], a, b);
-            if (2 * k < left) f8_put(o, a);
-            o += args.ld;
-            if (2 * k + 1 < left) f8_put(o, b);
-            o += args.ld;
-          }
-        }
-      }
-      __syncwarp();
     }
   }
 
@@ -494,8 +604,29 @@ bool tmap_e4m3_rows(CUtensorMap* m, const void* base, int64_t K, int64_t rows, i
   return make_tmap(m, base, grouped ? 3 : 2, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8);
 }
 
+// A's rows in boxes of 128.  Mixed: of each 32 rows, box row 8 k + u is row 4 u + k, by a map with dimensions u (4 rows
+// apart) and k (one row apart).
+bool tmap_a(CUtensorMap* m, const void* base, int64_t K, int64_t rows, int64_t groups, int64_t ld, bool mixed) {
+  if (!mixed) return tmap_e4m3_rows(m, base, K, rows, groups, ld, 128, true);
+  const uint64_t dims[5] = {(uint64_t)K, 8, 4, (uint64_t)rows / 32, (uint64_t)groups};
+  const uint64_t strides[4] = {(uint64_t)(4 * ld), (uint64_t)ld, (uint64_t)(32 * ld), (uint64_t)(ld * rows)};
+  const uint32_t box[5] = {128, 8, 4, 4, 1};
+  return make_tmap(m, base, 5, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8);
+}
+
+// B's rows in boxes of 128, 64 and 32
+bool tmap_boxes(CUtensorMap (&m)[3], const void* base, int64_t K, int64_t rows, int64_t ld) {
+  for (int i = 0; i < 3; ++i)
+    if (!tmap_e4m3_rows(&m[i], base, K, rows, 1, ld, 128u >> i, false)) return false;
+  return true;
+}
+
+bool f8_wide(const void* out, int64_t ld, int64_t width, bool bf16) {
+  return ld % 4 == 0 && width % 4 == 0 && (reinterpret_cast<uintptr_t>(out) & (bf16 ? 7u : 15u)) == 0;
+}
+
 template <bool WGRAD, typename OUT>
-cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const Fp8GemmArgs& args, int64_t tiles, int n_sm,
+cudaError_t launch(const CUtensorMap& ta, const CUtensorMap (&tb)[3], const Fp8GemmArgs& args, int64_t tiles, int n_sm,
                    cudaStream_t st) {
   auto kern = fp8_gemm_kernel<WGRAD, OUT>;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)f8_smem(FP8_MAX_E));
@@ -512,7 +643,7 @@ cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const Fp8GemmAr
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(tiles, std::max(1, n_sm / 2))), 1, 1);
-  err = cudaLaunchKernelEx(&cfg, kern, ta, tb, args);
+  err = cudaLaunchKernelEx(&cfg, kern, ta, tb[0], tb[1], tb[2], args);
   return err != cudaSuccess ? err : cudaGetLastError();
 }
 
@@ -531,6 +662,8 @@ cudaError_t launch_fp8_product_pairs(const Fp8MatmulArgs& a, bool bf16_out, int 
   g.b_ld = a.x_scale_stride;
   g.out = a.out;
   g.ld = a.out_stride;
+  g.mixed = a.N % 32 == 0;
+  g.wide_out = g.mixed && f8_wide(a.out, a.out_stride, a.N, bf16_out);
   g.status = a.status;
   // narrower chunks while the tiles of wider ones leave pairs without work
   g.nmax = 256;
@@ -539,9 +672,9 @@ cudaError_t launch_fp8_product_pairs(const Fp8MatmulArgs& a, bool bf16_out, int 
     g.nmax /= 2;
   const int64_t tiles = ((a.R + g.nmax - 1) / g.nmax + a.E) * g.MT;  // at most
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
-  CUtensorMap ta, tb;
-  if (!tmap_e4m3_rows(&ta, a.w, a.K, a.N, a.E, a.w_stride, 128, true) ||
-      !tmap_e4m3_rows(&tb, a.x, a.K, a.R, 1, a.x_stride, 32, false))
+  CUtensorMap ta, tb[3];
+  if (!tmap_a(&ta, a.w, a.K, a.N, a.E, a.w_stride, g.mixed) ||
+      !tmap_boxes(tb, a.x, a.K, a.R, a.x_stride))
     return cudaErrorInvalidValue;
   return bf16_out ? launch<false, __nv_bfloat16>(ta, tb, g, tiles, n_sm, st) : launch<false, float>(ta, tb, g, tiles, n_sm, st);
 }
@@ -560,16 +693,18 @@ cudaError_t launch_fp8_weight_grad(const Fp8WeightGradArgs& a, bool bf16_out, in
   g.b_ld = a.N;
   g.out = a.out;
   g.ld = a.H;
+  g.mixed = a.H % 32 == 0;
+  g.wide_out = g.mixed && f8_wide(a.out, a.H, a.H, bf16_out);
   g.status = a.status;
   g.nmax = 256;
   const int64_t pairs = std::max(1, n_sm / 2);
   while (g.nmax > 32 && a.E * g.MT * ((a.N + g.nmax - 1) / g.nmax) < pairs) g.nmax /= 2;
   const int64_t tiles = a.E * (int64_t)g.MT * ((a.N + g.nmax - 1) / g.nmax);
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
-  CUtensorMap ta, tb;
+  CUtensorMap ta, tb[3];
   const int64_t P = 128 * g.blocks;
-  if (!tmap_e4m3_rows(&ta, a.x, P, a.H, 1, a.x_stride, 128, true) ||
-      !tmap_e4m3_rows(&tb, a.dy, P, a.N, 1, a.dy_stride, 32, false))
+  if (!tmap_a(&ta, a.x, P, a.H, 1, a.x_stride, g.mixed) ||
+      !tmap_boxes(tb, a.dy, P, a.N, a.dy_stride))
     return cudaErrorInvalidValue;
   return bf16_out ? launch<true, __nv_bfloat16>(ta, tb, g, tiles, n_sm, st) : launch<true, float>(ta, tb, g, tiles, n_sm, st);
 }

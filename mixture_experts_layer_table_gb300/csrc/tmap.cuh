@@ -34,9 +34,9 @@ inline bool make_tmap(CUtensorMap* m, const void* base, int rank, const uint64_t
                       CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
-  if (rank < 1 || rank > 4) return false;
-  cuuint64_t d[4], s[3];
-  cuuint32_t b[4], es[4] = {1, 1, 1, 1};
+  if (rank < 1 || rank > 5) return false;
+  cuuint64_t d[5], s[4];
+  cuuint32_t b[5], es[5] = {1, 1, 1, 1, 1};
   for (int i = 0; i < rank; ++i) {
     d[i] = dims[i];
     b[i] = box[i];
