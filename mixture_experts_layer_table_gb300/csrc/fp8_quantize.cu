@@ -8,9 +8,9 @@
 // The source is rows in hand, rows gathered by a schedule table (with their gates), the SwiGLU of [h | u] rows, or
 // its gradient.  One read of the source gives both layouts.
 //
-// A block of 256 threads takes a tile of 16 RPT rows x 128 columns: half-warp w holds rows RPT w .. RPT w + RPT - 1,
-// lane l of it columns 8 l .. 8 l + 7, so that a row's maximum is 4 shuffles, a store of a row 128 bytes and, with
-// RPT = 8, a lane's 8 rows of a column one 8-byte word of the transposed tile.
+// A half-warp holds whole rows of 128 columns, lane l columns 8 l .. 8 l + 7, so that a row's maximum is 4 shuffles and
+// a store of a row 128 bytes.  Rows alone: 256 threads, 1 or 4 rows a half-warp.  128 x 128 tiles: 512 threads, 4 rows a
+// half-warp, a lane's 4 rows of a column one word of the transposed tile.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -23,153 +23,199 @@
 namespace mok {
 namespace {
 
-constexpr int THREADS = 256;
+constexpr int THREADS = 256;       // rows alone
+constexpr int TILE_THREADS = 512;  // 128 x 128 tiles: 32 half-warps of 4 rows
 constexpr float LEAST = 7.703719777548943e-34f;  // 2^-110
 constexpr float BIG = 3.4028234663852886e38f;
 
-// What a block's elements are divided by, in the form the quotient is made of.
-struct Divisor {
-  float a, inv;  // amax / 512 (exact), its reciprocal
-};
-__device__ __forceinline__ Divisor divisor(float amax) {
-  Divisor d;
-  d.a = fmaxf(amax, LEAST) * (1.0f / 512);
-  d.inv = 1.0f / d.a;
-  return d;
+// Off by a unit in the last place at most; 0 for what would be below 2^-126.
+__device__ __forceinline__ float reciprocal(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
-__device__ __forceinline__ float block_scale(float amax) { return fmaxf(amax, LEAST) / 448.0f; }
 
-// (448 x / 512) / (amax / 512) for two elements: the product with the reciprocal, then one correction by the
-// remainder x' - y a, which the FMA forms exactly.  A quotient that is a multiple of few bits (a border between two
-// E4M3 values, common with bf16 inputs) comes out as itself, so that ties go to even as they should.  A NaN
-// or an infinity gives NaN (inf - inf in the remainder).
-__device__ __forceinline__ uint16_t quantize2(float x0, float x1, F2 a0a1, F2 i0i1) {
-  const F2 x = mul2(f2(x0, x1), f2(0.875f));
-  const F2 y = mul2(x, i0i1);
-  float y0, y1, a0, a1;
-  split(y, y0, y1);
-  split(a0a1, a0, a1);
-  const F2 r = fma2(f2(-y0, -y1), a0a1, x);
-  split(fma2(r, i0i1, y), y0, y1);
+// What a block's elements are divided by, in the form the quotient is made of: -amax / 512 (exact) and about 512 / amax.
+struct Divisor {
+  F2 minus_a, inv;
+};
+__device__ __forceinline__ Divisor divisor(float amax0, float amax1) {
+  const float a0 = fmaxf(amax0, LEAST) * (1.0f / 512), a1 = fmaxf(amax1, LEAST) * (1.0f / 512);
+  return {f2(-a0, -a1), f2(reciprocal(a0), reciprocal(a1))};
+}
+__device__ __forceinline__ Divisor divisor(float amax) {
+  const float a = fmaxf(amax, LEAST) * (1.0f / 512);
+  return {f2(-a), f2(reciprocal(a))};
+}
+// amax / 448, rounded once: the product with 1 / 448, corrected by its remainder.
+__device__ __forceinline__ float block_scale(float amax) {
+  const float m = fmaxf(amax, LEAST), q = m * (1.0f / 448);
+  return fmaf(fmaf(-q, 448.0f, m), 1.0f / 448, q);
+}
+
+// (448 x / 512) / (amax / 512) for two elements: the product with the reciprocal, then one correction by the remainder
+// x' - y a, which the FMA forms exactly: the quotient as a division rounds it.  One that is a multiple of few bits (a border
+// between two E4M3 values, common with bf16 inputs) comes out as itself, so that ties go to even as they should; without the
+// correction twice as many elements of computed values lay on the other side of a border.  A NaN gives NaN.
+__device__ __forceinline__ uint16_t quantize2(F2 x, F2 minus_a, F2 inv) {
+  x = mul2(x, f2(0.875f));
+  const F2 y = mul2(x, inv);
+  float y0, y1;
+  split(fma2(fma2(y, minus_a, x), inv, y), y0, y1);
   return e4m3x2_from_f32(y0, y1);
 }
-__device__ __forceinline__ uint2 quantize8(const float (&v)[8], F2 a, F2 inv) {
+
+// Eight columns of a row.
+struct Row8 {
+  F2 v[4];
+};
+__device__ __forceinline__ uint2 quantize8(const Row8& x, const Divisor& d) {
   uint2 o;
-  o.x = quantize2(v[0], v[1], a, inv) | (uint32_t)quantize2(v[2], v[3], a, inv) << 16;
-  o.y = quantize2(v[4], v[5], a, inv) | (uint32_t)quantize2(v[6], v[7], a, inv) << 16;
+  o.x = quantize2(x.v[0], d.minus_a, d.inv) | (uint32_t)quantize2(x.v[1], d.minus_a, d.inv) << 16;
+  o.y = quantize2(x.v[2], d.minus_a, d.inv) | (uint32_t)quantize2(x.v[3], d.minus_a, d.inv) << 16;
   return o;
 }
 
-// The magnitude that counts for a block: infinities and NaN stay out of it (their elements become NaN, the
-// others what they are without them).
-__device__ __forceinline__ float magnitude(float v) {
-  const float m = fabsf(v);
-  return m <= BIG ? m : 0.0f;
+// Infinities become NaN: the conversion keeps a NaN but takes an infinity for 448, and a NaN stays out of maxima.
+__device__ __forceinline__ void infinities_to_nan(Row8& x) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) x.v[j] = fma2(x.v[j], f2(0.0f), x.v[j]);
 }
-
+__device__ __forceinline__ float largest8(const Row8& x) {  // infinities count, NaN do not
+  float m = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float a, b;
+    split(x.v[j], a, b);
+    m = fmaxf(fmaxf(m, fabsf(a)), fabsf(b));
+  }
+  return m;
+}
 __device__ __forceinline__ float widen(float v) { return v; }
 __device__ __forceinline__ float widen(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ Row8 zero8() { return {{0, 0, 0, 0}}; }
 
 // Columns c .. c + 7 of a row of `width` elements; zeros behind its end.  VEC: the row is 16-byte aligned and
 // width a multiple of 8.
 template <bool VEC>
-__device__ __forceinline__ void load8(const float* row, int64_t c, int64_t width, float (&v)[8]) {
+__device__ __forceinline__ Row8 load8(const float* row, int64_t c, int64_t width) {
+  Row8 x = zero8();
   if (VEC) {
     if (c < width) {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(row + c)), b = __ldg(reinterpret_cast<const float4*>(row + c) + 1);
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-      return;
+      const ulonglong2 a = __ldg(reinterpret_cast<const ulonglong2*>(row + c)),
+                       b = __ldg(reinterpret_cast<const ulonglong2*>(row + c) + 1);
+      x = {{a.x, a.y, b.x, b.y}};
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = c + j < width ? __ldg(row + c + j) : 0.0f;
+    for (int j = 0; j < 4; ++j)
+      x.v[j] = f2(c + 2 * j < width ? __ldg(row + c + 2 * j) : 0.0f, c + 2 * j + 1 < width ? __ldg(row + c + 2 * j + 1) : 0.0f);
   }
+  return x;
 }
 template <bool VEC>
-__device__ __forceinline__ void load8(const __nv_bfloat16* row, int64_t c, int64_t width, float (&v)[8]) {
+__device__ __forceinline__ Row8 load8(const __nv_bfloat16* row, int64_t c, int64_t width) {
+  Row8 x;
   if (VEC) {
     uint4 w = make_uint4(0, 0, 0, 0);
     if (c < width) w = __ldg(reinterpret_cast<const uint4*>(row + c));
-    const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&w);
+    const uint32_t words[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = __bfloat1622float2(b[j]);
-      v[2 * j] = f.x;
-      v[2 * j + 1] = f.y;
-    }
+    for (int j = 0; j < 4; ++j) x.v[j] = f2(__uint_as_float(words[j] << 16), __uint_as_float(words[j] & 0xffff0000u));
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = c + j < width ? __bfloat162float(row[c + j]) : 0.0f;
+    for (int j = 0; j < 4; ++j)
+      x.v[j] = f2(c + 2 * j < width ? __bfloat162float(row[c + 2 * j]) : 0.0f,
+                  c + 2 * j + 1 < width ? __bfloat162float(row[c + 2 * j + 1]) : 0.0f);
   }
+  return x;
 }
 
-// silu(h) = h sigmoid(h).  The accurate exponential and quotient: with the approximations (2^-21) a value on the other side of a
-// border between two E4M3 values was ten times as frequent, and the kernel is bound by its memory all the same.
-__device__ __forceinline__ float sigmoid(float h) { return 1.0f / (1.0f + expf(-h)); }
+// 1 / (1 + e^-h), two at a time: the accurate exponential, and a reciprocal corrected once.  With the hardware's 2^x and
+// 1 / x alone (2^-21) a value on the other side of a border between two E4M3 values was ten times as frequent.  From h = -87
+// down the value stays at 2^-125, far below what counts beside LEAST, so that nothing overflows on the way.
+__device__ __forceinline__ F2 sigmoid2(F2 h) {
+  float a, b;
+  split(h, a, b);
+  const F2 d = add2(f2(expf(-fmaxf(a, -87.0f)), expf(-fmaxf(b, -87.0f))), f2(1.0f));
+  split(d, a, b);
+  const F2 r = f2(reciprocal(a), reciprocal(b));
+  return fma2(fma2(mul2(d, f2(-1.0f)), r, f2(1.0f)), r, r);
+}
 
-// Row r (of the sorted order) of the source, columns c .. c + 7.
-template <int SRC, typename T, bool VEC>
-__device__ __forceinline__ void source8(const Fp8QuantizeArgs& a, int64_t r, int64_t c, float (&v)[8]) {
+// Where a row of the source lies.
+template <typename T>
+struct Source {
+  const T* x;     // null: a row of zeros
+  const T* grad;
+  float gate;
+};
+template <int SRC, typename T>
+__device__ __forceinline__ Source<T> source_row(const Fp8QuantizeArgs& a, int64_t r) {
   const T* x = static_cast<const T*>(a.x);
+  if (SRC != FP8_PLAIN)
+    return {x + r * a.x_stride, SRC == FP8_SWIGLU_GRAD ? static_cast<const T*>(a.grad) + r * a.grad_stride : nullptr, 1.0f};
+  if (a.src_of == nullptr) return {x + r * a.x_stride, nullptr, 1.0f};
+  const int32_t s = __ldg(a.src_of + r);
+  if (s < 0 || s >= a.T * a.k) {
+    if (s != -1) report_status(a.status, MOK_DEV_INVALID_ROUTING, SITE_FP8_SOURCE);
+    return {nullptr, nullptr, 1.0f};
+  }
+  return {x + (int64_t)(s / a.k) * a.x_stride, nullptr, a.gates != nullptr ? __ldg(a.gates + s) : 1.0f};
+}
+
+// Columns c .. c + 7 of the quantised row that comes of it.
+template <int SRC, typename T, bool VEC>
+__device__ __forceinline__ Row8 source8(const Fp8QuantizeArgs& a, const Source<T>& s, int64_t c) {
+  Row8 o = zero8();
   if (SRC == FP8_PLAIN) {
-    if (a.src_of == nullptr) {
-      load8<VEC>(x + r * a.x_stride, c, a.C, v);
-      return;
-    }
-    const int32_t s = __ldg(a.src_of + r);
-    const bool ok = s >= 0 && s < a.T * a.k;
-    if (!ok) {
-      if (s != -1) report_status(a.status, MOK_DEV_INVALID_ROUTING, SITE_FP8_SOURCE);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-      return;
-    }
-    load8<VEC>(x + (int64_t)(s / a.k) * a.x_stride, c, a.C, v);
+    if (s.x == nullptr) return o;
+    o = load8<VEC>(s.x, c, a.C);
     if (a.gates != nullptr) {
-      const float g = __ldg(a.gates + s);
+      const F2 g = f2(s.gate);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= g;
+      for (int j = 0; j < 4; ++j) o.v[j] = mul2(o.v[j], g);
     }
   } else if (SRC == FP8_SWIGLU) {
-    const T* row = x + r * a.x_stride;
-    float u[8];
-    load8<VEC>(row, c, a.C, v);
-    load8<VEC>(row + a.C, c, a.C, u);
+    const Row8 h = load8<VEC>(s.x, c, a.C), u = load8<VEC>(s.x + a.C, c, a.C);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = v[j] * sigmoid(v[j]) * u[j];
+    for (int j = 0; j < 4; ++j) o.v[j] = mul2(mul2(h.v[j], sigmoid2(h.v[j])), u.v[j]);
   } else {
     const int64_t I = a.C / 2;
-    const T* row = x + r * a.x_stride;
-    const T* grad = static_cast<const T*>(a.grad) + r * a.grad_stride;
     // VEC: I is a multiple of 8, so that a lane's columns lie in one half
     if (VEC) {
-      const bool up = c >= I;
-      const int64_t i = up ? c - I : c;
-      float h[8], u[8], d[8];
-      load8<true>(row, i, I, h);
-      load8<true>(grad, i, I, d);
-      if (!up) load8<true>(row + I, i, I, u);
+      if (c >= I) {
+        const Row8 h = load8<true>(s.x, c - I, I), d = load8<true>(s.grad, c - I, I);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float sg = sigmoid(h[j]);
-        v[j] = up ? d[j] * h[j] * sg : d[j] * u[j] * sg * (1.0f + h[j] * (1.0f - sg));
+        for (int j = 0; j < 4; ++j) o.v[j] = mul2(mul2(d.v[j], h.v[j]), sigmoid2(h.v[j]));
+      } else {
+        const Row8 h = load8<true>(s.x, c, I), d = load8<true>(s.grad, c, I), u = load8<true>(s.x + I, c, I);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const F2 sg = sigmoid2(h.v[j]);
+          o.v[j] = mul2(mul2(mul2(d.v[j], u.v[j]), sg), add2(mul2(h.v[j], fma2(sg, f2(-1.0f), f2(1.0f))), f2(1.0f)));
+        }
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const bool up = c + j >= I;
-        const int64_t i = up ? c + j - I : c + j;
-        v[j] = 0.0f;
-        if (c + j < a.C) {
-          const float h = widen(row[i]), d = widen(grad[i]), sg = sigmoid(h);
-          v[j] = up ? d * h * sg : d * widen(row[I + i]) * sg * (1.0f + h * (1.0f - sg));
+      for (int j = 0; j < 4; ++j) {
+        float v[2];
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          const int64_t col = c + 2 * j + z, i = col >= I ? col - I : col;
+          v[z] = 0.0f;
+          if (col < a.C) {
+            const float hh = widen(s.x[i]), dd = widen(s.grad[i]);
+            float sg, other;
+            split(sigmoid2(f2(hh)), sg, other);
+            v[z] = col >= I ? dd * hh * sg : dd * widen(s.x[I + i]) * sg * fmaf(hh, 1.0f - sg, 1.0f);
+          }
         }
+        o.v[j] = f2(v[0], v[1]);
       }
     }
   }
+  return o;
 }
 
 // 8 bytes at p, of which `n` lie in front of the end.
@@ -183,30 +229,53 @@ __device__ __forceinline__ void store8(uint8_t* p, uint2 v, int64_t n) {
   }
 }
 
-// The transposed tile in shared memory, 128 columns of 128 bytes: the 8-byte word of half-warp k lies at word
-// k ^ (c / 8 mod 16) of column c, so that neither the writes (16 lanes with columns 8 apart) nor the reads (16 words of a
-// column) meet in a bank.
-__device__ __forceinline__ int tile_word(int c, int k) { return c * 16 + (k ^ ((c >> 3) & 15)); }
+// The transposed tile in shared memory, 128 columns of 128 bytes: the 4-byte word of half-warp k lies at word k ^ 2 (c / 8 mod
+// 16) of column c, so that the writes of a warp (16 lanes with columns 8 apart, two words) do not meet in a bank; the
+// words of two neighbouring half-warps stay together, 8 bytes for the way out.
+__device__ __forceinline__ int tile_word(int c, int k) { return c * 32 + (k ^ (2 * ((c >> 3) & 15))); }
 
-// bytes[i] of row i (two words) -> word j: byte i is byte j of row i.
-__device__ __forceinline__ uint2 column_word(const uint2 (&rows)[8], int j) {
-  const bool high = j >= 4;
-  const int s = j & 3;
-  const uint32_t sel = s | (s + 4) << 4;
-  uint32_t h[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    h[i] = __byte_perm(high ? rows[2 * i].y : rows[2 * i].x, high ? rows[2 * i + 1].y : rows[2 * i + 1].x, sel);
-  return make_uint2(__byte_perm(h[0], h[1], 0x5410), __byte_perm(h[2], h[3], 0x5410));
+// Byte j of each of four rows.
+__device__ __forceinline__ uint32_t column_word(const uint2 (&rows)[4], int j) {
+  const uint32_t sel = (j & 3) | ((j & 3) + 4) << 4;
+  const uint32_t lo = j < 4 ? __byte_perm(rows[0].x, rows[1].x, sel) : __byte_perm(rows[0].y, rows[1].y, sel);
+  const uint32_t hi = j < 4 ? __byte_perm(rows[2].x, rows[3].x, sel) : __byte_perm(rows[2].y, rows[3].y, sel);
+  return __byte_perm(lo, hi, 0x5410);
 }
 
 // Writes the tile's 128 columns to qt rows (128 bytes each, `n` of them in front of the end), of which `cols` exist.
-__device__ __forceinline__ void store_tile(const uint2* tile, uint8_t* qt, int64_t stride, int64_t cols, int64_t n) {
-  const int k = threadIdx.x & 15;
+__device__ __forceinline__ void store_tile(const uint32_t* tile, uint8_t* qt, int64_t stride, int64_t cols, int64_t n) {
+  const int k = threadIdx.x & 15, c0 = threadIdx.x >> 4;
+  uint8_t* to = qt + c0 * stride + 8 * k;
+  if (cols >= 128 && n >= 128) {
 #pragma unroll
-  for (int s = 0; s < 8; ++s) {
-    const int c = s * 16 + (threadIdx.x >> 4);
-    if (c < cols) store8(qt + c * stride + 8 * k, tile[tile_word(c, k)], n - 8 * k);
+    for (int s = 0; s < 4; ++s)
+      *reinterpret_cast<uint2*>(to + s * (32 * stride)) = *reinterpret_cast<const uint2*>(tile + tile_word(c0 + 32 * s, 2 * k));
+  } else {
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+      if (c0 + 32 * s < cols)
+        store8(to + s * (32 * stride), *reinterpret_cast<const uint2*>(tile + tile_word(c0 + 32 * s, 2 * k)), n - 8 * k);
+  }
+}
+
+// The largest finite magnitude of each of a half-warp's rows (of the warp's lanes, infinities have become NaN).
+template <int RPT>
+__device__ __forceinline__ void row_maxima(const Row8 (&v)[RPT], float (&m)[RPT]) {
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    m[i] = largest8(v[i]);
+#pragma unroll
+    for (int s = 8; s > 0; s >>= 1) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], s));
+  }
+}
+template <int RPT>
+__device__ __forceinline__ void finite_or_nan(Row8 (&v)[RPT]) {
+  float all = 0.0f;
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) all = fmaxf(all, largest8(v[i]));
+  if (__any_sync(0xffffffffu, all > BIG)) {
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) infinities_to_nan(v[i]);
   }
 }
 
@@ -219,27 +288,21 @@ __global__ void __launch_bounds__(THREADS) fp8_rows_kernel(const Fp8QuantizeArgs
   const int64_t r0 = (int64_t)(blockIdx.x / col_blocks) * (16 * RPT);
   const int w = threadIdx.x >> 4, l = threadIdx.x & 15;
   const int64_t c = (int64_t)b * FP8_BLOCK + 8 * l;
-  float v[RPT][8];
+  Row8 v[RPT];
 #pragma unroll
   for (int i = 0; i < RPT; ++i) {
     const int64_t r = r0 + w * RPT + i;
-    if (r < a.R) source8<SRC, T, VEC>(a, r, c, v[i]);
-    else
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+    v[i] = r < a.R ? source8<SRC, T, VEC>(a, source_row<SRC, T>(a, r), c) : zero8();
   }
+  float m[RPT];
+  finite_or_nan(v);
+  row_maxima(v, m);
 #pragma unroll
   for (int i = 0; i < RPT; ++i) {
     const int64_t r = r0 + w * RPT + i;
-    float m = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = fmaxf(m, magnitude(v[i][j]));
-#pragma unroll
-    for (int s = 8; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
-    const Divisor d = divisor(m);
-    const uint2 bytes = quantize8(v[i], f2(d.a), f2(d.inv));
+    const uint2 bytes = quantize8(v[i], divisor(m[i]));
     if (r < a.R && c < a.C) store8(a.q + r * a.q_stride + c, bytes, a.C - c);
-    if (l == 0) s_scale[w * RPT + i] = block_scale(m);
+    if (l == 0) s_scale[w * RPT + i] = block_scale(m[i]);
   }
   __syncthreads();
   for (int i = threadIdx.x; i < 16 * RPT; i += THREADS)
@@ -250,19 +313,18 @@ __global__ void __launch_bounds__(THREADS) fp8_rows_kernel(const Fp8QuantizeArgs
 // A tile is 128 rows of one expert (of the padded order) x 128 columns.  A block takes `group` column blocks of
 // one row tile, after it has found the tile's expert: the offsets are read and scanned by the block itself.
 template <int SRC, typename T, bool VEC>
-__global__ void __launch_bounds__(THREADS, 2) fp8_columns_kernel(const Fp8QuantizeArgs a, int col_blocks, int group,
-                                                                 int groups) {
-  __shared__ uint2 tile[128 * 16];
-  __shared__ float s_max[8][128];
-  __shared__ float2 s_div[128];
-  __shared__ float s_scale[128];
-  __shared__ int s_warp[8], s_where[2];
+__global__ void __launch_bounds__(TILE_THREADS, 2) fp8_columns_kernel(const Fp8QuantizeArgs a, int col_blocks, int group,
+                                                                      int groups) {
+  __shared__ __align__(16) uint32_t tile[128 * 32];
+  __shared__ __align__(16) int s_max[2][128];  // bits of the columns' maxima, of this round and the next
+  __shared__ float s_scale[2][128];
+  __shared__ int s_warp[16], s_where[2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int p = blockIdx.x / groups;  // row tile
-  // the expert whose 128-row blocks hold block p: a scan of the experts' blocks, 256 experts at a time
+  // the expert whose 128-row blocks hold block p: a scan of the experts' blocks, 512 experts at a time
   if (threadIdx.x == 0) s_where[1] = 0;
   int before = 0;  // blocks of the experts before this round's
-  for (int e0 = 0; e0 < a.E; e0 += THREADS) {
+  for (int e0 = 0; e0 < a.E; e0 += TILE_THREADS) {
     const int e = e0 + threadIdx.x;
     int lo = 0, hi = 0;
     if (e < a.E) {
@@ -280,7 +342,7 @@ __global__ void __launch_bounds__(THREADS, 2) fp8_columns_kernel(const Fp8Quanti
     __syncthreads();
     int total = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 16; ++i) {
       if (i < warp) sum += s_warp[i];
       total += s_warp[i];
     }
@@ -296,114 +358,167 @@ __global__ void __launch_bounds__(THREADS, 2) fp8_columns_kernel(const Fp8Quanti
   const int rows = s_where[1] == 0 ? 0 : (int)min((int64_t)s_where[1], a.R - row0);  // whatever the table says
   if (rows <= 0) return;  // behind the last expert's blocks
   const int w = threadIdx.x >> 4, l = threadIdx.x & 15;
+  uint8_t* to = a.q + (row0 + w * 4) * a.q_stride;
   const int b_end = min(col_blocks, (int)(blockIdx.x % groups + 1) * group);
-  for (int b = (blockIdx.x % groups) * group; b < b_end; ++b) {
+  if (threadIdx.x < 128) s_max[0][threadIdx.x] = s_max[1][threadIdx.x] = 0;
+  __syncthreads();
+  for (int b = (blockIdx.x % groups) * group, turn = 0; b < b_end; ++b, turn ^= 1) {
     const int64_t c = (int64_t)b * FP8_BLOCK + 8 * l;
-    float v[8][8];
+    const bool full = rows == 128 && (b + 1) * (int64_t)FP8_BLOCK <= a.C;  // uniform, and most tiles
+    Row8 v[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (w * 8 + i < rows) source8<SRC, T, VEC>(a, row0 + w * 8 + i, c, v[i]);
-      else
+    for (int i = 0; i < 4; ++i) v[i] = full || w * 4 + i < rows ? source8<SRC, T, VEC>(a, source_row<SRC, T>(a, row0 + w * 4 + i), c) : zero8();
+    finite_or_nan(v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
-    }
-    float top[8];
+    for (int j = 0; j < 4; ++j) {
+      float t0 = 0.0f, t1 = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) top[j] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float m = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float n = magnitude(v[i][j]);
-        top[j] = fmaxf(top[j], n);
-        m = fmaxf(m, n);
+      for (int i = 0; i < 4; ++i) {
+        float x, y;
+        split(v[i].v[j], x, y);
+        t0 = fmaxf(t0, fabsf(x));
+        t1 = fmaxf(t1, fabsf(y));
       }
-      if (a.q != nullptr) {
-#pragma unroll
-        for (int s = 8; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
-        const Divisor d = divisor(m);
-        const uint2 bytes = quantize8(v[i], f2(d.a), f2(d.inv));
-        if (w * 8 + i < rows && c < a.C) store8(a.q + (row0 + w * 8 + i) * a.q_stride + c, bytes, a.C - c);
-        if (l == 0) s_scale[w * 8 + i] = block_scale(m);
-      }
+      t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 16));
+      t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 16));
+      // both half-warps hold the maxima: each brings one (as integers, which order like the values they are bits of)
+      atomicMax(&s_max[turn][8 * l + 2 * j + (lane >> 4)], __float_as_int(lane < 16 ? t0 : t1));
     }
+    if (a.q != nullptr) {
+      float m[4];
+      row_maxima(v, m);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], 16));
-    if (lane < 16) {
-      float4* m = reinterpret_cast<float4*>(&s_max[warp][8 * l]);
-      m[0] = make_float4(top[0], top[1], top[2], top[3]);
-      m[1] = make_float4(top[4], top[5], top[6], top[7]);
+      for (int i = 0; i < 4; ++i) {
+        const uint2 bytes = quantize8(v[i], divisor(m[i]));
+        if (full) *reinterpret_cast<uint2*>(to + i * a.q_stride + c) = bytes;
+        else if (w * 4 + i < rows && c < a.C) store8(to + i * a.q_stride + c, bytes, a.C - c);
+        if (l == 0) s_scale[turn][w * 4 + i] = block_scale(m[i]);
+      }
     }
     __syncthreads();
     if (threadIdx.x < 128) {
-      float m = s_max[0][threadIdx.x];
-#pragma unroll
-      for (int i = 1; i < 8; ++i) m = fmaxf(m, s_max[i][threadIdx.x]);
-      const Divisor d = divisor(m);
-      s_div[threadIdx.x] = make_float2(d.a, d.inv);
       const int64_t col = (int64_t)b * FP8_BLOCK + threadIdx.x;
-      if (col < a.C) a.qt_scale[p * a.C + col] = block_scale(m);
+      if (col < a.C) a.qt_scale[p * a.C + col] = block_scale(__int_as_float(s_max[turn][threadIdx.x]));
     } else if (a.q != nullptr && (int)threadIdx.x - 128 < rows) {
-      a.scale[b * a.scale_stride + row0 + threadIdx.x - 128] = s_scale[threadIdx.x - 128];
+      a.scale[b * a.scale_stride + row0 + threadIdx.x - 128] = s_scale[turn][threadIdx.x - 128];
     }
-    __syncthreads();
-    uint2 bytes[8];
+    uint2 bytes[4];
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {  // two columns at a time: their divisors in a pair
-      const float2 d0 = s_div[8 * l + j], d1 = s_div[8 * l + j + 1];
-      const F2 da = f2(d0.x, d1.x), di = f2(d0.y, d1.y);
+    for (int h = 0; h < 2; ++h) {
+      const int4 t = *reinterpret_cast<const int4*>(&s_max[turn][8 * l + 4 * h]);
+      const float m[4] = {__int_as_float(t.x), __int_as_float(t.y), __int_as_float(t.z), __int_as_float(t.w)};
+      uint32_t q[4][2];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t h = quantize2(v[i][j], v[i][j + 1], da, di);
-        uint32_t& word = j < 4 ? bytes[i].x : bytes[i].y;
-        word = (j & 3) == 0 ? h : word | h << 16;
+      for (int j = 0; j < 2; ++j) {  // two columns at a time: their divisors in a pair
+        const Divisor d = divisor(m[2 * j], m[2 * j + 1]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i][j] = quantize2(v[i].v[2 * h + j], d.minus_a, d.inv);
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) (h == 0 ? bytes[i].x : bytes[i].y) = q[i][0] | q[i][1] << 16;
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) tile[tile_word(8 * l + j, w)] = column_word(bytes, j);
+    // the other turn's maxima have been read: every thread is past the barrier above
+    if (threadIdx.x >= 256 && threadIdx.x < 384) s_max[turn ^ 1][threadIdx.x - 256] = 0;
     __syncthreads();
     store_tile(tile, a.qt + (int64_t)b * FP8_BLOCK * a.qt_stride + (int64_t)p * 128, a.qt_stride,
                a.C - (int64_t)b * FP8_BLOCK, 128);
-    __syncthreads();  // the tile and the maxima are free again
+    // the next round writes the tile after its first barrier, which every thread reaches after this
   }
 }
 
 // ------------------------------------------------------------------ weights
+// A row's eight columns as they are kept until the block's scale is known: bf16 rows in their own four words (half the
+// registers, so that three blocks share an SM, and maxima of two elements at once).
+struct RawRow8 {
+  uint32_t w[4];
+};
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(THREADS, 2) fp8_weights_kernel(const Fp8WeightsArgs a, int n_blocks, int k_blocks) {
-  __shared__ uint2 tile[128 * 16];
-  __shared__ float s_max[8];
-  const int64_t e = blockIdx.x / ((int64_t)n_blocks * k_blocks);
-  const int nb = (int)(blockIdx.x / k_blocks % n_blocks), kb = (int)(blockIdx.x % k_blocks);
+struct Kept {
+  using type = Row8;
+};
+template <>
+struct Kept<__nv_bfloat16, true> {
+  using type = RawRow8;
+};
+template <bool VEC, typename T>
+__device__ __forceinline__ void keep(Row8& x, const T* row, int64_t c, int64_t width) { x = load8<VEC>(row, c, width); }
+template <bool VEC>
+__device__ __forceinline__ void keep(RawRow8& x, const __nv_bfloat16* row, int64_t c, int64_t width) {
+  uint4 w = make_uint4(0, 0, 0, 0);
+  if (c < width) w = __ldg(reinterpret_cast<const uint4*>(row + c));
+  x = {{w.x, w.y, w.z, w.w}};
+}
+__device__ __forceinline__ Row8 kept(const Row8& x) { return x; }
+__device__ __forceinline__ Row8 kept(const RawRow8& x) {
+  Row8 o;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) o.v[j] = f2(__uint_as_float(x.w[j] << 16), __uint_as_float(x.w[j] & 0xffff0000u));
+  return o;
+}
+__device__ __forceinline__ float kept_largest(const Row8 (&v)[4]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = fmaxf(m, largest8(v[i]));
+  return m;
+}
+__device__ __forceinline__ float kept_largest(const RawRow8 (&v)[4]) {
+  // magnitudes as unsigned 16-bit numbers order like the values, NaN above infinity: they are looked at again then
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = __vmaxu2(m, v[i].w[j] & 0x7fff7fffu);
+  return __uint_as_float(max(m & 0xffffu, m >> 16) << 16);
+}
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(TILE_THREADS, VEC && sizeof(T) == 2 ? 3 : 2) fp8_weights_kernel(const Fp8WeightsArgs a, int n_blocks, int k_blocks) {
+  __shared__ __align__(16) uint32_t tile[128 * 32];
+  __shared__ float s_max[16];
+  const int row_block = (int)blockIdx.x / k_blocks, kb = (int)blockIdx.x - row_block * k_blocks;
+  const int64_t e = row_block / n_blocks;
+  const int nb = row_block % n_blocks;
   const int w = threadIdx.x >> 4, l = threadIdx.x & 15;
   const int64_t n0 = (int64_t)nb * FP8_BLOCK, k0 = (int64_t)kb * FP8_BLOCK, c = k0 + 8 * l;
-  const T* x = static_cast<const T*>(a.w) + e * a.N * a.K;
-  float v[8][8], m = 0.0f;
+  const bool full = n0 + FP8_BLOCK <= a.N && k0 + FP8_BLOCK <= a.K;  // uniform, and most tiles
+  const T* from = static_cast<const T*>(a.w) + (e * a.N + n0 + w * 4) * a.K;
+  uint8_t* to = a.q + (e * a.N + n0 + w * 4) * a.q_stride;
+  typename Kept<T, VEC>::type v[4] = {};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t n = n0 + w * 8 + i;
-    if (n < a.N) load8<VEC>(x + n * a.K, c, a.K, v[i]);
-    else
+  for (int i = 0; i < 4; ++i)
+    if (full || n0 + w * 4 + i < a.N) keep<VEC>(v[i], from + i * a.K, c, full ? c + 8 : a.K);
+  float m = kept_largest(v);
+  bool odd = false;  // not all elements of the warp are finite
+  if (__any_sync(0xffffffffu, !(m <= BIG))) {
+    odd = true;
+    m = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = fmaxf(m, magnitude(v[i][j]));
+    for (int i = 0; i < 4; ++i) {
+      Row8 x = kept(v[i]);
+      infinities_to_nan(x);
+      m = fmaxf(m, largest8(x));
+    }
   }
 #pragma unroll
   for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
   if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, s_max[i]);
+  for (int i = 0; i < 16; ++i) m = fmaxf(m, s_max[i]);
   const Divisor d = divisor(m);
-  const F2 da = f2(d.a), di = f2(d.inv);
-  uint2 bytes[8];
+  uint2 bytes[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t n = n0 + w * 8 + i;
-    bytes[i] = quantize8(v[i], da, di);
-    if (a.q != nullptr && n < a.N && c < a.K) store8(a.q + (e * a.N + n) * a.q_stride + c, bytes[i], a.K - c);
+  for (int i = 0; i < 4; ++i) {
+    const int64_t n = n0 + w * 4 + i;
+    Row8 x = kept(v[i]);
+    if (odd) infinities_to_nan(x);
+    bytes[i] = quantize8(x, d);
+    if (a.q != nullptr) {
+      if (full) *reinterpret_cast<uint2*>(to + i * a.q_stride + c) = bytes[i];
+      else if (n < a.N && c < a.K) store8(to + i * a.q_stride + c, bytes[i], a.K - c);
+    }
   }
   if (threadIdx.x == 0) {
     if (a.q != nullptr) a.scale[(e * n_blocks + nb) * k_blocks + kb] = block_scale(m);
@@ -435,7 +550,7 @@ cudaError_t quantize(const Fp8QuantizeArgs& a, int n_sm, cudaStream_t st) {
   const int64_t groups = (col_blocks + group - 1) / group;
   if (tiles * groups > INT32_MAX) return cudaErrorInvalidValue;
   fp8_columns_kernel<SRC, T, VEC>
-      <<<(unsigned)(tiles * groups), THREADS, 0, st>>>(a, (int)col_blocks, group, (int)groups);
+      <<<(unsigned)(tiles * groups), TILE_THREADS, 0, st>>>(a, (int)col_blocks, group, (int)groups);
   return cudaGetLastError();
 }
 
@@ -456,8 +571,8 @@ cudaError_t weights(const Fp8WeightsArgs& a, cudaStream_t st) {
   const int64_t n = (a.N + 127) / 128, k = (a.K + 127) / 128, blocks = a.E * n * k;
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
   const bool vec = aligned(a.w, a.K * (int64_t)sizeof(T)) && a.K % 8 == 0;
-  if (vec) fp8_weights_kernel<T, true><<<(unsigned)blocks, THREADS, 0, st>>>(a, (int)n, (int)k);
-  else fp8_weights_kernel<T, false><<<(unsigned)blocks, THREADS, 0, st>>>(a, (int)n, (int)k);
+  if (vec) fp8_weights_kernel<T, true><<<(unsigned)blocks, TILE_THREADS, 0, st>>>(a, (int)n, (int)k);
+  else fp8_weights_kernel<T, false><<<(unsigned)blocks, TILE_THREADS, 0, st>>>(a, (int)n, (int)k);
   return cudaGetLastError();
 }
 
