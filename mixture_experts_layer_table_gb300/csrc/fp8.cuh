@@ -68,8 +68,6 @@ struct Fp8WeightGradArgs {
 
 cudaError_t launch_fp8_quantize(const Fp8QuantizeArgs& a, int source, bool bf16, int n_sm, cudaStream_t st);
 cudaError_t launch_fp8_weights(const Fp8WeightsArgs& a, bool bf16, cudaStream_t st);
-// The product on CTA pairs (many rows a group); launch_fp8_matmul chooses.
-cudaError_t launch_fp8_product_pairs(const Fp8MatmulArgs& a, bool bf16_out, int n_sm, cudaStream_t st);
 cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, bool bf16_out, int n_sm, cudaStream_t st);
 cudaError_t launch_fp8_weight_grad(const Fp8WeightGradArgs& a, bool bf16_out, int n_sm, cudaStream_t st);
 

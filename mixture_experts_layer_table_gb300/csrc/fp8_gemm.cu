@@ -48,6 +48,7 @@ struct Fp8GemmArgs {
   void* out;
   int64_t ld;             // elements between out's rows
   int mixed;              // TMEM lane 8 k + u of a quarter holds A's row 4 u + k, else the rows are in order
+  int splits;             // pairs of a cluster, each with its share of a tile's blocks
   int wide_out;           // mixed, and out's rows take four neighbours at once
   int* status;
 };
@@ -83,8 +84,8 @@ struct Fp8Tile {
 
 // Tile g: the groups' first tiles by binary search (product), or by division (weight grad).
 // s_at / s_cnt: product: first row and rows of each group, s_first: chunks before it; weight grad: first block, blocks.
-template <bool WGRAD>
-__device__ __forceinline__ Fp8Tile f8_tile(int g, const Fp8GemmArgs& a, const int* s_at, const int* s_cnt,
+template <bool WGRAD, bool SPLIT>
+__device__ __forceinline__ Fp8Tile f8_tile(int g, int split, const Fp8GemmArgs& a, const int* s_at, const int* s_cnt,
                                            const int* s_first) {
   Fp8Tile t;
   int nc, c, rows;
@@ -114,6 +115,11 @@ __device__ __forceinline__ Fp8Tile f8_tile(int g, const Fp8GemmArgs& a, const in
     t.kb0 = 0;
     t.nkb = a.nkb;
     t.col0 = s_at[lo];
+  }
+  if (SPLIT) {
+    const int lo = t.nkb * split / a.splits;
+    t.kb0 += lo;
+    t.nkb = t.nkb * (split + 1) / a.splits - lo;
   }
   const int each = ((rows + nc - 1) / nc + 15) & ~15;  // equal chunks
   t.col0 += c * each;
@@ -145,6 +151,9 @@ __device__ __forceinline__ bool f8_wait(uint32_t bar, uint32_t parity, volatile 
   return true;
 }
 
+// 32-column pieces of the epilogue warp that has most of them (two warps take turns).
+__device__ __forceinline__ int np_of(int n) { return (((n + 31) >> 5) + 1) >> 1; }
+
 // Blocks of K whose sums share an accumulator of 256 columns: narrow tiles hand over several at once, since handing
 // over costs the epilogue as much as 128 columns do.
 __device__ __forceinline__ int f8_blocks_at_once(int n) { return n <= 64 ? 4 : n <= 128 ? 2 : 1; }
@@ -163,7 +172,7 @@ __device__ __forceinline__ void f8_put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void f8_put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
 // tmA: A's rows, [groups][NM][K] bytes, boxes of 128 bytes x 128 rows; tmB: B's rows, boxes of 128 bytes x 32 rows.
-template <bool WGRAD, typename OUT>
+template <bool WGRAD, bool SPLIT, typename OUT>
 __global__ void __launch_bounds__(F8_THREADS, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmB64, const __grid_constant__ CUtensorMap tmB32,
@@ -184,9 +193,11 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
 
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);  // uniform, and known to be
   const int lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
-  const int pair = (int)blockIdx.x >> 1;
-  const int npairs = (int)gridDim.x >> 1;
+  const uint32_t cta = cluster_ctarank(), rank = cta & 1;  // rank 0 issues its pair's MMAs
+  const int split = SPLIT ? (int)(cta >> 1) : 0;
+  const int pair = SPLIT ? (int)blockIdx.x / (2 * args.splits) : (int)blockIdx.x >> 1;  // with splits: the cluster
+  const int npairs = SPLIT ? (int)gridDim.x / (2 * args.splits) : (int)gridDim.x >> 1;
+  const uint16_t both = (uint16_t)(3u << (cta & ~1u));
   const uint32_t bars0 = smem_u32(bars);
   auto full_bar = [&](int s) { return bars0 + 8u * s; };
   auto empty_bar = [&](int s) { return bars0 + 8u * (STAGES + s); };
@@ -270,6 +281,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
   const uint32_t tmem_base = *tmem_slot;
   const int total = WGRAD ? args.E * args.MT * ((args.NB + args.nmax - 1) / args.nmax) : s_first[args.E] * args.MT;
 
+  bool met = false;  // has been at the two meetings of a split tile's pairs
   if (warp < 4) {
     reg_dec<F8Regs<WGRAD>::FEW>();
     if (warp == 0) {
@@ -282,13 +294,13 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
       const uint64_t pol_a = l2_policy_evict_normal();
       const uint64_t pol_once = l2_policy_evict_first();
       const uint64_t pol_b = l2_policy_evict_last();  // read by every tile along A's rows
-      const uint32_t full0_cl = mapa_shared(full_bar(0), 0);
+      const uint32_t full0_cl = mapa_shared(full_bar(0), cta & ~1u);
       const uint32_t smem0 = smem_u32(smem);
       int stage = 0, issued = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (int g = pair; g < total && ok; g += npairs) {
-        const Fp8Tile t = f8_tile<WGRAD>(g, args, s_at, s_cnt, s_first);
+        const Fp8Tile t = f8_tile<WGRAD, SPLIT>(g, split, args, s_at, s_cnt, s_first);
         const int half = t.n >> 1;
         // the CTA's rows of B in the fewest boxes of 128, 64 and 32 rows
         const int b128 = half > 96, b64 = !b128 && half > 32, b32 = !b128 && (half <= 32 || half > 64);
@@ -351,7 +363,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         uint32_t phase = 0, acc_phase = 0;
         bool ok = true, any = false;
         for (int g = pair; g < total && ok; g += npairs) {
-          const Fp8Tile t = f8_tile<WGRAD>(g, args, s_at, s_cnt, s_first);
+          const Fp8Tile t = f8_tile<WGRAD, SPLIT>(g, split, args, s_at, s_cnt, s_first);
           const uint32_t idesc = idesc_e4m3_f32(256, t.n);
           const int per = f8_blocks_at_once(t.n), width = 256 / per;
           for (int kb = 0; kb < t.nkb; ++kb) {
@@ -367,8 +379,8 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
 #pragma unroll
               for (int k4 = 0; k4 < 4; ++k4)
                 umma_f8_pair(tmem_base + acc * 256 + sub * width, adesc0 + off + 2 * k4, bdesc0 + off + 2 * k4, idesc, k4 != 0 ? 1u : 0u);
-              umma_commit_pair(empty_bar(stage), 0x3);
-              if (last) umma_commit_pair(pfull_bar(acc), 0x3);
+              umma_commit_pair(empty_bar(stage), both);
+              if (last) umma_commit_pair(pfull_bar(acc), both);
             }
             __syncwarp();
             any = true;
@@ -383,7 +395,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
           }
         }
         if (any) {
-          if (leader) umma_commit_pair(drain_bar, 0x1);
+          if (leader) umma_commit_pair(drain_bar, (uint16_t)(1u << cta));
           volatile int no_abort = 0;
           f8_wait(drain_bar, 0, &no_abort, args.status, SITE_GEMM_DRAIN);
         }
@@ -395,7 +407,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
       uint32_t q_phase = 0;
       bool ok = true;
       for (int g = pair; g < total && ok; g += npairs) {
-        const Fp8Tile t = f8_tile<WGRAD>(g, args, s_at, s_cnt, s_first);
+        const Fp8Tile t = f8_tile<WGRAD, SPLIT>(g, split, args, s_at, s_cnt, s_first);
         const int a_row = t.m * 256 + 128 * (int)rank;
         for (int kb0 = 0; kb0 < t.nkb; kb0 += F8_GROUP) {
           float b[F8_GROUP][8], a4[F8_GROUP][4];
@@ -445,7 +457,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     // ------------------------------------------------------------------ epilogue (both CTAs)
     const int quarter = warp & 3;
     const int side = (warp - 4) >> 2;  // 32-column pieces 2 i + side are this warp's
-    const uint32_t pempty0_cl = mapa_shared(pempty_bar(0), 0);
+    const uint32_t pempty0_cl = mapa_shared(pempty_bar(0), cta & ~1u);
     const uint32_t tlane = tmem_base + (uint32_t(quarter * 32) << 16) + side * 32;
     const uint32_t lane_slot = side * 128 + 16 * (lane & 3), lane_rows = 4 * (256 + quarter * 32 + (lane >> 2) * (args.mixed ? 4 : 1)), row_step = args.mixed ? 4 : 32;
     const bool leader = elect_one();
@@ -453,7 +465,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     uint32_t acc_phase = 0, q_phase = 0;
     bool ok = true, ready = false;
     for (int g = pair; g < total && ok; g += npairs) {
-      const Fp8Tile t = f8_tile<WGRAD>(g, args, s_at, s_cnt, s_first);
+      const Fp8Tile t = f8_tile<WGRAD, SPLIT>(g, split, args, s_at, s_cnt, s_first);
       // sum[s]: piece s / 2, TMEM lanes 16 (s % 2) of the quarter: [g][row lane / 4, + 8], columns 2 t, 2 t + 1 of group g
       float sum[8][4][2][2];
 #pragma unroll
@@ -552,6 +564,35 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
       else if (pieces > 2) run(two{}, two{});
       else run(one{}, four{});
       if (!ok) break;
+      if (SPLIT) {
+        // One tile a cluster: the other pairs' sums come into the stages of the first one's CTAs, which nothing uses any more
+        // once all have met, and are added in the splits' order.
+        cluster_sync();
+        const uint32_t to = mapa_shared(smem_u32(smem), rank) + 4u * (threadIdx.x - 128);
+        const int regs = 32 * np_of(t.n);  // of this warp's side or the wider one
+        if (split > 0) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if ((i >> 1) < np_of(t.n))
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                st_shared_cluster_u32(to + 1024u * (uint32_t)((split - 1) * regs + 16 * i + j),
+                                      __float_as_uint(sum[i][j >> 2][j >> 1 & 1][j & 1]));
+        }
+        cluster_sync();
+        met = true;
+        if (split > 0) break;
+        const uint32_t from = smem_u32(smem) + 4u * (threadIdx.x - 128);
+#pragma unroll 1
+        for (int p = 1; p < args.splits; ++p) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if ((i >> 1) < np_of(t.n))
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                sum[i][j >> 2][j >> 1 & 1][j & 1] += lds1(from + 1024u * (uint32_t)((p - 1) * regs + 16 * i + j));
+        }
+      }
       // out[column][row]: of a column a lane has four rows, neighbours where the rows are mixed
       const int u = lane >> 2;
       const int j0 = t.m * 256 + 128 * (int)rank + 32 * quarter + (args.mixed ? 4 * u : u);
@@ -585,6 +626,10 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     }
   }
 
+  if (SPLIT && !met) {  // the roles that joined no sums, and pairs without a tile
+    cluster_sync();
+    cluster_sync();
+  }
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // neither CTA leaves while the pair's MMAs or signals may still touch it
@@ -625,16 +670,77 @@ bool f8_wide(const void* out, int64_t ld, int64_t width, bool bf16) {
   return ld % 4 == 0 && width % 4 == 0 && (reinterpret_cast<uintptr_t>(out) & (bf16 ? 7u : 15u)) == 0;
 }
 
+// How many clusters of 2, 4 and 8 CTAs fit the device at once; asked once for each device.
+template <bool WGRAD, typename OUT>
+cudaError_t f8_clusters(int (&clusters)[3]) {
+  static int known[64][3] = {};
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (known[dev][0] == 0) {
+    auto kern = fp8_gemm_kernel<WGRAD, true, OUT>;
+    err = cudaFuncSetAttribute(fp8_gemm_kernel<WGRAD, false, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)f8_smem(FP8_MAX_E));
+    if (err != cudaSuccess) return err;
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)f8_smem(FP8_MAX_E));
+    for (int i = 2; i >= 0 && err == cudaSuccess; --i) {  // the first entry last: it says that the others are there
+      cudaLaunchConfig_t cfg{};
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 2u << i;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.blockDim = dim3(F8_THREADS, 1, 1);
+      cfg.gridDim = dim3(64u << i, 1, 1);
+      cfg.dynamicSmemBytes = f8_smem(FP8_MAX_E);
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int n = 0;
+      err = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+      known[dev][i] = std::max(1, n);
+    }
+    if (err != cudaSuccess) return err;
+  }
+  for (int i = 0; i < 3; ++i) clusters[i] = known[dev][i];
+  return cudaSuccess;
+}
+
+// The columns of a chunk (g.nmax) and the pairs that share a tile (g.splits), by the time of the pair that has most to do:
+// about 200 + 4 n cycles for each block of n columns (measured: 1,200 at 256, 700 at 128, 450 at 64), a tile's start and end about
+// 3,000, the joining of splits 3,000 + 20 n.  `each`: columns of each of the groups; where the groups' sizes are not known here
+// (`known` false) it is their average, and half a chunk a group is added.  Splits are taken only where every tile has its
+// own cluster and all clusters fit at once (36 of 4 CTAs, 15 of 8 on GB300), and the sums fit the first pair's stages.  Returns
+// the tiles at most.
+int64_t f8_plan(Fp8GemmArgs& g, int n_sm, int64_t nkb, int64_t groups, int64_t each, bool known, const int (&clusters)[3]) {
+  const int64_t pairs = std::max(1, n_sm / 2);
+  int64_t best = INT64_MAX, tiles = 0;
+  for (int nmax = 256; nmax >= 32; nmax /= 2)
+    for (int splits = 1; splits <= 4; splits *= 2) {
+      const int64_t whole = (each + nmax - 1) / nmax;
+      const int64_t chunks = known ? groups * whole : std::max(groups, groups * (2 * each + nmax) / (2 * nmax));
+      const int64_t most = (known ? chunks : groups * whole + g.E) * g.MT;
+      if (splits > 1 && (most > clusters[splits / 2] || nkb < 4 * splits || (splits - 1) * nmax * 512 > F8_STAGES * F8_STAGE)) continue;
+      const int64_t n = std::max<int64_t>(16, groups * each / chunks);
+      const int64_t waves = (chunks * g.MT * splits + pairs - 1) / pairs;
+      const int64_t cost = waves * ((nkb + splits - 1) / splits * (200 + 4 * n) + 3000) + (splits > 1 ? 3000 + 20 * n : 0);
+      if (cost < best) {
+        best = cost;
+        tiles = most;
+        g.nmax = nmax;
+        g.splits = splits;
+      }
+    }
+  return tiles;
+}
+
 template <bool WGRAD, typename OUT>
 cudaError_t launch(const CUtensorMap& ta, const CUtensorMap (&tb)[3], const Fp8GemmArgs& args, int64_t tiles, int n_sm,
                    cudaStream_t st) {
-  auto kern = fp8_gemm_kernel<WGRAD, OUT>;
-  cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)f8_smem(FP8_MAX_E));
-  if (err != cudaSuccess) return err;
+  auto kern = args.splits > 1 ? fp8_gemm_kernel<WGRAD, true, OUT> : fp8_gemm_kernel<WGRAD, false, OUT>;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.x = 2 * args.splits;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.blockDim = dim3(F8_THREADS, 1, 1);
@@ -642,14 +748,15 @@ cudaError_t launch(const CUtensorMap& ta, const CUtensorMap (&tb)[3], const Fp8G
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(tiles, std::max(1, n_sm / 2))), 1, 1);
-  err = cudaLaunchKernelEx(&cfg, kern, ta, tb[0], tb[1], tb[2], args);
+  // with splits every tile has its cluster
+  cfg.gridDim = dim3((unsigned)(2 * args.splits * (args.splits > 1 ? tiles : std::min<int64_t>(tiles, std::max(1, n_sm / 2)))), 1, 1);
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, ta, tb[0], tb[1], tb[2], args);
   return err != cudaSuccess ? err : cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_fp8_product_pairs(const Fp8MatmulArgs& a, bool bf16_out, int n_sm, cudaStream_t st) {
+cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, bool bf16_out, int n_sm, cudaStream_t st) {
   Fp8GemmArgs g = {};
   g.E = a.E;
   g.nkb = (int)((a.K + 127) / 128);
@@ -665,12 +772,12 @@ cudaError_t launch_fp8_product_pairs(const Fp8MatmulArgs& a, bool bf16_out, int 
   g.mixed = a.N % 32 == 0;
   g.wide_out = g.mixed && f8_wide(a.out, a.out_stride, a.N, bf16_out);
   g.status = a.status;
-  // narrower chunks while the tiles of wider ones leave pairs without work
-  g.nmax = 256;
-  const int64_t pairs = std::max(1, n_sm / 2);
-  while (g.nmax > 32 && g.MT * std::max<int64_t>((a.R + g.nmax - 1) / g.nmax, std::min<int64_t>(a.E, a.R)) < pairs)
-    g.nmax /= 2;
-  const int64_t tiles = ((a.R + g.nmax - 1) / g.nmax + a.E) * g.MT;  // at most
+  const int64_t groups = std::min<int64_t>(a.E, a.R);  // that can have rows
+  int clusters[3];
+  const cudaError_t err = bf16_out ? f8_clusters<false, __nv_bfloat16>(clusters) : f8_clusters<false, float>(clusters);
+  if (err != cudaSuccess) return err;
+  int64_t tiles = f8_plan(g, n_sm, g.nkb, groups, (a.R + groups - 1) / groups, a.E == 1, clusters);
+  if (a.E > 1) tiles = ((a.R + g.nmax - 1) / g.nmax + a.E) * g.MT;  // at most, whatever the groups' sizes
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
   CUtensorMap ta, tb[3];
   if (!tmap_a(&ta, a.w, a.K, a.N, a.E, a.w_stride, g.mixed) ||
@@ -696,10 +803,10 @@ cudaError_t launch_fp8_weight_grad(const Fp8WeightGradArgs& a, bool bf16_out, in
   g.mixed = a.H % 32 == 0;
   g.wide_out = g.mixed && f8_wide(a.out, a.H, a.H, bf16_out);
   g.status = a.status;
-  g.nmax = 256;
-  const int64_t pairs = std::max(1, n_sm / 2);
-  while (g.nmax > 32 && a.E * g.MT * ((a.N + g.nmax - 1) / g.nmax) < pairs) g.nmax /= 2;
-  const int64_t tiles = a.E * (int64_t)g.MT * ((a.N + g.nmax - 1) / g.nmax);
+  int clusters[3];
+  const cudaError_t err = bf16_out ? f8_clusters<true, __nv_bfloat16>(clusters) : f8_clusters<true, float>(clusters);
+  if (err != cudaSuccess) return err;
+  const int64_t tiles = f8_plan(g, n_sm, (a.R / 128 + a.E - 1) / a.E, a.E, a.N, true, clusters);
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
   CUtensorMap ta, tb[3];
   const int64_t P = 128 * g.blocks;

@@ -65,13 +65,18 @@ def _fn(name, desc, pointers):
     return fn
 
 
+# The current device's index and a device's current stream, without what torch.cuda adds to them (0.5 us of a call).
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _device(t, name) -> int:
     """The index of the device that a CUDA tensor is on: the current one."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    device = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if device < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    device = t.get_device()
-    if device != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if device != _current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{_current_device()}")
     return device
 
 
@@ -85,11 +90,13 @@ def _expect(t, shape, dtype, name, device):
 
 def _packed(t, shape, dtype, name, device) -> int:
     """The address of a contiguous tensor of this shape and type."""
-    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.get_device() == device and
-            t.is_contiguous()):
-        _expect(t, shape, dtype, name, device)
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    try:
+        if t.shape == shape and t.dtype is dtype and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _expect(t, shape, dtype, name, device)
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _optional(t, shape, dtype, name, device) -> Optional[int]:
@@ -99,15 +106,23 @@ def _optional(t, shape, dtype, name, device) -> Optional[int]:
 def _rows(t, shape, dtype, name, device, unit=1):
     """(address, row stride) of a [rows][width] tensor whose rows are contiguous, do not overlap and start at multiples
     of `unit` elements; a stride of 0 stands for the packed one."""
-    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.get_device() == device):
+    try:
+        if not (t.shape == shape and t.dtype is dtype and t.get_device() == device):
+            _expect(t, shape, dtype, name, device)
+    except AttributeError:
         _expect(t, shape, dtype, name, device)
-    if t.is_contiguous() and (unit == 1 or shape[1] % unit == 0):
-        return t.data_ptr(), 0
     rows, width = shape
+    if t.is_contiguous() and (unit == 1 or width % unit == 0):
+        return t.data_ptr(), 0
     if (width > 1 and t.stride(1) != 1) or (rows > 1 and (t.stride(0) < width or t.stride(0) % unit)):
         raise ValueError(f"{name}: rows must be contiguous, must not overlap and must start at multiples of {unit} "
                          f"elements, got strides {t.stride()}")
     return t.data_ptr(), t.stride(0) if rows > 1 else 0
+
+
+def _queue(stream, device):
+    """The handle of the stream of a call: the device's current one unless given."""
+    return _raw_stream(device) if stream is None and _raw_stream is not None else _stream(stream)
 
 
 def empty_e4m3(*shape, device="cuda") -> torch.Tensor:
@@ -122,11 +137,13 @@ def _blocks(n) -> int:
 
 # ------------------------------------------------------------------ rows by a schedule table
 
-def _elem(t, name):
-    if not isinstance(t, torch.Tensor) or t.dtype not in ELEM_TYPES or t.dim() != 2:
+def _elem(t, name) -> int:
+    """The mok_elem_type of a matrix."""
+    kind = ELEM_TYPES.get(t.dtype) if isinstance(t, torch.Tensor) and t.dim() == 2 else None
+    if kind is None:
         raise ValueError(f"{name}: expected a float32 or bfloat16 matrix, got "
                          f"{(tuple(t.shape), t.dtype) if isinstance(t, torch.Tensor) else type(t).__name__}")
-    return t.dtype
+    return kind
 
 
 def gather_rows(x: torch.Tensor, src_of: torch.Tensor, k: int, gates: Optional[torch.Tensor] = None,
@@ -134,7 +151,7 @@ def gather_rows(x: torch.Tensor, src_of: torch.Tensor, k: int, gates: Optional[t
                 stream=None) -> torch.Tensor:
     """Sorted rows [R][H] of tokens x [T][H] (mok_gather_rows): row r is gates[a] x[a / k], a = src_of[r]; zeros where
     src_of is -1.  ``device_status``: int32 [2] CUDA tensor for an index out of range."""
-    dtype = _elem(x, "x")
+    kind, dtype = _elem(x, "x"), x.dtype
     device = _device(x, "x")
     T, H = x.shape
     R = src_of.shape[0] if isinstance(src_of, torch.Tensor) and src_of.dim() == 1 else -1
@@ -142,11 +159,11 @@ def gather_rows(x: torch.Tensor, src_of: torch.Tensor, k: int, gates: Optional[t
         out = torch.empty((max(0, R), H), dtype=dtype, device=x.device)
     xp, xs = _rows(x, (T, H), dtype, "x", device)
     op, os_ = _rows(out, (R, H), dtype, "out", device)
-    d = RowsDesc(T, R, H, xs, os_, k, ELEM_TYPES[dtype])
+    d = RowsDesc(T, R, H, xs, os_, k, kind)
     code = _fn("mok_gather_rows", RowsDesc, 5)(
         d, xp, _packed(src_of, (R,), torch.int32, "src_of", device),
         _optional(gates, (T, k), torch.float32, "gates", device), op,
-        _optional(device_status, (2,), torch.int32, "device_status", device), _stream(stream))
+        _optional(device_status, (2,), torch.int32, "device_status", device), _queue(stream, device))
     if code:
         _check("mok_gather_rows", code)
     return out
@@ -163,7 +180,7 @@ def merge_rows(o: torch.Tensor, row_of: torch.Tensor, k: int, gates: Optional[to
                stream=None) -> torch.Tensor:
     """Tokens [T][H] of sorted rows o [R][H] (mok_merge_rows): y[t] = sum_j gates[t][j] o[row_of[t k + j]], where
     row_of is -1 nothing.  Without gates the gradient of ``gather_rows``."""
-    dtype = _elem(o, "o")
+    kind, dtype = _elem(o, "o"), o.dtype
     device = _device(o, "o")
     R, H = o.shape
     T = _tokens(row_of, k)
@@ -171,11 +188,11 @@ def merge_rows(o: torch.Tensor, row_of: torch.Tensor, k: int, gates: Optional[to
         out = torch.empty((T, H), dtype=dtype, device=o.device)
     rp, rs = _rows(o, (R, H), dtype, "o", device)
     yp, ys = _rows(out, (T, H), dtype, "out", device)
-    d = RowsDesc(T, R, H, ys, rs, k, ELEM_TYPES[dtype])
+    d = RowsDesc(T, R, H, ys, rs, k, kind)
     code = _fn("mok_merge_rows", RowsDesc, 5)(
         d, rp, _packed(row_of, (T * k,), torch.int32, "row_of", device),
         _optional(gates, (T, k), torch.float32, "gates", device), yp,
-        _optional(device_status, (2,), torch.int32, "device_status", device), _stream(stream))
+        _optional(device_status, (2,), torch.int32, "device_status", device), _queue(stream, device))
     if code:
         _check("mok_merge_rows", code)
     return out
@@ -186,7 +203,7 @@ def merge_rows_backward(dy: torch.Tensor, o: torch.Tensor, row_of: torch.Tensor,
                         stream=None) -> Dict[str, torch.Tensor]:
     """Gradient of ``merge_rows`` (mok_merge_rows_backward): {"do": [R][H], "dgates": f32 [T][k]}.  Rows of "do" that
     no assignment names are left as they were (zeros where it is made here)."""
-    dtype = _elem(dy, "dy")
+    kind, dtype = _elem(dy, "dy"), dy.dtype
     device = _device(dy, "dy")
     if not isinstance(gates, torch.Tensor) or gates.dim() != 2:
         raise ValueError("gates: expected a float32 matrix")
@@ -200,12 +217,12 @@ def merge_rows_backward(dy: torch.Tensor, o: torch.Tensor, row_of: torch.Tensor,
     dp, ds = _rows(out["do"], (R, H), dtype, 'out["do"]', device)
     if ds != rs and (ds or H) != (rs or H):
         raise ValueError(f'out["do"]: rows {ds or H} elements apart, those of o {rs or H}')
-    d = RowsDesc(T, R, H, ys, rs, k, ELEM_TYPES[dtype])
+    d = RowsDesc(T, R, H, ys, rs, k, kind)
     code = _fn("mok_merge_rows_backward", RowsDesc, 7)(
         d, yp, rp, _packed(row_of, (T * k,), torch.int32, "row_of", device),
         _packed(gates, (T, k), torch.float32, "gates", device), dp,
         _packed(out["dgates"], (T, k), torch.float32, 'out["dgates"]', device),
-        _optional(device_status, (2,), torch.int32, "device_status", device), _stream(stream))
+        _optional(device_status, (2,), torch.int32, "device_status", device), _queue(stream, device))
     if code:
         _check("mok_merge_rows_backward", code)
     return out
@@ -230,7 +247,7 @@ def fp8_quantize(x: torch.Tensor, source: str = "plain", grad: Optional[torch.Te
     [R][C/2]).  Returns {"q" [R][C], "scale" [C/128][R]} (without ``rows`` neither) and, with the groups' ``offsets``
     [E+1], {"qt" [C][P], "qt_scale" [P/128][C]}: along each group's rows, for ``fp8_weight_grad``.  ``out``: buffers
     for the pairs that are wanted."""
-    dtype = _elem(x, "x")
+    kind, dtype = _elem(x, "x"), x.dtype
     device = _device(x, "x")
     if source not in SOURCES:
         raise ValueError(f"source must be one of {', '.join(SOURCES)}, got {source!r}")
@@ -253,7 +270,7 @@ def fp8_quantize(x: torch.Tensor, source: str = "plain", grad: Optional[torch.Te
             out |= {"q": empty_e4m3(max(0, R), C, device=x.device), "scale": new(_blocks(C), max(0, R))}
         if E:
             out |= {"qt": empty_e4m3(C, fp8_columns(R, E), device=x.device), "qt_scale": new(R // 128 + E, C)}
-    d = Fp8QuantizeDesc(R, C, T, 0, 0, 0, 0, 0, E, k, SOURCES[source], ELEM_TYPES[dtype])
+    d = Fp8QuantizeDesc(R, C, T, 0, 0, 0, 0, 0, E, k, SOURCES[source], kind)
     xp, d.x_stride = _rows(x, (T, width), dtype, "x", device)
     gp = qp = sp = tp = tsp = None
     if grad is not None:
@@ -270,7 +287,7 @@ def fp8_quantize(x: torch.Tensor, source: str = "plain", grad: Optional[torch.Te
         d, xp, gp, _optional(src_of, (R,), torch.int32, "src_of", device),
         _optional(gates, (T, k), torch.float32, "gates", device),
         _optional(offsets, (E + 1,), torch.int32, "offsets", device), qp, sp, tp, tsp,
-        _optional(device_status, (2,), torch.int32, "device_status", device), _stream(stream))
+        _optional(device_status, (2,), torch.int32, "device_status", device), _queue(stream, device))
     if code:
         _check("mok_fp8_quantize", code)
     return out
@@ -354,7 +371,7 @@ class Fp8Weights:
         d = Fp8WeightsDesc(N, K, self._q[1], self._qt[1], E, ELEM_TYPES[w.dtype])
         code = _fn("mok_fp8_quantize_weights", Fp8WeightsDesc, 5)(
             d, _packed(w, shape, w.dtype, "w", self._index), self._q[0], self._scale, self._qt[0], self._qt_scale,
-            _stream(stream))
+            _queue(stream, self._index))
         if code:
             _check("mok_fp8_quantize_weights", code)
         return self
@@ -377,7 +394,7 @@ class Fp8Weights:
 
     def _matmul(self, x, x_scale, offsets, out, dtype, stream, N, K, w, w_scale):
         device = self._index
-        if device != torch.cuda.current_device():
+        if device != _current_device():
             raise ValueError(f"the weights are on cuda:{device}, not on the current device")
         E = self.shape[0]
         if offsets is None and E != 1:
@@ -395,7 +412,7 @@ class Fp8Weights:
         op, d.out_stride = _rows(out, (R, N), dtype, "out", device)
         code = _fn("mok_fp8_matmul", Fp8MatmulDesc, 7)(
             d, xp, sp, w[0], w_scale, _optional(offsets, (E + 1,), torch.int32, "offsets", device), op, self._status,
-            _stream(stream))
+            _queue(stream, device))
         if code:
             _check("mok_fp8_matmul", code)
         return out
@@ -435,7 +452,7 @@ def fp8_weight_grad(dy: torch.Tensor, dy_scale: torch.Tensor, x: torch.Tensor, x
         _packed(x_scale, (columns // 128, H), torch.float32, "x_scale", device),
         _packed(offsets, (E + 1,), torch.int32, "offsets", device),
         _packed(out, (E, N, H), dtype, "out", device),
-        _optional(device_status, (2,), torch.int32, "device_status", device), _stream(stream))
+        _optional(device_status, (2,), torch.int32, "device_status", device), _queue(stream, device))
     if code:
         _check("mok_fp8_weight_grad", code)
     return out

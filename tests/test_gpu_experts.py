@@ -404,7 +404,8 @@ def check_product(got, want, size, K, dtype):
 # rule on sizes, rows behind the last group
 PRODUCTS = [([1], 1, 1), ([3], 7, 16), ([1, 0, 2], 130, 300), ([8, 9, 0, 7], 100, 128), ([17, 30, 5], 264, 1111),
             ([40], 513, 640), ([0, 0, 70, 1], 384, 257), ([129], 256, 512), ([300, 0, 5, 64], 500, 384), ([1] * 40, 48, 200),
-            ([513, 250], 260, 900), ([0, 0], 16, 16), ([33] * 5, 1024, 128), ([700], 250, 2000)]
+            ([513, 250], 260, 900), ([0, 0], 16, 16), ([33] * 5, 1024, 128), ([700], 250, 2000), ([5, 0, 90], 64, 4100),
+            ([250], 96, 2200), ([100], 1000, 6000)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
@@ -430,7 +431,8 @@ def test_product(counts, N, K, dtype):
     assert (torch.as_strided(out2, (R - 1, 3), (N + 3, 1), N) == 3.0).all()
 
 
-@pytest.mark.parametrize("R,N,K", [(1, 64, 256), (5, 1000, 100), (16, 256, 2048), (100, 130, 384), (257, 700, 1300)])
+@pytest.mark.parametrize("R,N,K", [(1, 64, 256), (5, 1000, 100), (16, 256, 2048), (100, 130, 384), (257, 700, 1300), (1, 520, 7168), (64, 260, 4100),
+                                   (200, 96, 3000)])
 def test_product_without_groups(R, N, K):
     rng = np.random.default_rng(R)
     w, _ = values(rng, (N, K), BF)
@@ -450,7 +452,8 @@ def test_product_without_groups(R, N, K):
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("counts,N,H", [([1], 1, 1), ([3, 0, 130], 7, 300), ([128, 256], 129, 64), ([0, 0, 0], 33, 65),
                                         ([1] * 30, 40, 24), ([300, 1, 513], 256, 260), ([700], 513, 640),
-                                        ([64] * 8, 520, 256)], ids=lambda v: str(v)[:24])
+                                        ([64] * 8, 520, 256), ([2100], 70, 100), ([1100, 1200], 40, 64)],
+                         ids=lambda v: str(v)[:24])
 def test_weight_grad(counts, N, H, dtype):
     rng = np.random.default_rng(sum(counts) + N)
     E = len(counts)
