@@ -49,6 +49,7 @@ struct Fp8GemmArgs {
   int64_t ld;             // elements between out's rows
   int mixed;              // TMEM lane 8 k + u of a quarter holds A's row 4 u + k, else the rows are in order
   int splits;             // pairs of a cluster, each with its share of a tile's blocks
+  uint32_t magic_per, magic_nc;  // f8_divide: tiles of a group and of a column (weight grad), or MT
   int wide_out;           // mixed, and out's rows take four neighbours at once
   int* status;
 };
@@ -82,46 +83,55 @@ struct Fp8Tile {
   int kb0, nkb;       // first block of K, number of blocks
 };
 
-// Tile g: the groups' first tiles by binary search (product), or by division (weight grad).
-// s_at / s_cnt: product: first row and rows of each group, s_first: chunks before it; weight grad: first block, blocks.
+// g / d by a product with ceil(2^32 / d), which is at most one too much for g below 2^31.
+__device__ __forceinline__ int f8_divide(int g, int d, uint32_t magic) {
+  if (d == 1) return g;
+  const int q = (int)__umulhi((uint32_t)g, magic);
+  return q - (q * (int64_t)d > g);
+}
+
+// Tile g, by all lanes of a warp together.  s_at / s_cnt (addresses in shared memory): product: first row and rows of
+// each group, s_first: chunks before it; weight grad: first block and blocks.  The product's group is the last whose first
+// tile is not behind g: 32 entries are looked at at once, first every 32nd.
 template <bool WGRAD, bool SPLIT>
-__device__ __forceinline__ Fp8Tile f8_tile(int g, int split, const Fp8GemmArgs& a, const int* s_at, const int* s_cnt,
-                                           const int* s_first) {
+__device__ __forceinline__ Fp8Tile f8_tile(int g, int split, const Fp8GemmArgs& a, uint32_t s_at, uint32_t s_cnt,
+                                           uint32_t s_first) {
   Fp8Tile t;
   int nc, c, rows;
   if (WGRAD) {
     nc = (a.NB + a.nmax - 1) / a.nmax;
-    const int per = nc * a.MT;
-    t.e = g / per;
-    const int l = g - t.e * per;
-    t.m = l / nc;
+    t.e = f8_divide(g, nc * a.MT, a.magic_per);
+    const int l = g - t.e * nc * a.MT;
+    t.m = f8_divide(l, nc, a.magic_nc);
     c = l - t.m * nc;
     rows = a.NB;
-    t.kb0 = s_at[t.e];
-    t.nkb = s_cnt[t.e];
+    t.kb0 = lds1i(s_at + 4 * t.e);
+    t.nkb = lds1i(s_cnt + 4 * t.e);
     t.col0 = 0;
   } else {
-    int lo = 0, hi = a.E;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (s_first[mid] * a.MT <= g) lo = mid; else hi = mid;
-    }
+    const int chunk = f8_divide(g, a.MT, a.magic_per);  // this tile's place among chunks, groups without rows left out
+    const int lane = threadIdx.x & 31;
+    int lo = 0;
+    if (a.E > 32) lo = 32 * (__popc(__ballot_sync(0xffffffffu, lds1i(s_first + 4 * min(32 * lane, a.E)) <= chunk && 32 * lane < a.E)) - 1);
+    const int at = lo + lane;
+    lo += __popc(__ballot_sync(0xffffffffu, at < a.E && lds1i(s_first + 4 * min(at, a.E)) <= chunk)) - 1;
     t.e = lo;
-    nc = s_first[lo + 1] - s_first[lo];
-    const int l = g - s_first[lo] * a.MT;
-    t.m = l / nc;
+    const int before = lds1i(s_first + 4 * lo);
+    nc = lds1i(s_first + 4 * lo + 4) - before;
+    const int l = g - before * a.MT;
+    t.m = nc == 1 ? l : l / nc;
     c = l - t.m * nc;
-    rows = s_cnt[lo];
+    rows = lds1i(s_cnt + 4 * lo);
     t.kb0 = 0;
     t.nkb = a.nkb;
-    t.col0 = s_at[lo];
+    t.col0 = lds1i(s_at + 4 * lo);
   }
   if (SPLIT) {
     const int lo = t.nkb * split / a.splits;
     t.kb0 += lo;
     t.nkb = t.nkb * (split + 1) / a.splits - lo;
   }
-  const int each = ((rows + nc - 1) / nc + 15) & ~15;  // equal chunks
+  const int each = nc == 1 ? rows : ((rows + nc - 1) / nc + 15) & ~15;  // equal chunks
   t.col0 += c * each;
   t.cols = max(0, min(each, rows - c * each));
   t.n = max(16, (t.cols + 15) & ~15);
@@ -190,8 +200,9 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
   int* s_at = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + F8_SMEM_BARS);
   int* s_cnt = s_at + (args.E + 1);
   int* s_first = s_cnt + (args.E + 1);
+  const uint32_t at0 = smem_u32(s_at);
 
-  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);  // uniform, and known to be
+  const int warp = __reduce_max_sync(0xffffffffu, (int)threadIdx.x >> 5);  // uniform, and known to be
   const int lane = threadIdx.x & 31;
   const uint32_t cta = cluster_ctarank(), rank = cta & 1;  // rank 0 issues its pair's MMAs
   const int split = SPLIT ? (int)(cta >> 1) : 0;
@@ -278,7 +289,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
   __syncthreads();
   cluster_sync();  // both CTAs' barriers are initialised before either signals the other's
   tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t tmem_base = __reduce_or_sync(0xffffffffu, *tmem_slot);
   const int total = WGRAD ? args.E * args.MT * ((args.NB + args.nmax - 1) / args.nmax) : s_first[args.E] * args.MT;
 
   bool met = false;  // has been at the two meetings of a split tile's pairs
@@ -300,7 +311,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
       uint32_t phase = 0;
       bool ok = true;
       for (int g = pair; g < total && ok; g += npairs) {
-        const Fp8Tile t = f8_tile<WGRAD, SPLIT>(g, split, args, s_at, s_cnt, s_first);
+        const Fp8Tile t = f8_tile<WGRAD, SPLIT>(g, split, args, at0, at0 + 4 * (args.E + 1), at0 + 8 * (args.E + 1));
         const int half = t.n >> 1;
         // the CTA's rows of B in the fewest boxes of 128, 64 and 32 rows
         const int b128 = half > 96, b64 = !b128 && half > 32, b32 = !b128 && (half <= 32 || half > 64);
@@ -363,7 +374,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         uint32_t phase = 0, acc_phase = 0;
         bool ok = true, any = false;
         for (int g = pair; g < total && ok; g += npairs) {
-          const Fp8Tile t = f8_tile<WGRAD, SPLIT>(g, split, args, s_at, s_cnt, s_first);
+          const Fp8Tile t = f8_tile<WGRAD, SPLIT>(g, split, args, at0, at0 + 4 * (args.E + 1), at0 + 8 * (args.E + 1));
           const uint32_t idesc = idesc_e4m3_f32(256, t.n);
           const int per = f8_blocks_at_once(t.n), width = 256 / per;
           for (int kb = 0; kb < t.nkb; ++kb) {
@@ -407,7 +418,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
       uint32_t q_phase = 0;
       bool ok = true;
       for (int g = pair; g < total && ok; g += npairs) {
-        const Fp8Tile t = f8_tile<WGRAD, SPLIT>(g, split, args, s_at, s_cnt, s_first);
+        const Fp8Tile t = f8_tile<WGRAD, SPLIT>(g, split, args, at0, at0 + 4 * (args.E + 1), at0 + 8 * (args.E + 1));
         const int a_row = t.m * 256 + 128 * (int)rank;
         for (int kb0 = 0; kb0 < t.nkb; kb0 += F8_GROUP) {
           float b[F8_GROUP][8], a4[F8_GROUP][4];
@@ -458,14 +469,14 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     const int quarter = warp & 3;
     const int side = (warp - 4) >> 2;  // 32-column pieces 2 i + side are this warp's
     const uint32_t pempty0_cl = mapa_shared(pempty_bar(0), cta & ~1u);
-    const uint32_t tlane = tmem_base + (uint32_t(quarter * 32) << 16) + side * 32;
+    const uint32_t tlane = __reduce_or_sync(0xffffffffu, tmem_base + (uint32_t(quarter * 32) << 16) + side * 32);
     const uint32_t lane_slot = side * 128 + 16 * (lane & 3), lane_rows = 4 * (256 + quarter * 32 + (lane >> 2) * (args.mixed ? 4 : 1)), row_step = args.mixed ? 4 : 32;
     const bool leader = elect_one();
     int acc = 0, q = 0;
     uint32_t acc_phase = 0, q_phase = 0;
     bool ok = true, ready = false;
     for (int g = pair; g < total && ok; g += npairs) {
-      const Fp8Tile t = f8_tile<WGRAD, SPLIT>(g, split, args, s_at, s_cnt, s_first);
+      const Fp8Tile t = f8_tile<WGRAD, SPLIT>(g, split, args, at0, at0 + 4 * (args.E + 1), at0 + 8 * (args.E + 1));
       // sum[s]: piece s / 2, TMEM lanes 16 (s % 2) of the quarter: [g][row lane / 4, + 8], columns 2 t, 2 t + 1 of group g
       float sum[8][4][2][2];
 #pragma unroll
@@ -597,32 +608,36 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
       const int u = lane >> 2;
       const int j0 = t.m * 256 + 128 * (int)rank + 32 * quarter + (args.mixed ? 4 * u : u);
       const int jstep = args.mixed ? 1 : 8;
-      OUT* out = static_cast<OUT*>(args.out) + (WGRAD ? (int64_t)t.e * args.NB + t.col0 : (int64_t)t.col0) * args.ld + j0;
+      const int left = t.cols - side * 32 - 2 * (lane & 3);  // of the columns from this lane's first on
+      OUT* o = static_cast<OUT*>(args.out) +
+               ((WGRAD ? (int64_t)t.e * args.NB + t.col0 : (int64_t)t.col0) + side * 32 + 2 * (lane & 3)) * args.ld + j0;
+      const int64_t ld = args.ld;
+      auto columns = [&](auto&& store) {  // store(o, four rows of a column)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i, o += 32 * ld)
 #pragma unroll
-        for (int g8 = 0; g8 < 4; ++g8) {
-          const int c = (2 * i + side) * 32 + 8 * g8 + 2 * (lane & 3);
-          float x[2][4];
+          for (int g8 = 0; g8 < 4; ++g8, o += 8 * ld)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            x[0][k] = sum[2 * i + (k >> 1)][g8][k & 1][0];
-            x[1][k] = sum[2 * i + (k >> 1)][g8][k & 1][1];
+            for (int h = 0; h < 2; ++h)
+              store(o + h * ld, 64 * i + 8 * g8 + h < left,
+                    make_float4(sum[2 * i][g8][0][h], sum[2 * i][g8][1][h], sum[2 * i + 1][g8][0][h], sum[2 * i + 1][g8][1][h]));
+      };
+      if (args.wide_out && t.cols == 256 && j0 < args.NM) {
+        columns([&](OUT* p, bool, float4 v) { f8_put4(p, v); });
+      } else if (args.wide_out) {
+        if (j0 < args.NM) columns([&](OUT* p, bool in, float4 v) {
+          if (in) f8_put4(p, v);
+        });
+      } else {
+        columns([&](OUT* p, bool in, float4 v) {
+          if (in) {
+            if (j0 < args.NM) f8_put(p, v.x);
+            if (j0 + jstep < args.NM) f8_put(p + jstep, v.y);
+            if (j0 + 2 * jstep < args.NM) f8_put(p + 2 * jstep, v.z);
+            if (j0 + 3 * jstep < args.NM) f8_put(p + 3 * jstep, v.w);
           }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (c + h < t.cols) {
-              OUT* o = out + (int64_t)(c + h) * args.ld;
-              if (args.wide_out) {
-                if (j0 < args.NM) f8_put4(o, make_float4(x[h][0], x[h][1], x[h][2], x[h][3]));
-              } else {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  if (j0 + k * jstep < args.NM) f8_put(o + k * jstep, x[h][k]);
-              }
-            }
-          }
-        }
+        });
+      }
     }
   }
 
@@ -669,6 +684,8 @@ bool tmap_boxes(CUtensorMap (&m)[3], const void* base, int64_t K, int64_t rows, 
 bool f8_wide(const void* out, int64_t ld, int64_t width, bool bf16) {
   return ld % 4 == 0 && width % 4 == 0 && (reinterpret_cast<uintptr_t>(out) & (bf16 ? 7u : 15u)) == 0;
 }
+
+uint32_t f8_magic(int64_t d) { return d == 1 ? 0 : (uint32_t)(((int64_t(1) << 32) + d - 1) / d); }
 
 // How many clusters of 2, 4 and 8 CTAs fit the device at once; asked once for each device.
 template <bool WGRAD, typename OUT>
@@ -779,6 +796,7 @@ cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, bool bf16_out, int n_sm, c
   int64_t tiles = f8_plan(g, n_sm, g.nkb, groups, (a.R + groups - 1) / groups, a.E == 1, clusters);
   if (a.E > 1) tiles = ((a.R + g.nmax - 1) / g.nmax + a.E) * g.MT;  // at most, whatever the groups' sizes
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+  g.magic_per = f8_magic(g.MT);
   CUtensorMap ta, tb[3];
   if (!tmap_a(&ta, a.w, a.K, a.N, a.E, a.w_stride, g.mixed) ||
       !tmap_boxes(tb, a.x, a.K, a.R, a.x_stride))
@@ -808,6 +826,9 @@ cudaError_t launch_fp8_weight_grad(const Fp8WeightGradArgs& a, bool bf16_out, in
   if (err != cudaSuccess) return err;
   const int64_t tiles = f8_plan(g, n_sm, (a.R / 128 + a.E - 1) / a.E, a.E, a.N, true, clusters);
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+  const int64_t nc = (a.N + g.nmax - 1) / g.nmax;
+  g.magic_per = f8_magic(nc * g.MT);
+  g.magic_nc = f8_magic(nc);
   CUtensorMap ta, tb[3];
   const int64_t P = 128 * g.blocks;
   if (!tmap_a(&ta, a.x, P, a.H, 1, a.x_stride, g.mixed) ||

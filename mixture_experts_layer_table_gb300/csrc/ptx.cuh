@@ -32,6 +32,11 @@ __device__ __forceinline__ float lds1(uint32_t a) {
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(a));
   return f;
 }
+__device__ __forceinline__ int lds1i(uint32_t a) {
+  int v;
+  asm volatile("ld.shared.s32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
 __device__ __forceinline__ void sts1(uint32_t a, float f) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(f) : "memory"); }
 
 // ---------------------------------------------------------------- mbarrier
