@@ -48,6 +48,7 @@ struct Fp8GemmArgs {
   void* out;
   int64_t ld;             // elements between out's rows
   int mixed;              // TMEM lane 8 k + u of a quarter holds A's row 4 u + k, else the rows are in order
+  int packed;             // host: which kernel
   int splits;             // pairs of a cluster, each with its share of a tile's blocks
   uint32_t magic_per, magic_nc;  // f8_divide: tiles of a group and of a column (weight grad), or MT
   int wide_out;           // mixed, and out's rows take four neighbours at once
@@ -182,7 +183,8 @@ __device__ __forceinline__ void f8_put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void f8_put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
 // tmA: A's rows, [groups][NM][K] bytes, boxes of 128 bytes x 128 rows; tmB: B's rows, boxes of 128 bytes x 32 rows.
-template <bool WGRAD, bool SPLIT, typename OUT>
+// PACKED: wide tiles form two sums in one instruction (launch chooses).
+template <bool WGRAD, bool SPLIT, bool PACKED, typename OUT>
 __global__ void __launch_bounds__(F8_THREADS, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmB64, const __grid_constant__ CUtensorMap tmB32,
@@ -541,13 +543,19 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
                   for (int r = 0; r < 2; ++r) {
-                    float x0 = __uint_as_float(v[p & 1][4 * j + 2 * r]), x1 = __uint_as_float(v[p & 1][4 * j + 2 * r + 1]);
-                    if (WGRAD) {
-                      x0 *= sa[2 * (p & 1) + r];
-                      x1 *= sa[2 * (p & 1) + r];
+                    float2 x = make_float2(__uint_as_float(v[p & 1][4 * j + 2 * r]), __uint_as_float(v[p & 1][4 * j + 2 * r + 1]));
+                    float (&to)[2] = sum[p][j][r];
+                    const float rs = WGRAD ? sa[2 * (p & 1) + r] : 1.0f;
+                    if (PACKED && G == 1) {
+                      if (WGRAD) x = __fmul2_rn(x, make_float2(rs, rs));
+                      const float2 z = __ffma2_rn(x, make_float2(c[j][0], c[j][1]), make_float2(to[0], to[1]));
+                      to[0] = z.x;
+                      to[1] = z.y;
+                    } else {
+                      if (WGRAD) x = make_float2(x.x * rs, x.y * rs);
+                      to[0] = fmaf(x.x, c[j][0], to[0]);
+                      to[1] = fmaf(x.y, c[j][1], to[1]);
                     }
-                    sum[p][j][r][0] = fmaf(x0, c[j][0], sum[p][j][r][0]);
-                    sum[p][j][r][1] = fmaf(x1, c[j][1], sum[p][j][r][1]);
                   }
                 if (p + 1 < S) tmem_wait_ld();
               }
@@ -696,10 +704,11 @@ cudaError_t f8_clusters(int (&clusters)[3]) {
   if (err != cudaSuccess) return err;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (known[dev][0] == 0) {
-    auto kern = fp8_gemm_kernel<WGRAD, true, OUT>;
-    err = cudaFuncSetAttribute(fp8_gemm_kernel<WGRAD, false, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)f8_smem(FP8_MAX_E));
-    if (err != cudaSuccess) return err;
+    auto kern = fp8_gemm_kernel<WGRAD, true, false, OUT>;
+    for (auto other : {fp8_gemm_kernel<WGRAD, false, false, OUT>, fp8_gemm_kernel<WGRAD, false, true, OUT>}) {
+      err = cudaFuncSetAttribute(other, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)f8_smem(FP8_MAX_E));
+      if (err != cudaSuccess) return err;
+    }
     err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)f8_smem(FP8_MAX_E));
     for (int i = 2; i >= 0 && err == cudaSuccess; --i) {  // the first entry last: it says that the others are there
       cudaLaunchConfig_t cfg{};
@@ -753,7 +762,9 @@ int64_t f8_plan(Fp8GemmArgs& g, int n_sm, int64_t nkb, int64_t groups, int64_t e
 template <bool WGRAD, typename OUT>
 cudaError_t launch(const CUtensorMap& ta, const CUtensorMap (&tb)[3], const Fp8GemmArgs& args, int64_t tiles, int n_sm,
                    cudaStream_t st) {
-  auto kern = args.splits > 1 ? fp8_gemm_kernel<WGRAD, true, OUT> : fp8_gemm_kernel<WGRAD, false, OUT>;
+  auto kern = args.splits > 1 ? fp8_gemm_kernel<WGRAD, true, false, OUT>
+              : args.packed   ? fp8_gemm_kernel<WGRAD, false, true, OUT>
+                              : fp8_gemm_kernel<WGRAD, false, false, OUT>;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -797,6 +808,9 @@ cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, bool bf16_out, int n_sm, c
   if (a.E > 1) tiles = ((a.R + g.nmax - 1) / g.nmax + a.E) * g.MT;  // at most, whatever the groups' sizes
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
   g.magic_per = f8_magic(g.MT);
+  // 8,192 x 8,192 x 8,192 564 -> 541 us with two sums an instruction, but 16,384 rows of 128 groups 713 -> 732 (the narrower
+  // tiles' loop loses registers to the pairs)
+  g.packed = a.R >= 192 * groups;
   CUtensorMap ta, tb[3];
   if (!tmap_a(&ta, a.w, a.K, a.N, a.E, a.w_stride, g.mixed) ||
       !tmap_boxes(tb, a.x, a.K, a.R, a.x_stride))
@@ -829,6 +843,9 @@ cudaError_t launch_fp8_weight_grad(const Fp8WeightGradArgs& a, bool bf16_out, in
   const int64_t nc = (a.N + g.nmax - 1) / g.nmax;
   g.magic_per = f8_magic(nc * g.MT);
   g.magic_nc = f8_magic(nc);
+  // 1,024 rows a group 1,399 -> 1,301 us with two sums an instruction, but 128 rows (one block) 720 -> 793: the sums' pairs cost
+  // the stores moves
+  g.packed = a.R >= 384 * (int64_t)a.E;
   CUtensorMap ta, tb[3];
   const int64_t P = 128 * g.blocks;
   if (!tmap_a(&ta, a.x, P, a.H, 1, a.x_stride, g.mixed) ||
