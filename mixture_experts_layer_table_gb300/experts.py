@@ -430,11 +430,11 @@ def fp8_weight_grad(dy: torch.Tensor, dy_scale: torch.Tensor, x: torch.Tensor, x
                     device_status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """dW = dy^T x over each group's rows (mok_fp8_weight_grad): dy [N][P] and x [H][P] with their scales ("qt" and
     "qt_scale" of ``fp8_quantize`` with the same offsets) -> [E][N][H], f32 or bf16; zeros for a group without rows."""
-    for t, name in ((dy, "dy"), (x, "x"), (offsets, "offsets")):
-        if not isinstance(t, torch.Tensor) or t.dim() != (1 if name == "offsets" else 2):
-            raise ValueError(f"{name}: expected a {'vector' if name == 'offsets' else 'matrix'}")
-    device = _device(dy, "dy")
-    (N, columns), H, E = dy.shape, x.shape[0], offsets.shape[0] - 1
+    try:
+        (N, columns), (H, _), (E,) = dy.shape, x.shape, offsets.shape
+    except (AttributeError, ValueError):
+        raise ValueError("dy and x: expected matrices; offsets: expected a vector") from None
+    device, E = _device(dy, "dy"), E - 1
     if E < 1 or columns % 128 or columns < 128 * E:
         raise ValueError(f"dy: expected 128 (R / 128 + E) columns, got {columns} with {E} groups")
     if out is None:

@@ -487,6 +487,68 @@ def test_bad_offsets_stay_in_the_tensors():
     torch.cuda.synchronize()
 
 
+def test_as_many_groups_as_there_may_be():
+    rng = np.random.default_rng(12)
+    E, N, K = 1024, 40, 150
+    counts = rng.integers(0, 4, E)
+    counts[[3, 500, 1023]] = 130, 0, 77
+    offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    R = int(offsets[-1])
+    x, _ = values(rng, (R, K), BF)
+    dy, _ = values(rng, (R, N), BF)
+    w = mok.Fp8Weights(values(rng, (E, N, K), BF)[0])
+    q, d = mok.fp8_quantize(x, offsets=cuda(offsets)), mok.fp8_quantize(dy, offsets=cuda(offsets), rows=False)
+    got = w.matmul(q["q"], q["scale"], cuda(offsets), dtype=F32)
+    want, size = O.product(f64(q["q"]), f64(q["scale"]), f64(w.q), f64(w.scale), offsets)
+    check_product(f64(got), want, size, K, F32)
+    got = mok.fp8_weight_grad(d["qt"], d["qt_scale"], q["qt"], q["qt_scale"], cuda(offsets))
+    want, size = O.weight_grad(f64(d["qt"]), f64(d["qt_scale"]), f64(q["qt"]), f64(q["qt_scale"]), offsets)
+    check_product(f64(got), want, size, int(counts.max()), F32)
+    with pytest.raises(mok.MokError):
+        mok.Fp8Weights.empty(1025, 16, 16).matmul(mok.empty_e4m3(1, 16), torch.zeros(1, 1).cuda(),
+                                                  torch.zeros(1026, dtype=torch.int32).cuda())
+
+
+@pytest.mark.slow
+def test_elements_behind_the_reach_of_32_bits():
+    """Tensors of more than 2^31 elements: the last rows against calls on those rows alone."""
+    R, H, tail = 540_000, 4096, 300
+    x = torch.empty(R, H, dtype=BF, device="cuda").normal_()
+    back = torch.arange(R - 1, -1, -1, dtype=torch.int32, device="cuda")
+    g = mok.gather_rows(x, back, 1)
+    assert torch.equal(g[-5:], x[:5].flip(0)) and torch.equal(g[:5], x[-5:].flip(0))
+    gates = torch.rand(R, 1, device="cuda")
+    y = mok.merge_rows(g, back, 1, gates)
+    assert torch.equal(y[-tail:], (x[-tail:].float() * gates[-tail:]).bfloat16())
+    out = mok.merge_rows_backward(x, g, back, gates)
+    assert torch.equal(out["do"][:tail], (x[-tail:].float() * gates[-tail:]).bfloat16().flip(0))
+    dots = (x[-tail:].double() ** 2).sum(1)
+    assert ((out["dgates"][-tail:, 0].double() - dots).abs() <= (H / 32 + 29) * U * dots).all()
+    del g, y, out
+    first = R - tail
+    offsets = torch.tensor([0, 100, first, R], dtype=torch.int32, device="cuda")
+    q = mok.fp8_quantize(x, offsets=offsets)
+    alone = mok.fp8_quantize(x[-tail:], offsets=torch.tensor([0, tail], dtype=torch.int32, device="cuda"))
+    assert torch.equal(q["q"][-tail:].view(torch.uint8), alone["q"].view(torch.uint8))
+    assert torch.equal(q["scale"][:, -tail:], alone["scale"])
+    block = 1 + -(-(first - 100) // 128)
+    assert torch.equal(q["qt"][:, 128 * block:128 * (block + 3)].view(torch.uint8), alone["qt"][:, :384].view(torch.uint8))
+    assert torch.equal(q["qt_scale"][block:block + 3], alone["qt_scale"][:3])
+    del x
+    w = mok.Fp8Weights(torch.randn(3, H, 256, device="cuda"))
+    few = {n: (t[:, :256] if n == "q" else t[:2]) for n, t in q.items() if n in ("q", "scale")}
+    out = w.matmul(few["q"], few["scale"], offsets)
+    want, size = O.product(f64(few["q"][-tail:]), f64(few["scale"][:, -tail:]), f64(w.q[2:]), f64(w.scale[2:]), [0, tail])
+    check_product(f64(out[-tail:]), want, size, 256, BF)
+    del out
+    E = 140
+    some = (torch.arange(E + 1, device="cuda") * 3).int()
+    a = mok.fp8_quantize(torch.randn(3 * E, H, device="cuda"), offsets=some, rows=False)
+    out = mok.fp8_weight_grad(a["qt"], a["qt_scale"], a["qt"], a["qt_scale"], some, dtype=BF)
+    p = f64(a["qt"][:, 128 * (E - 1):128 * E]) * f64(a["qt_scale"][E - 1])[:, None]
+    check_product(f64(out[-1]), p @ p.T, np.abs(p) @ np.abs(p).T, 3, BF)
+
+
 def test_an_experts_training_step_together():
     """Both products, their gradients and the way of the rows, each against the oracle on the operands that the call
     before it made, the last ones against the unquantised layer too."""
