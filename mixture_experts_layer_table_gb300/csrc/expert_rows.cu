@@ -10,6 +10,7 @@
 #include <algorithm>
 
 #include "expert_rows.cuh"
+#include "ptx.cuh"
 #include "status.cuh"
 
 namespace mok {
@@ -35,6 +36,14 @@ __device__ __forceinline__ void load_raw(uint4& v, const void* p) {
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
 }
+// The same for a line that is read again soon: a token's row is read by its k experts, far apart in time.
+__device__ __forceinline__ void load_keep(uint4& v, const void* p, uint64_t policy) {
+  asm volatile("ld.global.nc.L1::no_allocate.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p), "l"(policy));
+}
+template <typename W>
+__device__ __forceinline__ void load_keep(W& v, const void* p, uint64_t) { v = __ldg(static_cast<const W*>(p)); }
 __device__ __forceinline__ void load_raw(uint32_t& v, const void* p) { v = __ldg(static_cast<const uint32_t*>(p)); }
 __device__ __forceinline__ void load_raw(uint16_t& v, const void* p) {
   v = __ldg(static_cast<const unsigned short*>(p));
@@ -72,40 +81,54 @@ __device__ __forceinline__ int64_t checked(int32_t i, int64_t n, int* status, in
   return -1;
 }
 
-// blockDim.x threads to a row, blockDim.y rows to a block; V pieces of a thread in flight at once.  Short-lived
-// blocks in row order, as the layer's own gather (rows.cu) found best.
-template <typename T, int BYTES, int V>
+// V pieces of a row, X apart, from piece i on: all loaded, then all stored.  ALL: they are all there.
+template <typename T, int BYTES, int V, int X, bool ALL, typename W>
+__device__ __forceinline__ void copy_pieces(const char* s, char* d, int i, int pieces, bool gated, float g, const W*) {
+  const uint64_t keep = BYTES == 16 ? l2_policy_evict_last() : 0;
+  W v[V] = {};
+  s += (int64_t)i * BYTES;
+  d += (int64_t)i * BYTES;
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+    if (ALL || i + j * X < pieces) load_keep(v[j], s + j * X * BYTES, keep);
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+    if (ALL || i + j * X < pieces) {
+      if (gated) {
+        float f[Piece<T, BYTES>::N];
+        unpack<T, BYTES>(v[j], f);
+#pragma unroll
+        for (int q = 0; q < Piece<T, BYTES>::N; ++q) f[q] *= g;
+        pack<T, BYTES>(v[j], f);
+      }
+      store_raw(d + j * X * BYTES, v[j]);
+    }
+}
+
+// X threads to a row, 128 / X rows to a block, 8 pieces of a thread in flight at once.  Short-lived blocks in row order, as
+// the layer's own gather (rows.cu) found best, and the tokens' lines kept in L2 (32,768 rows of 7,168 bf16 133 -> 102 us,
+// 5.2 TB/s; 524,288 rows of 64 bf16, 16 of them a block instead of 4, 131 -> 37).
+template <typename T, int BYTES, int X>
 __global__ void __launch_bounds__(128) expert_gather_kernel(const RowsArgs a, int pieces) {
   using W = typename Raw<T, BYTES>::type;
-  const int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  const W* kind = nullptr;
+  const int64_t r = (int64_t)blockIdx.x * (128 / X) + threadIdx.y;
   if (r >= a.R) return;
   const int64_t src = checked(a.index[r], a.T * a.k, a.status, SITE_ROWS_GATHER);
-  const float g = a.gates != nullptr && src >= 0 ? a.gates[src] : 1.0f;
-  const char* s = static_cast<const char*>(a.tokens) + (src < 0 ? 0 : src / a.k) * a.token_stride * (int64_t)sizeof(T);
   char* d = static_cast<char*>(a.out) + r * a.row_stride * (int64_t)sizeof(T);
-  for (int base = threadIdx.x; base < pieces; base += blockDim.x * V) {
-    W v[V] = {};
-    if (src >= 0) {
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int i = base + j * blockDim.x;
-        if (i < pieces) load_raw(v[j], s + (int64_t)i * BYTES);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int i = base + j * blockDim.x;
-      if (i < pieces) {
-        if (a.gates != nullptr && src >= 0) {
-          float f[Piece<T, BYTES>::N];
-          unpack<T, BYTES>(v[j], f);
-#pragma unroll
-          for (int q = 0; q < Piece<T, BYTES>::N; ++q) f[q] *= g;
-          pack<T, BYTES>(v[j], f);
-        }
-        store_raw(d + (int64_t)i * BYTES, v[j]);
-      }
-    }
+  int i = threadIdx.x;
+  if (src < 0) {
+    for (; i < pieces; i += X) store_raw(d + (int64_t)i * BYTES, W{});
+    return;
+  }
+  const bool gated = a.gates != nullptr;
+  const float g = gated ? a.gates[src] : 1.0f;
+  const char* s = static_cast<const char*>(a.tokens) + (int64_t)((int)src / a.k) * a.token_stride * (int64_t)sizeof(T);
+  for (; i + 7 * X < pieces; i += 8 * X) copy_pieces<T, BYTES, 8, X, true>(s, d, i, pieces, gated, g, kind);
+  if (i + 2 * X < pieces) {
+    copy_pieces<T, BYTES, 8, X, false>(s, d, i, pieces, gated, g, kind);
+  } else if (i < pieces) {
+    copy_pieces<T, BYTES, 2, X, false>(s, d, i, pieces, gated, g, kind);
   }
 }
 
@@ -144,6 +167,48 @@ __global__ void __launch_bounds__(128) expert_merge_kernel(const RowsArgs a, int
   W o;
   pack<T, BYTES>(o, acc);
   store_raw(static_cast<char*>(a.out) + t * a.token_stride * (int64_t)sizeof(T) + (int64_t)i * BYTES, o);
+}
+
+// The same for pieces of one element, which instructions bound: a block takes one token, whose rows are found once for all
+// of its pieces (4,096 tokens of 8 rows of 7,167: f32 305 -> 201 us, bf16 301 -> 274; two bf16 a piece 158 -> 172, so
+// those stay with the other).
+template <typename T, int BYTES, int KMAX>
+__global__ void __launch_bounds__(128) expert_merge_token_kernel(const RowsArgs a, int pieces) {
+  using W = typename Raw<T, BYTES>::type;
+  const int64_t t = blockIdx.x;
+  const char* row[KMAX];
+  float g[KMAX];
+#pragma unroll
+  for (int j = 0; j < KMAX; ++j) {
+    row[j] = nullptr;
+    g[j] = 0.0f;
+    if (j < a.k) {
+      const int64_t r = checked(a.index[t * a.k + j], a.R, a.status, SITE_ROWS_MERGE);
+      if (r >= 0) {
+        g[j] = a.gates != nullptr ? a.gates[t * a.k + j] : 1.0f;
+        row[j] = static_cast<const char*>(a.rows) + r * a.row_stride * (int64_t)sizeof(T);
+      }
+    }
+  }
+  char* out = static_cast<char*>(a.out) + t * a.token_stride * (int64_t)sizeof(T);
+  for (int i = threadIdx.x; i < pieces; i += blockDim.x) {
+    W v[KMAX];
+#pragma unroll
+    for (int j = 0; j < KMAX; ++j)
+      if (row[j] != nullptr) load_raw(v[j], row[j] + (int64_t)i * BYTES);
+    float acc[Piece<T, BYTES>::N] = {};
+#pragma unroll
+    for (int j = 0; j < KMAX; ++j)
+      if (row[j] != nullptr) {
+        float f[Piece<T, BYTES>::N];
+        unpack<T, BYTES>(v[j], f);
+#pragma unroll
+        for (int q = 0; q < Piece<T, BYTES>::N; ++q) acc[q] = fmaf(g[j], f[q], acc[q]);
+      }
+    W o;
+    pack<T, BYTES>(o, acc);
+    store_raw(out + (int64_t)i * BYTES, o);
+  }
 }
 
 // One token to a block: dy is read once and meets the token's rows four at a time.  The dot products are added
@@ -221,18 +286,30 @@ int piece_bytes(const RowsArgs& a, int item) {
 template <typename T, int BYTES>
 cudaError_t gather(const RowsArgs& a, cudaStream_t st) {
   const int pieces = (int)(a.H * (int64_t)sizeof(T) / BYTES);
-  // narrow rows share a block
-  const int x = pieces <= 32 ? 32 : pieces <= 64 ? 64 : 128;
+  // narrow rows share a block: as many threads as the row has pieces, up to a power of two
+  int x = 8;
+  while (x < 128 && x < pieces) x *= 2;
   const dim3 block(x, 128 / x);
   const int64_t blocks = (a.R + block.y - 1) / block.y;
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  expert_gather_kernel<T, BYTES, 8><<<(unsigned)blocks, block, 0, st>>>(a, pieces);
+  switch (x) {
+    case 8: expert_gather_kernel<T, BYTES, 8><<<(unsigned)blocks, block, 0, st>>>(a, pieces); break;
+    case 16: expert_gather_kernel<T, BYTES, 16><<<(unsigned)blocks, block, 0, st>>>(a, pieces); break;
+    case 32: expert_gather_kernel<T, BYTES, 32><<<(unsigned)blocks, block, 0, st>>>(a, pieces); break;
+    case 64: expert_gather_kernel<T, BYTES, 64><<<(unsigned)blocks, block, 0, st>>>(a, pieces); break;
+    default: expert_gather_kernel<T, BYTES, 128><<<(unsigned)blocks, block, 0, st>>>(a, pieces); break;
+  }
   return cudaGetLastError();
 }
 
 template <typename T, int BYTES, int KMAX>
 cudaError_t merge_k(const RowsArgs& a, cudaStream_t st) {
   const int pieces = (int)(a.H * (int64_t)sizeof(T) / BYTES);
+  if (BYTES == (int)sizeof(T) && pieces >= 96 && a.T >= 512) {  // rows long enough and tokens enough to fill the SMs a block each
+    if (a.T > INT32_MAX) return cudaErrorInvalidValue;
+    expert_merge_token_kernel<T, BYTES, KMAX><<<(unsigned)a.T, 128, 0, st>>>(a, pieces);
+    return cudaGetLastError();
+  }
   const int64_t blocks = (a.T * pieces + 127) / 128;
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
   expert_merge_kernel<T, BYTES, KMAX><<<(unsigned)blocks, 128, 0, st>>>(a, pieces);

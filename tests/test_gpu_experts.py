@@ -68,7 +68,7 @@ def table(rng, T, k, E, dropped=0.0, skew=0.0):
 
 # (T, k, E, H): one of everything, narrow and odd rows, pieces of 2, 4 and 16 bytes, k of every kernel, wide rows
 ROWS = [(1, 1, 1, 1), (3, 2, 5, 7), (50, 3, 8, 36), (33, 4, 16, 126), (20, 6, 48, 1111), (9, 8, 16, 4096),
-        (5, 16, 16, 264), (200, 1, 2, 40), (2, 12, 20, 9000), (330, 2, 8, 520)]
+        (5, 16, 16, 264), (200, 1, 2, 40), (2, 12, 20, 9000), (330, 2, 8, 520), (600, 3, 8, 101), (520, 2, 4, 402)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
