@@ -502,7 +502,8 @@ mok_status mok_adamw_step(const mok_adamw_tensor* tensors, int32_t count, const 
 /* ------------------------------------------------------------------ experts outside the layer
  * For experts that are not the layer's (another FFN, weights in 8 bits with a scale for each 128 x 128, a shared
  * expert): the layer's table (mok_schedule) moves the rows, and the products run on E4M3 operands.  The pages have
- * no counterpart: their experts are SwiGLU FFNs in BF16 or MXFP8.
+ * no counterpart: their experts are SwiGLU FFNs in BF16 or MXFP8.  Rows, and assignments, stay below 2^31, widths below
+ * 2^28, groups are at most 1024 (MOK_ERR_UNSUPPORTED).  No call has a workspace: calls may overlap.
  *
  * Rows by a table.
  *   T  tokens, R  rows of the sorted order (mok_schedule: T k; fewer or more where assignments are dropped or rows

@@ -2,29 +2,35 @@
 // mok_fp8_weight_grad):
 //   product       out[r][n] = sum_b xs[b][r] ws[e][n / 128][b] (x_b w_b^T)[r][n]     over the rows r of group e
 //   weight grad   out[e][n][h] = sum_b ds[b][n] xs[b][h] (dy_b x_b^T)[n][h]        over the 128-row blocks b of group e
-// Both are out[col][lane] = sum_b s_b (A_b B_b^T) with A's rows the MMA's M (256 a pair tile, 128 a CTA: weights' rows, or
-// h) and B's rows its N (a multiple of 16 up to 256: the group's rows, or n), so that a group of few rows pads to 16
-// only and a warp's 32 lanes store 32 consecutive elements of out.
+// Both are out[col][row] = sum_b s_b (A_b B_b^T) with A's rows the MMA's M (256 a pair tile, 128 a CTA: weights' rows, or
+// h) and B's rows its N (a multiple of 16 up to 256: the group's rows, or n), so that a group of few rows pads to 16 only.
 //
 // The scales are arbitrary f32 numbers and change with each 128 of K, so a block's sum cannot stay in the tensor
-// cores: tcgen05.mma.kind::f8f6f4 forms it (four K = 32 steps) in one of two TMEM accumulators, and the epilogue warps
-// add it, scaled, to their f32 sums in registers while the next block's MMAs run into the other.  For 256 columns that
-// is 64 packed FMAs, 4 TMEM loads and 32 broadcast shared loads of a warp for each block, against 512 cycles of MMAs.
+// cores: tcgen05.mma.kind::f8f6f4 forms it (four K = 32 steps) in one of two TMEM accumulators of 256 columns, and eight epilogue
+// warps add it, scaled, to their f32 sums in registers (128 a thread) while the next block's MMAs run into the other.  They
+// read TMEM as 16 lanes x 256 bits: a lane then has two columns of each 8, so that it needs a quarter of the columns' scales, and
+// four rows of each column.  With A's rows mixed on the way into shared memory (a five-dimensional tensor map: TMEM lane
+// 8 k + u holds row 4 u + k) these four are neighbours in out, stored together.  Tiles of at most 128 (64) columns put two
+// (four) blocks into an accumulator and hand them over together.
+// What bounds it: few rows a group, DRAM (32 rows on 25 of 64 experts of 7,168 x 2,048 64 us, 5.7 TB/s; 16,384 rows of 128
+// experts of 4,096 x 7,168 720 us, 5.5 TB/s).  Many, the epilogue: a block of 256 columns takes its warps about 1,150 cycles
+// against 520 of MMAs (8,192^3 539 us, 2.04 PFLOP/s; the MMAs alone 246 us, with their loads 338).
 //
-// Roles of both CTAs of a pair: warp 0 TMA producer, warp 1 MMA issuer (even CTA, one thread), warp 2 the scales, warps 4
-// to 11 epilogue (warp w reads TMEM lane quarter w % 4; the two warps of a quarter take alternate 32-column pieces).  The
-// scales' warp reads four blocks' scales at a time, multiplies the two where one is the same for a whole 128-row
-// tile (product) and puts them into a ring in shared memory.  Barriers: full[s] in the even CTA (one arrival with
-// both CTAs' bytes), empty[s] and pfull[a] in both (multicast commits), pempty[a] in the even CTA (16 arrivals),
-// sfull[q] and sempty[q] in each CTA.  Tiles (group, weight tile m, chunk c of the group's rows; c fastest, then m)
-// are dealt to the pairs round-robin; every output element is one tile's sum over its blocks in order, so results do not
-// depend on the deal.  Every wait is bounded.
+// Roles of both CTAs of a pair: warp 0 TMA producer, warp 1 MMA issuer (even CTA), warp 2 the scales, warps 4 to 11 epilogue
+// (warp w reads TMEM lane quarter w % 4; the two warps of a quarter take alternate 32-column pieces).  The scales' warp
+// reads four blocks' scales at a time, multiplies the two where one is the same for a whole 128-row tile (product) and puts
+// them into a ring in shared memory, in the order in which the epilogue's lanes take them.  All waits and loops are a whole
+// warp's, one elected thread issues: addresses and descriptors then stay in uniform registers.  Barriers: full[s] in the even
+// CTA (one arrival with both CTAs' bytes), empty[s] and pfull[a] in both (multicast commits), pempty[a] in the even CTA (16
+// arrivals), sfull[q] and sempty[q] in each CTA.  Tiles (group, weight tile m, chunk c of the group's rows; c fastest, then
+// m) are dealt to the pairs round-robin; where there are few, up to four pairs of a cluster share a tile along K and add
+// their sums in order.  Every output element is summed over its blocks in order, so results do not depend on the deal.
+// Every wait is bounded.
 #include <cuda_bf16.h>
 
 #include <algorithm>
 #include <type_traits>
 
-#include "f32x2.cuh"
 #include "fp8.cuh"
 #include "ptx.cuh"
 #include "tmap.cuh"
