@@ -540,7 +540,7 @@ mok_status mok_merge_rows_backward(const mok_rows_desc* desc, const void* dy, co
  * of E4M3 elements start at multiples of 16 bytes.
  *   R  rows, C  width of the quantised rows;  x_stride, grad_stride  elements between rows (0 = packed)
  *   source   MOK_FP8_PLAIN: x [R][C]; with src_of, rows gates[a] x[a / k] of x [T][C] as in mok_gather_rows
- *            (gates may be NULL)
+ *            (gates may be NULL; an index out of range is reported in device_status)
  *            MOK_FP8_SWIGLU: x [R][2C] = h | u; quantised is silu(h) u
  *            MOK_FP8_SWIGLU_GRAD: x [R][C] = h | u, grad [R][C/2] = da; quantised is the gradient dh | du [R][C] of
  *            a = silu(h) u

@@ -121,6 +121,7 @@ mok_status mok_fp8_quantize(const mok_fp8_quantize_desc* d, const void* x, const
   if ((d->source == MOK_FP8_SWIGLU_GRAD) != (grad != nullptr)) return MOK_ERR_INVALID_ARG;
   if (d->source == MOK_FP8_SWIGLU_GRAD && d->C % 2 != 0) return MOK_ERR_INVALID_ARG;
   if (gathered && d->k < 1) return MOK_ERR_INVALID_ARG;
+  if (d->R == 0) return MOK_OK;  // nothing to read or write: no pointer is looked at
   if ((q == nullptr) != (scale == nullptr) || (qt == nullptr) != (qt_scale == nullptr)) return MOK_ERR_INVALID_ARG;
   if (q == nullptr && qt == nullptr) return MOK_ERR_INVALID_ARG;
   if (qt != nullptr && (offsets == nullptr || d->E < 1)) return MOK_ERR_INVALID_ARG;
@@ -135,7 +136,6 @@ mok_status mok_fp8_quantize(const mok_fp8_quantize_desc* d, const void* x, const
   if (d->R >= kMaxRows - 128 || d->C >= kMaxWidth || (qt != nullptr && d->E > mok::FP8_MAX_E) ||
       (gathered && (d->k > mok::ROWS_MAX_K || d->T >= kMaxRows / d->k)))
     return MOK_ERR_UNSUPPORTED;
-  if (d->R == 0) return MOK_OK;
   if (x == nullptr && !(gathered && d->T == 0)) return MOK_ERR_INVALID_ARG;
   mok::Fp8QuantizeArgs a = {};
   a.R = d->R;

@@ -78,7 +78,7 @@ def quantize(d, **kw):
     ({}, dict(qt=None), 1), ({}, dict(qt_scale=None), 1), ({}, dict(q=None, scale=None, qt=None, qt_scale=None), 1),
     ({}, dict(offsets=None), 1), ({}, dict(x=None), 1), ({}, dict(x=0x100001), 1), ({}, dict(q=0x100008), 1),
     ({}, dict(qt=0x100004), 1), ({}, dict(scale=0x100002), 1), ({}, dict(offsets=0x100001), 1), ({}, dict(status=0x100002), 1),
-    (dict(R=0, T=0), {}, 0)])
+    (dict(R=0, T=0), {}, 0), (dict(R=0), dict(x=None, q=None, scale=None, qt=None, qt_scale=None), 0)])
 def test_quantize_refuses(lib, d, kw, code):
     assert quantize(d, **kw) == code
 

@@ -156,6 +156,14 @@ def test_empty_tables():
     assert (mok.merge_rows(x, drop, 2) == 0).all()
     out = mok.merge_rows_backward(torch.ones(3, 16).cuda(), x, drop, torch.ones(3, 2).cuda())
     assert (out["dgates"] == 0).all()
+    # no rows at all, with and without groups, through every call of an expert
+    off = torch.zeros(4, dtype=torch.int32).cuda()
+    w = mok.Fp8Weights(torch.ones(3, 8, 16).cuda(), transposed=True)
+    q = mok.fp8_quantize(x, src_of=none, k=2, offsets=off)
+    h = mok.fp8_quantize(w.matmul(q["q"], q["scale"], off), source="swiglu", offsets=off)
+    assert h["q"].shape == (0, 4) and w.matmul_transposed(mok.fp8_quantize(torch.ones(0, 8).cuda())["q"],
+                                                          torch.ones(1, 0).cuda(), off).shape == (0, 16)
+    assert (mok.fp8_weight_grad(h["qt"], h["qt_scale"], q["qt"], q["qt_scale"], off) == 0).all()
     # rows without tokens
     assert (mok.gather_rows(x, drop, 2) == 0).all()
     q = mok.fp8_quantize(x, src_of=drop, k=2)
