@@ -210,19 +210,22 @@ __device__ __forceinline__ Row8 source8(const Fp8QuantizeArgs& a, const Source<T
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        float v[2];
+        float h[2], d[2], u[2];
+        bool up[2];
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
-          const int64_t col = c + 2 * j + z, i = col >= I ? col - I : col;
-          v[z] = 0.0f;
-          if (col < a.C) {
-            const float hh = widen(s.x[i]), dd = widen(s.grad[i]);
-            float sg, other;
-            split(sigmoid2(f2(hh)), sg, other);
-            v[z] = col >= I ? dd * hh * sg : dd * widen(s.x[I + i]) * sg * fmaf(hh, 1.0f - sg, 1.0f);
-          }
+          const int64_t col = c + 2 * j + z;
+          const bool in = col < a.C;
+          up[z] = col >= I;
+          const int64_t i = up[z] ? col - I : col;
+          h[z] = in ? widen(s.x[i]) : 0.0f;
+          d[z] = in ? widen(s.grad[i]) : 0.0f;
+          u[z] = in && !up[z] ? widen(s.x[I + i]) : 0.0f;
         }
-        o.v[j] = f2(v[0], v[1]);
+        const F2 hh = f2(h[0], h[1]), dd = f2(d[0], d[1]), sg = sigmoid2(hh);
+        const F2 du = mul2(mul2(dd, hh), sg);
+        const F2 dh = mul2(mul2(mul2(dd, f2(u[0], u[1])), sg), add2(mul2(hh, fma2(sg, f2(-1.0f), f2(1.0f))), f2(1.0f)));
+        o.v[j] = f2(up[0] ? du.x : dh.x, up[1] ? du.y : dh.y);
       }
     }
   }
