@@ -287,14 +287,24 @@ __device__ __forceinline__ void store_tile(const uint32_t* tile, uint8_t* qt, in
 }
 
 // The largest finite magnitude of each of a half-warp's rows (of the warp's lanes, infinities have become NaN).
-template <int RPT>
-__device__ __forceinline__ void row_maxima(const Row8 (&v)[RPT], float (&m)[RPT]) {
+__device__ __forceinline__ void row_maxima(const Row8 (&v)[1], float (&m)[1]) {
+  m[0] = largest8(v[0]);
 #pragma unroll
-  for (int i = 0; i < RPT; ++i) {
-    m[i] = largest8(v[i]);
+  for (int s = 8; s > 0; s >>= 1) m[0] = fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], s));
+}
+// Of four rows: each exchange halves the rows that a lane reduces (9 shuffles, not 16).
+__device__ __forceinline__ void row_maxima(const Row8 (&v)[4], float (&m)[4]) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int s = 8; s > 0; s >>= 1) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], s));
-  }
+  for (int i = 0; i < 4; ++i) m[i] = largest8(v[i]);
+  const bool hi = lane & 8, odd = lane & 4;
+  const float x = fmaxf(hi ? m[2] : m[0], __shfl_xor_sync(0xffffffffu, hi ? m[0] : m[2], 8));
+  const float y = fmaxf(hi ? m[3] : m[1], __shfl_xor_sync(0xffffffffu, hi ? m[1] : m[3], 8));
+  float z = fmaxf(odd ? y : x, __shfl_xor_sync(0xffffffffu, odd ? x : y, 4));
+  z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 2));
+  z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 1));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m[i] = __shfl_sync(0xffffffffu, z, (lane & 16) | 4 * i);
 }
 template <int RPT>
 __device__ __forceinline__ void finite_or_nan(Row8 (&v)[RPT]) {
@@ -305,36 +315,6 @@ __device__ __forceinline__ void finite_or_nan(Row8 (&v)[RPT]) {
 #pragma unroll
     for (int i = 0; i < RPT; ++i) infinities_to_nan(v[i]);
   }
-}
-
-// ------------------------------------------------------------------ rows
-// Tiles of 16 RPT rows along the rows only.
-template <int SRC, typename T, bool VEC, int RPT>
-__global__ void __launch_bounds__(THREADS) fp8_rows_kernel(const Fp8QuantizeArgs a, int col_blocks) {
-  __shared__ float s_scale[16 * RPT];
-  const int b = blockIdx.x % col_blocks;
-  const int64_t r0 = (int64_t)(blockIdx.x / col_blocks) * (16 * RPT);
-  const int w = threadIdx.x >> 4, l = threadIdx.x & 15;
-  const int64_t c = (int64_t)b * FP8_BLOCK + 8 * l;
-  Row8 v[RPT];
-#pragma unroll
-  for (int i = 0; i < RPT; ++i) {
-    const int64_t r = r0 + w * RPT + i;
-    v[i] = r < a.R ? source8<SRC, T, VEC>(a, source_row<SRC, T>(a, r), c) : zero8();
-  }
-  float m[RPT];
-  finite_or_nan(v);
-  row_maxima(v, m);
-#pragma unroll
-  for (int i = 0; i < RPT; ++i) {
-    const int64_t r = r0 + w * RPT + i;
-    const uint2 bytes = quantize8(v[i], divisor(m[i]));
-    if (r < a.R && c < a.C) store8(a.q + r * a.q_stride + c, bytes, a.C - c);
-    if (l == 0) s_scale[w * RPT + i] = block_scale(m[i]);
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 16 * RPT; i += THREADS)
-    if (r0 + i < a.R) a.scale[b * a.scale_stride + r0 + i] = s_scale[i];
 }
 
 // A row's eight columns as they are kept until the scales are known: bf16 rows in their own four words (half the
@@ -386,49 +366,100 @@ __device__ __forceinline__ float kept_largest(const RawRow8 (&v)[4]) {
 }
 
 // Infinities become NaN.  Returns whether an element of the warp's rows is not finite: its magnitude is then left out below.
-__device__ __forceinline__ bool only_finite_or_nan(Row8 (&v)[4]) {
+template <int RPT>
+__device__ __forceinline__ bool only_finite_or_nan(Row8 (&v)[RPT]) {
   finite_or_nan(v);
   return false;  // maxima leave NaN out by themselves
 }
-__device__ __forceinline__ bool only_finite_or_nan(RawRow8 (&v)[4]) {
+template <int RPT>
+__device__ __forceinline__ bool only_finite_or_nan(RawRow8 (&v)[RPT]) {
   const bool odd = __any_sync(0xffffffffu, !(kept_largest(v) <= BIG));
   if (odd) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < RPT; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[i].w[j] |= __vcmpgeu2(v[i].w[j] & 0x7fff7fffu, 0x7f807f80u) & 0x7fff7fffu;
   }
   return odd;
 }
-// The largest magnitudes of columns 2 j and 2 j + 1 of the four rows.
-__device__ __forceinline__ float2 two_columns(const Row8 (&v)[4], int j, bool) {
+template <bool ODD>
+__device__ __forceinline__ uint32_t magnitudes(uint32_t w) {
+  w &= 0x7fff7fffu;
+  return ODD ? w & __vcmpltu2(w, 0x7f807f80u) : w;
+}
+// The largest magnitudes of columns 2 j and 2 j + 1 of the warp's rows.
+template <bool ODD>
+__device__ __forceinline__ float2 two_columns(const Row8 (&v)[4], int j) {
   float2 t = make_float2(0.0f, 0.0f);
 #pragma unroll
   for (int i = 0; i < 4; ++i) t = make_float2(fmaxf(t.x, fabsf(v[i].v[j].x)), fmaxf(t.y, fabsf(v[i].v[j].y)));
   return make_float2(fmaxf(t.x, __shfl_xor_sync(0xffffffffu, t.x, 16)), fmaxf(t.y, __shfl_xor_sync(0xffffffffu, t.y, 16)));
 }
-__device__ __forceinline__ uint32_t magnitudes(uint32_t w, bool odd) {
-  w &= 0x7fff7fffu;
-  return odd ? w & __vcmpltu2(w, 0x7f807f80u) : w;
-}
-__device__ __forceinline__ float2 two_columns(const RawRow8 (&v)[4], int j, bool odd) {
+template <bool ODD>
+__device__ __forceinline__ float2 two_columns(const RawRow8 (&v)[4], int j) {
   uint32_t t = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) t = __vmaxu2(t, magnitudes(v[i].w[j], odd));
+  for (int i = 0; i < 4; ++i) t = __vmaxu2(t, magnitudes<ODD>(v[i].w[j]));
   t = __vmaxu2(t, __shfl_xor_sync(0xffffffffu, t, 16));
   return make_float2(__uint_as_float(t << 16), __uint_as_float(t & 0xffff0000u));
 }
-__device__ __forceinline__ void kept_row_maxima(const Row8 (&v)[4], float (&m)[4], bool) { row_maxima(v, m); }
-__device__ __forceinline__ void kept_row_maxima(const RawRow8 (&v)[4], float (&m)[4], bool odd) {
+template <bool ODD, int RPT>
+__device__ __forceinline__ void kept_row_maxima(const Row8 (&v)[RPT], float (&m)[RPT]) { row_maxima(v, m); }
+// Two rows' maxima in a word: 5 shuffles for four rows.
+template <bool ODD>
+__device__ __forceinline__ void kept_row_maxima(const RawRow8 (&v)[4], float (&m)[4]) {
+  uint32_t t[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint32_t t = 0;
+    t[i] = magnitudes<ODD>(v[i].w[0]);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) t = __vmaxu2(t, magnitudes(v[i].w[j], odd));
-#pragma unroll
-    for (int s = 8; s > 0; s >>= 1) t = __vmaxu2(t, __shfl_xor_sync(0xffffffffu, t, s));
-    m[i] = __uint_as_float(max(t & 0xffffu, t >> 16) << 16);
+    for (int j = 1; j < 4; ++j) t[i] = __vmaxu2(t[i], magnitudes<ODD>(v[i].w[j]));
   }
+  const uint32_t x = __vmaxu2(__byte_perm(t[0], t[1], 0x5410), __byte_perm(t[0], t[1], 0x7632));
+  const uint32_t y = __vmaxu2(__byte_perm(t[2], t[3], 0x5410), __byte_perm(t[2], t[3], 0x7632));
+  const bool hi = threadIdx.x & 8;
+  uint32_t z = __vmaxu2(hi ? y : x, __shfl_xor_sync(0xffffffffu, hi ? x : y, 8));
+#pragma unroll
+  for (int s = 4; s > 0; s >>= 1) z = __vmaxu2(z, __shfl_xor_sync(0xffffffffu, z, s));
+  const uint32_t o = __shfl_xor_sync(0xffffffffu, z, 8), first = hi ? o : z, second = hi ? z : o;
+  m[0] = __uint_as_float(first << 16), m[1] = __uint_as_float(first & 0xffff0000u);
+  m[2] = __uint_as_float(second << 16), m[3] = __uint_as_float(second & 0xffff0000u);
+}
+
+// ------------------------------------------------------------------ rows
+// Tiles of 16 RPT rows along the rows only.  RAW: bf16 rows as they are, as below (16,384 x 7,168
+// gathered 106 -> 80 us).
+template <int SRC, typename T, bool VEC, int RPT, bool RAW>
+__global__ void __launch_bounds__(THREADS) fp8_rows_kernel(const Fp8QuantizeArgs a, int col_blocks) {
+  __shared__ float s_scale[16 * RPT];
+  const int b = blockIdx.x % col_blocks;
+  const int64_t r0 = (int64_t)(blockIdx.x / col_blocks) * (16 * RPT);
+  const int w = threadIdx.x >> 4, l = threadIdx.x & 15;
+  const int64_t c = (int64_t)b * FP8_BLOCK + 8 * l;
+  typename std::conditional<RAW, RawRow8, Row8>::type v[RPT];
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    const int64_t r = r0 + w * RPT + i;
+    if constexpr (RAW) {
+      const T* x = r < a.R ? source_row<SRC, T>(a, r).x : nullptr;
+      keep<VEC>(v[i], x, c, x == nullptr ? 0 : a.C);
+    } else {
+      v[i] = r < a.R ? source8<SRC, T, VEC>(a, source_row<SRC, T>(a, r), c) : zero8();
+    }
+  }
+  float m[RPT];
+  if (only_finite_or_nan(v)) kept_row_maxima<true>(v, m);
+  else kept_row_maxima<false>(v, m);
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    const int64_t r = r0 + w * RPT + i;
+    const uint2 bytes = quantize8(kept(v[i]), divisor(m[i]));
+    if (r < a.R && c < a.C) store8(a.q + r * a.q_stride + c, bytes, a.C - c);
+    if (l == 0) s_scale[w * RPT + i] = block_scale(m[i]);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 16 * RPT; i += THREADS)
+    if (r0 + i < a.R) a.scale[b * a.scale_stride + r0 + i] = s_scale[i];
 }
 
 // ------------------------------------------------------------------ rows and columns
@@ -437,7 +468,7 @@ __device__ __forceinline__ void kept_row_maxima(const RawRow8 (&v)[4], float (&m
 // PAIRED (the SwiGLU's gradient where I is a multiple of 128): a round takes column block b of dh and of du, which come of the
 // same h, u and da; du waits in shared memory, each thread's in its own place (169 -> 133 us for 16,384 x 4,096).
 // RAW (bf16 rows in hand or gathered, without gates): the rows are kept as they are, and three blocks share an SM (16,384 x 7,168
-// in both layouts 223 -> 178 us, gathered 225 -> 205; the gates take products in 32 bits, which words of 16 cannot hold).
+// in both layouts 223 -> 168 us, gathered 225 -> 195; the gates take products in 32 bits, which words of 16 cannot hold).
 template <int SRC, typename T, bool VEC, bool PAIRED, bool RAW>
 __global__ void __launch_bounds__(TILE_THREADS, RAW ? 3 : 2) fp8_columns_kernel(const Fp8QuantizeArgs a, int col_blocks, int group,
                                                                       int groups) {
@@ -524,13 +555,14 @@ __global__ void __launch_bounds__(TILE_THREADS, RAW ? 3 : 2) fp8_columns_kernel(
     const bool odd = only_finite_or_nan(v);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float2 t = two_columns(v, j, odd);
+      const float2 t = odd ? two_columns<true>(v, j) : two_columns<false>(v, j);
       // both half-warps hold the maxima: each brings one (as integers, which order like the values they are bits of)
       atomicMax(&s_max[turn][8 * l + 2 * j + (lane >> 4)], __float_as_int(lane < 16 ? t.x : t.y));
     }
     if (a.q != nullptr) {
       float m[4];
-      kept_row_maxima(v, m, odd);
+      if (odd) kept_row_maxima<true>(v, m);
+      else kept_row_maxima<false>(v, m);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint2 bytes = quantize8(kept(v[i]), divisor(m[i]));
@@ -639,8 +671,14 @@ cudaError_t quantize(const Fp8QuantizeArgs& a, int n_sm, cudaStream_t st) {
     const bool wide = col_blocks * ((a.R + 63) / 64) >= 2 * n_sm;
     const int64_t blocks = col_blocks * (wide ? (a.R + 63) / 64 : (a.R + 15) / 16);
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-    if (wide) fp8_rows_kernel<SRC, T, VEC, 4><<<(unsigned)blocks, THREADS, 0, st>>>(a, (int)col_blocks);
-    else fp8_rows_kernel<SRC, T, VEC, 1><<<(unsigned)blocks, THREADS, 0, st>>>(a, (int)col_blocks);
+    if constexpr (SRC == FP8_PLAIN && VEC && sizeof(T) == 2) {
+      if (wide && a.gates == nullptr) {
+        fp8_rows_kernel<SRC, T, true, 4, true><<<(unsigned)blocks, THREADS, 0, st>>>(a, (int)col_blocks);
+        return cudaGetLastError();
+      }
+    }
+    if (wide) fp8_rows_kernel<SRC, T, VEC, 4, false><<<(unsigned)blocks, THREADS, 0, st>>>(a, (int)col_blocks);
+    else fp8_rows_kernel<SRC, T, VEC, 1, false><<<(unsigned)blocks, THREADS, 0, st>>>(a, (int)col_blocks);
     return cudaGetLastError();
   }
   const int64_t tiles = a.R / 128 + a.E;

@@ -356,6 +356,28 @@ def test_what_is_not_finite_stays_an_element():
         assert torch.equal(torch.nan_to_num(w.q.float()), v.q.float())
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("R,C", [(10_000, 384), (10_001, 376)])
+def test_what_is_not_finite_in_many_rows(R, C, dtype):
+    """As above in as many rows as take the larger tiles: along the rows alone and in both layouts."""
+    rng = np.random.default_rng(6)
+    x, _ = values(rng, (R, C), dtype)
+    bad, clean = x.clone(), x.clone()
+    rows = rng.integers(0, R, 500)
+    cols = rng.integers(0, C, 500)
+    for i, v in enumerate((float("nan"), float("inf"), float("-inf"), -float("nan"))):
+        bad[cuda(rows[i::4]), cuda(cols[i::4])] = v
+    places = ~torch.isfinite(bad)
+    clean[places] = 0.0
+    offsets = cuda(np.array([0, 1, 1, 5_000, R], np.int32))
+    got, want = mok.fp8_quantize(bad), mok.fp8_quantize(clean)
+    both = mok.fp8_quantize(bad, offsets=offsets)
+    assert torch.equal(got["scale"], want["scale"]) and torch.equal(both["scale"], want["scale"])
+    for q in (got["q"], both["q"]):
+        assert torch.equal(torch.isnan(q.float()), places)
+        assert torch.equal(torch.nan_to_num(q.float()), want["q"].float())
+
+
 def test_the_ends_of_the_range():
     """Blocks of zeros, of the type's smallest and largest values."""
     for dtype in (BF, F32):
