@@ -473,14 +473,14 @@ template <int SRC, typename T, bool VEC, bool PAIRED, bool RAW>
 __global__ void __launch_bounds__(TILE_THREADS, RAW ? 3 : 2) fp8_columns_kernel(const Fp8QuantizeArgs a, int col_blocks, int group,
                                                                       int groups) {
   __shared__ __align__(16) uint32_t tile[128 * 32];
-  __shared__ __align__(16) int s_max[2][128];  // bits of the columns' maxima, of this round and the next
+  __shared__ __align__(16) int s_max[2][128];  // bits of the columns' maxima, of this turn and the next
   __shared__ float s_scale[2][128];
   __shared__ int s_warp[16], s_where[2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int p = blockIdx.x / groups;  // row tile
   // the expert whose 128-row blocks hold block p: a scan of the experts' blocks, 512 experts at a time
   if (threadIdx.x == 0) s_where[1] = 0;
-  int before = 0;  // blocks of the experts before this round's
+  int before = 0;  // blocks of the experts before this turn's
   for (int e0 = 0; e0 < a.E; e0 += TILE_THREADS) {
     const int e = e0 + threadIdx.x;
     int lo = 0, hi = 0;
