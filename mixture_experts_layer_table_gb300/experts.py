@@ -209,11 +209,12 @@ def merge_rows_backward(dy: torch.Tensor, o: torch.Tensor, row_of: torch.Tensor,
         raise ValueError("gates: expected a float32 matrix")
     T, H = dy.shape
     k = gates.shape[1]
-    if out is None:
-        out = {"do": torch.zeros_like(o), "dgates": torch.empty((T, k), dtype=torch.float32, device=dy.device)}
     R = o.shape[0] if isinstance(o, torch.Tensor) and o.dim() == 2 else -1
     yp, ys = _rows(dy, (T, H), dtype, "dy", device)
     rp, rs = _rows(o, (R, H), dtype, "o", device)
+    if out is None:  # rows as far apart as those of o
+        out = {"do": torch.zeros((R, rs or H), dtype=dtype, device=dy.device)[:, :H],
+               "dgates": torch.empty((T, k), dtype=torch.float32, device=dy.device)}
     dp, ds = _rows(out["do"], (R, H), dtype, 'out["do"]', device)
     if ds != rs and (ds or H) != (rs or H):
         raise ValueError(f'out["do"]: rows {ds or H} elements apart, those of o {rs or H}')
@@ -365,7 +366,8 @@ class Fp8Weights:
     def quantize(self, w: torch.Tensor, stream=None) -> "Fp8Weights":
         """Takes new weights (f32 or bf16, contiguous) into the buffers (mok_fp8_quantize_weights)."""
         E, N, K = self.shape
-        if not isinstance(w, torch.Tensor) or w.dtype not in ELEM_TYPES:
+        _device(w, "w")
+        if w.dtype not in ELEM_TYPES:
             raise ValueError("w: expected float32 or bfloat16 weights")
         shape = (N, K) if w.dim() == 2 and E == 1 else self.shape
         d = Fp8WeightsDesc(N, K, self._q[1], self._qt[1], E, ELEM_TYPES[w.dtype])

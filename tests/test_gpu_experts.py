@@ -126,6 +126,18 @@ def test_rows_further_apart(dtype, extra):
         assert (torch.as_strided(t, (t.shape[0] - 1, ld - H), (ld, 1), H) == 3.0).all()
 
 
+def test_merge_gradient_of_rows_further_apart_without_buffers():
+    rng = np.random.default_rng(8)
+    T, k, E, H = 12, 2, 4, 136
+    _, row, _ = table(rng, T, k, E)
+    dy, _ = values(rng, (T, H), BF)
+    o, _ = values(rng, (T * k, H + 24), BF)
+    o = o[:, :H]
+    g = cuda(rng.random((T, k)), F32)
+    got, want = mok.merge_rows_backward(dy, o, cuda(row), g), mok.merge_rows_backward(dy, o.contiguous(), cuda(row), g)
+    assert torch.equal(got["do"], want["do"]) and torch.equal(got["dgates"], want["dgates"])
+
+
 def test_indices_out_of_range_are_reported_and_left_out():
     x, o = torch.ones(4, 16).cuda(), torch.ones(8, 16).cuda()
     good = torch.arange(8, dtype=torch.int32)
