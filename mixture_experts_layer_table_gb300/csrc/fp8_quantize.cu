@@ -144,16 +144,38 @@ __device__ __forceinline__ Row8 load8(const __nv_bfloat16* row, int64_t c, int64
 }
 
 // 1 / (1 + e^-h), two at a time: the accurate exponential, and a reciprocal corrected once.  With the hardware's 2^x and
-// 1 / x alone (2^-21) a value on the other side of a border between two E4M3 values was ten times as frequent.  From h = -87
-// down the value stays at 2^-125, far below what counts beside LEAST, so that nothing overflows on the way.
+// 1 / x alone (2^-21) a value on the other side of a border between two E4M3 values was ten times as frequent.  From h = FAR
+// down the value stays at e^FAR: far8 brings the rest.
+constexpr float FAR = -40.0f;
 __device__ __forceinline__ F2 sigmoid2(F2 h) {
   float a, b;
   split(h, a, b);
-  const F2 d = add2(f2(expf(-fmaxf(a, -87.0f)), expf(-fmaxf(b, -87.0f))), f2(1.0f));
+  const F2 d = add2(f2(expf(-fmaxf(a, FAR)), expf(-fmaxf(b, FAR))), f2(1.0f));
   split(d, a, b);
   const F2 r = f2(reciprocal(a), reciprocal(b));
   return fma2(fma2(mul2(d, f2(-1.0f)), r, f2(1.0f)), r, r);
 }
+
+// Below FAR the sigmoid is e^h = e^FAR e^(h - FAR), soon out of f32's range, while h and what it is multiplied with may be as
+// large as the type allows (a mask's lowest value).  So the second part (h - FAR is exact) goes to that other factor, x (a NaN
+// for an infinite h), and h itself stops where nothing is left of any product: these then come out to f32's precision, or as 0.
+__device__ __forceinline__ void far2(F2& h, F2& x) {
+  x = mul2(x, f2(fmaf(h.x, 0.0f, expf(fminf(h.x - FAR, 0.0f))), fmaf(h.y, 0.0f, expf(fminf(h.y - FAR, 0.0f)))));
+  h = f2(fmaxf(h.x, -1e4f), fmaxf(h.y, -1e4f));
+}
+__device__ __forceinline__ void far8(Row8& h, Row8& x) {
+  float least = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) least = fminf(fminf(least, h.v[j].x), h.v[j].y);
+  if (least < FAR) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) far2(h.v[j], x.v[j]);
+  }
+}
+// silu(h) = h s, and its slope s (1 + h (1 - s)); the last product with another factor is the only one that can leave f32's
+// range, and only where the result does.
+__device__ __forceinline__ F2 silu2(F2 h, F2 s) { return mul2(h, s); }
+__device__ __forceinline__ F2 slope2(F2 h, F2 s) { return mul2(s, add2(mul2(h, fma2(s, f2(-1.0f), f2(1.0f))), f2(1.0f))); }
 
 // Where a row of the source lies.
 template <typename T>
@@ -189,24 +211,25 @@ __device__ __forceinline__ Row8 source8(const Fp8QuantizeArgs& a, const Source<T
       for (int j = 0; j < 4; ++j) o.v[j] = mul2(o.v[j], g);
     }
   } else if (SRC == FP8_SWIGLU) {
-    const Row8 h = load8<VEC>(s.x, c, a.C), u = load8<VEC>(s.x + a.C, c, a.C);
+    Row8 h = load8<VEC>(s.x, c, a.C), u = load8<VEC>(s.x + a.C, c, a.C);
+    far8(h, u);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) o.v[j] = mul2(mul2(h.v[j], sigmoid2(h.v[j])), u.v[j]);
+    for (int j = 0; j < 4; ++j) o.v[j] = mul2(silu2(h.v[j], sigmoid2(h.v[j])), u.v[j]);
   } else {
     const int64_t I = a.C / 2;
     // VEC: I is a multiple of 8, so that a lane's columns lie in one half
     if (VEC) {
       if (c >= I) {
-        const Row8 h = load8<true>(s.x, c - I, I), d = load8<true>(s.grad, c - I, I);
+        Row8 h = load8<true>(s.x, c - I, I), d = load8<true>(s.grad, c - I, I);
+        far8(h, d);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o.v[j] = mul2(mul2(d.v[j], h.v[j]), sigmoid2(h.v[j]));
+        for (int j = 0; j < 4; ++j) o.v[j] = mul2(silu2(h.v[j], sigmoid2(h.v[j])), d.v[j]);
       } else {
-        const Row8 h = load8<true>(s.x, c, I), d = load8<true>(s.grad, c, I), u = load8<true>(s.x + I, c, I);
+        Row8 h = load8<true>(s.x, c, I), d = load8<true>(s.grad, c, I);
+        const Row8 u = load8<true>(s.x + I, c, I);
+        far8(h, d);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const F2 sg = sigmoid2(h.v[j]);
-          o.v[j] = mul2(mul2(mul2(d.v[j], u.v[j]), sg), add2(mul2(h.v[j], fma2(sg, f2(-1.0f), f2(1.0f))), f2(1.0f)));
-        }
+        for (int j = 0; j < 4; ++j) o.v[j] = mul2(mul2(slope2(h.v[j], sigmoid2(h.v[j])), u.v[j]), d.v[j]);
       }
     } else {
 #pragma unroll
@@ -223,9 +246,10 @@ __device__ __forceinline__ Row8 source8(const Fp8QuantizeArgs& a, const Source<T
           d[z] = in ? widen(s.grad[i]) : 0.0f;
           u[z] = in && !up[z] ? widen(s.x[I + i]) : 0.0f;
         }
-        const F2 hh = f2(h[0], h[1]), dd = f2(d[0], d[1]), sg = sigmoid2(hh);
-        const F2 du = mul2(mul2(dd, hh), sg);
-        const F2 dh = mul2(mul2(mul2(dd, f2(u[0], u[1])), sg), add2(mul2(hh, fma2(sg, f2(-1.0f), f2(1.0f))), f2(1.0f)));
+        F2 hh = f2(h[0], h[1]), dd = f2(d[0], d[1]);
+        if (fminf(h[0], h[1]) < FAR) far2(hh, dd);
+        const F2 sg = sigmoid2(hh);
+        const F2 du = mul2(silu2(hh, sg), dd), dh = mul2(mul2(slope2(hh, sg), f2(u[0], u[1])), dd);
         o.v[j] = f2(up[0] ? du.x : dh.x, up[1] ? du.y : dh.y);
       }
     }
@@ -237,12 +261,14 @@ __device__ __forceinline__ Row8 source8(const Fp8QuantizeArgs& a, const Source<T
 template <typename T>
 __device__ __forceinline__ void swiglu_grad8(const Fp8QuantizeArgs& a, const Source<T>& s, int64_t i, Row8& dh, Row8& du) {
   const int64_t I = a.C / 2;
-  const Row8 h = load8<true>(s.x, i, I), u = load8<true>(s.x + I, i, I), d = load8<true>(s.grad, i, I);
+  Row8 h = load8<true>(s.x, i, I), d = load8<true>(s.grad, i, I);
+  const Row8 u = load8<true>(s.x + I, i, I);
+  far8(h, d);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const F2 sg = sigmoid2(h.v[j]);
-    du.v[j] = mul2(mul2(d.v[j], h.v[j]), sg);
-    dh.v[j] = mul2(mul2(mul2(d.v[j], u.v[j]), sg), add2(mul2(h.v[j], fma2(sg, f2(-1.0f), f2(1.0f))), f2(1.0f)));
+    du.v[j] = mul2(silu2(h.v[j], sg), d.v[j]);
+    dh.v[j] = mul2(mul2(slope2(h.v[j], sg), u.v[j]), d.v[j]);
   }
 }
 

@@ -301,6 +301,64 @@ def test_quantized_swiglu_and_its_gradient(T, k, E, C, dtype):
     check_quantized(mok.fp8_quantize(hu, source="swiglu_grad", grad=da), g, offsets, 2.0 ** -19, size)
 
 
+# rows, width of u: pairs of column blocks, aligned rows, odd widths, few rows and as many as take the larger tiles
+WIDTHS = [(300, 512), (140, 264), (70, 7), (130, 1111), (5000, 512), (2400, 1111)]
+
+
+def per_row(rng, R, choices):
+    return rng.choice(choices, (R, 1)) * rng.choice([-1.0, 1.0], (R, 1))
+
+
+def check_swiglu(hu64, da64, dtype, offsets):
+    """The SwiGLU and its gradient of these values, along the rows alone and in both layouts."""
+    hu, da = torch.tensor(hu64).to(dtype).cuda(), torch.tensor(da64).to(dtype).cuda()
+    off = cuda(offsets)
+    a, size = O.swiglu(f64(hu))
+    g, terms = O.swiglu_grad(f64(hu), f64(da))
+    for kw in (dict(), dict(offsets=off)):
+        check_quantized(mok.fp8_quantize(hu, source="swiglu", **kw), a, offsets, 2.0 ** -19, size)
+        check_quantized(mok.fp8_quantize(hu, source="swiglu_grad", grad=da, **kw), g, offsets, 2.0 ** -19, terms)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("R,C", WIDTHS)
+def test_swiglu_far_below_zero(R, C, dtype):
+    """h where e^h is smaller than f32's normal values, down to the type's lowest, in rows of nothing else and among others.
+    (The part of the sigmoid below e^-40 is an exponential of its own: two more roundings than counted at the top, in 2^-19.)"""
+    rng = np.random.default_rng(R + C)
+    far = rng.choice([-86.5, -87.5, -88.0, -90.0, -100.0, -104.0, -150.0, -1e4, -1e30, float(torch.finfo(dtype).min)], (R, C))
+    often = np.where(np.arange(R)[:, None] % 3 == 0, 1.0, 0.2)
+    h = np.where(rng.random((R, C)) < often, far, 2.0 * rng.normal(size=(R, C)))
+    u = rng.normal(size=(R, C)) * per_row(rng, R, [1.0, 1e3, 1e6, 1e30])
+    da = rng.normal(size=(R, C)) * per_row(rng, R, [1e-3, 1.0, 1e4])
+    check_swiglu(np.concatenate([h, u], 1), da, dtype, np.array([0, R // 3, R // 3, R], np.int32))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("R,C", WIDTHS[:4])
+def test_swiglu_gradient_whose_parts_leave_the_range(R, C, dtype):
+    """da u, da h and da s out of f32's range where the gradient is not; h and u both at the type's lowest."""
+    rng = np.random.default_rng(R)
+    h = -45 - 30 * rng.random((R, C))
+    size = rng.choice([(1e25, 1e25), (1.0, 1e36), (1e-10, 1e36), (1e25, 1e-10)], R)
+    u, da = rng.normal(size=(R, C)) * size[:, :1], rng.normal(size=(R, C)) * size[:, 1:]
+    h[::5] = u[::5] = float(torch.finfo(dtype).min)
+    check_swiglu(np.concatenate([h, u], 1), da, dtype, np.array([0, R // 2, R], np.int32))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_swiglu_of_minus_infinity(dtype):
+    """-inf e^-inf has no value: a NaN, out of its block's scale."""
+    hu = torch.ones(3, 512, dtype=dtype).cuda()
+    hu[1, 3] = float("-inf")
+    da = torch.ones(3, 256, dtype=dtype).cuda()
+    q, g = mok.fp8_quantize(hu, source="swiglu"), mok.fp8_quantize(hu, source="swiglu_grad", grad=da)
+    for out, places in ((q, [3]), (g, [3, 259])):
+        nan = torch.isnan(out["q"].float())
+        assert nan[1, places].all() and int(nan.sum()) == len(places)
+        assert torch.equal(out["scale"][:, 1], out["scale"][:, 0])
+
+
 def test_the_oracles_swiglu_gradient_by_differences():
     rng = np.random.default_rng(1)
     x, da = rng.normal(size=(3, 10)), rng.normal(size=(3, 5))
