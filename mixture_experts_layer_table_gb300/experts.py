@@ -2,7 +2,8 @@
 and back, and E4M3 operands with a scale for each block of 128: quantisers, grouped products, weight gradients.
 
 As in ``_native``: argument marshalling only, every step runs in the library's CUDA kernels, the
-stream is PyTorch's current stream unless given, and there is no fallback.  Tensors are on the current
+stream is PyTorch's current stream unless given, and there is no fallback.  A tensor that a call makes belongs to the
+stream of the call, as if that were the current one.  Tensors are on the current
 device.  Rows (tokens, expert rows, E4M3 rows, scales) may be further apart than they are long; E4M3 rows start
 at multiples of 16 bytes (``empty_e4m3``).
 
@@ -15,6 +16,7 @@ An expert's two products in training, with ``offsets``, ``src_of`` and ``row_of`
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Dict, Optional
 
@@ -125,6 +127,21 @@ def _queue(stream, device):
     return _raw_stream(device) if stream is None and _raw_stream is not None else _stream(stream)
 
 
+_HERE = contextlib.nullcontext()
+
+
+def _on(stream):
+    """The context in which a call makes its buffers: its stream's, whose allocator gives out no memory that another stream
+    is still to write, and on which a fill comes in front of the kernel."""
+    if stream is None:
+        return _HERE
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        # 0 and 1 both name the default stream, which is no external one to PyTorch
+        stream = torch.cuda.ExternalStream(handle) if handle > 1 else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
 def empty_e4m3(*shape, device="cuda") -> torch.Tensor:
     """An uninitialised E4M3 tensor whose rows (of the last dimension) start at multiples of 16 bytes."""
     width = shape[-1]
@@ -156,7 +173,8 @@ def gather_rows(x: torch.Tensor, src_of: torch.Tensor, k: int, gates: Optional[t
     T, H = x.shape
     R = src_of.shape[0] if isinstance(src_of, torch.Tensor) and src_of.dim() == 1 else -1
     if out is None:
-        out = torch.empty((max(0, R), H), dtype=dtype, device=x.device)
+        with _on(stream):
+            out = torch.empty((max(0, R), H), dtype=dtype, device=x.device)
     xp, xs = _rows(x, (T, H), dtype, "x", device)
     op, os_ = _rows(out, (R, H), dtype, "out", device)
     d = RowsDesc(T, R, H, xs, os_, k, kind)
@@ -185,7 +203,8 @@ def merge_rows(o: torch.Tensor, row_of: torch.Tensor, k: int, gates: Optional[to
     R, H = o.shape
     T = _tokens(row_of, k)
     if out is None:
-        out = torch.empty((T, H), dtype=dtype, device=o.device)
+        with _on(stream):
+            out = torch.empty((T, H), dtype=dtype, device=o.device)
     rp, rs = _rows(o, (R, H), dtype, "o", device)
     yp, ys = _rows(out, (T, H), dtype, "out", device)
     d = RowsDesc(T, R, H, ys, rs, k, kind)
@@ -213,8 +232,9 @@ def merge_rows_backward(dy: torch.Tensor, o: torch.Tensor, row_of: torch.Tensor,
     yp, ys = _rows(dy, (T, H), dtype, "dy", device)
     rp, rs = _rows(o, (R, H), dtype, "o", device)
     if out is None:  # rows as far apart as those of o
-        out = {"do": torch.zeros((R, rs or H), dtype=dtype, device=dy.device)[:, :H],
-               "dgates": torch.empty((T, k), dtype=torch.float32, device=dy.device)}
+        with _on(stream):
+            out = {"do": torch.zeros((R, rs or H), dtype=dtype, device=dy.device)[:, :H],
+                   "dgates": torch.empty((T, k), dtype=torch.float32, device=dy.device)}
     dp, ds = _rows(out["do"], (R, H), dtype, 'out["do"]', device)
     if ds != rs and (ds or H) != (rs or H):
         raise ValueError(f'out["do"]: rows {ds or H} elements apart, those of o {rs or H}')
@@ -267,10 +287,11 @@ def fp8_quantize(x: torch.Tensor, source: str = "plain", grad: Optional[torch.Te
     if out is None:
         new = lambda *s: torch.empty(s, dtype=torch.float32, device=x.device)  # noqa: E731
         out = {}
-        if rows:
-            out |= {"q": empty_e4m3(max(0, R), C, device=x.device), "scale": new(_blocks(C), max(0, R))}
-        if E:
-            out |= {"qt": empty_e4m3(C, fp8_columns(R, E), device=x.device), "qt_scale": new(R // 128 + E, C)}
+        with _on(stream):
+            if rows:
+                out |= {"q": empty_e4m3(max(0, R), C, device=x.device), "scale": new(_blocks(C), max(0, R))}
+            if E:
+                out |= {"qt": empty_e4m3(C, fp8_columns(R, E), device=x.device), "qt_scale": new(R // 128 + E, C)}
     d = Fp8QuantizeDesc(R, C, T, 0, 0, 0, 0, 0, E, k, SOURCES[source], kind)
     xp, d.x_stride = _rows(x, (T, width), dtype, "x", device)
     gp = qp = sp = tp = tsp = None
@@ -403,7 +424,8 @@ class Fp8Weights:
             raise ValueError(f"{E} groups need their offsets")
         R = x.shape[0] if isinstance(x, torch.Tensor) and x.dim() == 2 else -1
         if out is None:
-            out = torch.empty((max(0, R), N), dtype=dtype, device=self.q.device)
+            with _on(stream):
+                out = torch.empty((max(0, R), N), dtype=dtype, device=self.q.device)
         elif isinstance(out, torch.Tensor):
             dtype = out.dtype
         if dtype not in ELEM_TYPES:
@@ -440,7 +462,8 @@ def fp8_weight_grad(dy: torch.Tensor, dy_scale: torch.Tensor, x: torch.Tensor, x
     if E < 1 or columns % 128 or columns < 128 * E:
         raise ValueError(f"dy: expected 128 (R / 128 + E) columns, got {columns} with {E} groups")
     if out is None:
-        out = torch.empty((E, N, H), dtype=dtype, device=dy.device)
+        with _on(stream):
+            out = torch.empty((E, N, H), dtype=dtype, device=dy.device)
     elif isinstance(out, torch.Tensor):
         dtype = out.dtype
     if dtype not in ELEM_TYPES:

@@ -769,6 +769,52 @@ def test_captured_and_on_another_stream():
         assert torch.equal(a, b)
 
 
+def test_buffers_made_for_another_stream():
+    """Calls without buffers on a stream that is not the current one, given as such and by its handle, while the current
+    stream is busy and has still to write memory that its allocator has taken back."""
+    rng = np.random.default_rng(9)
+    T, k, E, H, N = 90, 3, 4, 256, 272
+    src, row, offsets = table(rng, T, k, E, dropped=0.3)
+    src_of, row_of, off = cuda(src), cuda(row), cuda(offsets)
+    x, _ = values(rng, (T, H), BF)
+    o, _ = values(rng, (T * k, H), BF)
+    dn, _ = values(rng, (T * k, N), BF)
+    g = cuda(rng.random((T, k)), F32)
+    w = mok.Fp8Weights(values(rng, (E, N, H), BF)[0], transposed=True)
+    q, d = mok.fp8_quantize(o, offsets=off), mok.fp8_quantize(dn, offsets=off)
+    used = 128 * int(sum(-(-n // 128) for n in np.diff(offsets)))
+
+    def calls(stream=None):
+        yield mok.gather_rows(x, src_of, k, g, stream=stream)
+        yield mok.merge_rows(o, row_of, k, g, stream=stream)
+        yield from mok.merge_rows_backward(x, o, row_of, g, stream=stream).values()
+        both = mok.fp8_quantize(x, src_of=src_of, k=k, offsets=off, stream=stream)
+        rows = int(offsets[-1])
+        yield both["q"][:rows].view(torch.uint8)
+        yield both["scale"][:, :rows]
+        yield both["qt"][:, :used].view(torch.uint8)
+        yield both["qt_scale"][:used // 128]
+        yield w.matmul(q["q"], q["scale"], off, stream=stream)[:rows]
+        yield w.matmul_transposed(d["q"], d["scale"], off, stream=stream)[:rows]
+        yield mok.fp8_weight_grad(d["qt"], d["qt_scale"], q["qt"], q["qt_scale"], off, stream=stream)
+
+    want = [t.clone() for t in calls()]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for here, stream in ((torch.cuda.current_stream(), side), (torch.cuda.current_stream(), side.cuda_stream),
+                         (side, torch.cuda.default_stream()), (side, 0)):
+        with torch.cuda.stream(here):
+            torch.cuda._sleep(200_000_000)
+            for n in (4, 1024, 16_384, 24_000, 70_000, 90_000, 140_000, 200_000, 500_000, 1_200_000):
+                for _ in range(3):
+                    torch.full((n,), 0x55, dtype=torch.uint8, device="cuda")
+            got = list(calls(stream))
+        assert not here.query()
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(got, want)):
+            assert torch.equal(a, b), i
+
+
 def test_two_calls_at_once():
     """The same weights on two streams: nothing is shared between calls."""
     rng = np.random.default_rng(4)
