@@ -328,12 +328,14 @@ class Fp8Weights:
         shape = (1, *w.shape) if w.dim() == 2 else tuple(w.shape)
         self._make(*shape, transposed, w.device)
         self.quantize(w)
+        _settle(w.device)
 
     @classmethod
     def empty(cls, E: int, N: int, K: int, transposed: bool = False, device="cuda") -> "Fp8Weights":
         """Room for weights that ``quantize`` fills."""
         self = cls.__new__(cls)
         self._make(E, N, K, transposed, device)
+        _settle(self.q.device)
         return self
 
     @classmethod
@@ -351,6 +353,7 @@ class Fp8Weights:
         self.shape = tuple(q.shape)
         self.q, self.scale, self.qt, self.qt_scale = q, scale, qt, qt_scale
         self._finish()
+        _settle(self.q.device)
         return self
 
     def _make(self, E, N, K, transposed, device):
@@ -372,7 +375,6 @@ class Fp8Weights:
             self._qt_scale = _packed(self.qt_scale, (E, _blocks(K), _blocks(N)), torch.float32, "qt_scale", self._index)
         self.device_status = torch.zeros(2, dtype=torch.int32, device=self.q.device)
         self._status = self.device_status.data_ptr()
-        _settle(self.q.device)
 
     def _elements(self, t, shape, name):
         """(address, bytes between rows) of [E][rows][width] elements, one row after the other."""

@@ -815,6 +815,36 @@ def test_buffers_made_for_another_stream():
             assert torch.equal(a, b), i
 
 
+def test_new_weights_are_ready_on_another_stream():
+    """The current stream is busy when weights are made; their first product goes to another stream at once."""
+    rng = np.random.default_rng(10)
+    E, N, K, R = 3, 304, 272, 50
+    offsets = cuda(np.array([0, 20, 20, R], np.int32))
+    w, _ = values(rng, (E, N, K), BF)
+    q, d = mok.fp8_quantize(values(rng, (R, K), BF)[0]), mok.fp8_quantize(values(rng, (R, N), BF)[0])
+    first = mok.Fp8Weights(w, transposed=True)
+    want = first.matmul(q["q"], q["scale"], offsets), first.matmul_transposed(d["q"], d["scale"], offsets)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for make in (lambda: mok.Fp8Weights(w, transposed=True),
+                 lambda: mok.Fp8Weights.of(first.q.clone(), first.scale.clone(), first.qt.clone(), first.qt_scale.clone())):
+        for n in (8, E * N * 272, E * K * 304, 64, 4096):
+            torch.full((n,), 0x55, dtype=torch.uint8, device="cuda")
+        torch.cuda._sleep(40_000_000)
+        weights = make()
+        assert torch.cuda.current_stream().query()
+        got = (weights.matmul(q["q"], q["scale"], offsets, stream=side),
+               weights.matmul_transposed(d["q"], d["scale"], offsets, stream=side))
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)) and weights.status() == (0, 0)
+    torch.cuda._sleep(40_000_000)
+    weights = mok.Fp8Weights.empty(E, N, K)
+    assert torch.cuda.current_stream().query()
+    got = weights.quantize(w, stream=side).matmul(q["q"], q["scale"], offsets, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want[0]) and weights.status() == (0, 0)
+
+
 def test_two_calls_at_once():
     """The same weights on two streams: nothing is shared between calls."""
     rng = np.random.default_rng(4)
