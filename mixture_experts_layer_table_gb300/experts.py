@@ -444,10 +444,12 @@ class Fp8Weights:
         return out
 
     def status(self):
-        """(code, site) of the first error on the device since the last call; waits for the device's work."""
+        """(code, site) of the first error on the device since the last call; waits for the work of all of its streams."""
+        torch.cuda.synchronize(self.q.device)
         code, site = self.device_status.tolist()
         if code:
             self.device_status.zero_()
+            _settle(self.q.device)
         return code, site
 
 

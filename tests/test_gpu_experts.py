@@ -845,6 +845,21 @@ def test_new_weights_are_ready_on_another_stream():
     assert torch.equal(got, want[0]) and weights.status() == (0, 0)
 
 
+def test_status_of_work_on_another_stream():
+    """What a busy stream reports late (written here by a fill) is read, and cleared for whatever comes next."""
+    w = mok.Fp8Weights(torch.ones(16, 16).cuda())
+    late = torch.tensor([5, 43], dtype=torch.int32).cuda()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(2):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(40_000_000)
+            w.device_status.copy_(late)
+        assert w.status() == (5, 43)
+        assert torch.cuda.current_stream().query()
+        assert w.status() == (0, 0)
+
+
 def test_two_calls_at_once():
     """The same weights on two streams: nothing is shared between calls."""
     rng = np.random.default_rng(4)
