@@ -595,7 +595,8 @@ mok_status mok_fp8_matmul(const mok_fp8_matmul_desc* desc, const uint8_t* x, con
 
 /* out[e][n][h] = sum over group e's blocks b of dy_scale[b][n] x_scale[b][h] sum_{r in b} dy[n][r] x[h][r]: the gradient
  * of the weights, with dy [N][P], x [H][P] and their scales as qt and qt_scale of mok_fp8_quantize for the same R, E and
- * offsets.  Zeros for a group without rows.  out f32 or bf16 [E][N][H], contiguous. */
+ * offsets.  Zeros for a group without rows.  out f32 or bf16 [E][N][H], contiguous.  device_status (or NULL) takes a wait that
+ * ran out (MOK_ERR_TIMEOUT); part of out is unwritten then, as of mok_fp8_matmul's. */
 typedef struct {
   int64_t R, N, H;
   int64_t dy_stride, x_stride;

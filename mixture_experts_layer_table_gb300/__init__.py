@@ -12,5 +12,5 @@ from ._native import (FLAG_GEMM_PAIR, FLAG_GEMM_SINGLE, FLAG_RING_PERSISTENT, FL
                       workspace_size)
 from .routing import GROUP_MAX, GROUP_TOP2, RouteDesc, Router, make_route_desc  # noqa: F401
 from .training import AdamW, GradNorm  # noqa: F401
-from .experts import (Fp8Weights, empty_e4m3, fp8_columns, fp8_quantize, fp8_weight_grad, gather_rows,  # noqa: F401
-                      merge_rows, merge_rows_backward)
+from .experts import (Fp8Weights, empty_e4m3, fp8_columns, fp8_quantize, fp8_status, fp8_weight_grad,  # noqa: F401
+                      gather_rows, merge_rows, merge_rows_backward)

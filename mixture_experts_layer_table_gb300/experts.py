@@ -445,19 +445,49 @@ class Fp8Weights:
 
     def status(self):
         """(code, site) of the first error on the device since the last call; waits for the work of all of its streams."""
-        torch.cuda.synchronize(self.q.device)
-        code, site = self.device_status.tolist()
-        if code:
-            self.device_status.zero_()
-            _settle(self.q.device)
-        return code, site
+        return _read_status(self.device_status)
+
+
+_STATUS: Dict[int, torch.Tensor] = {}  # of each device, for calls that bring no status word
+
+
+def _status_of(t, device) -> Optional[int]:
+    """The address of the device's status word, made by the first call that needs it.  Not under capture, whose memory is the
+    graph's: there is none then."""
+    word = _STATUS.get(device)
+    if word is None:
+        if torch.cuda.is_current_stream_capturing():
+            return None
+        word = torch.zeros(2, dtype=torch.int32, device=t.device)
+        _settle(t.device)
+        _STATUS[device] = word
+    return word.data_ptr()
+
+
+def _read_status(word):
+    torch.cuda.synchronize(word.device)
+    code, site = word.tolist()
+    if code:
+        word.zero_()
+        _settle(word.device)
+    return code, site
+
+
+def fp8_status(device=None):
+    """(code, site) of the first error on the device (the current one) of ``fp8_weight_grad`` calls without a
+    ``device_status``, since the last call; waits for the work of all of its streams."""
+    index = torch.device("cuda" if device is None else device).index
+    word = _STATUS.get(_current_device() if index is None else index)
+    return (0, 0) if word is None else _read_status(word)
 
 
 def fp8_weight_grad(dy: torch.Tensor, dy_scale: torch.Tensor, x: torch.Tensor, x_scale: torch.Tensor,
                     offsets: torch.Tensor, out: Optional[torch.Tensor] = None, dtype=torch.float32,
                     device_status: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """dW = dy^T x over each group's rows (mok_fp8_weight_grad): dy [N][P] and x [H][P] with their scales ("qt" and
-    "qt_scale" of ``fp8_quantize`` with the same offsets) -> [E][N][H], f32 or bf16; zeros for a group without rows."""
+    "qt_scale" of ``fp8_quantize`` with the same offsets) -> [E][N][H], f32 or bf16; zeros for a group without rows.
+    A wait on the device that ran out (which leaves part of the gradient unwritten) goes to ``device_status``, or without
+    one to what ``fp8_status`` reads (under capture only after a first call outside of one)."""
     try:
         (N, columns), (H, _), (E,) = dy.shape, x.shape, offsets.shape
     except (AttributeError, ValueError):
@@ -481,7 +511,8 @@ def fp8_weight_grad(dy: torch.Tensor, dy_scale: torch.Tensor, x: torch.Tensor, x
         _packed(x_scale, (columns // 128, H), torch.float32, "x_scale", device),
         _packed(offsets, (E + 1,), torch.int32, "offsets", device),
         _packed(out, (E, N, H), dtype, "out", device),
-        _optional(device_status, (2,), torch.int32, "device_status", device), _queue(stream, device))
+        _status_of(dy, device) if device_status is None else
+        _packed(device_status, (2,), torch.int32, "device_status", device), _queue(stream, device))
     if code:
         _check("mok_fp8_weight_grad", code)
     return out

@@ -860,6 +860,31 @@ def test_status_of_work_on_another_stream():
         assert w.status() == (0, 0)
 
 
+def test_the_weight_gradient_has_a_status_word(monkeypatch):
+    """Its own unless one is given, and the same for every call on a device."""
+    rng = np.random.default_rng(13)
+    offsets = cuda(np.array([0, 70, 90], np.int32))
+    q = mok.fp8_quantize(values(rng, (90, 48), BF)[0], offsets=offsets)
+    operands = (q["qt"], q["qt_scale"], q["qt"], q["qt_scale"], offsets)
+    mok.fp8_weight_grad(*operands)
+    assert mok.fp8_status() == (0, 0) == mok.fp8_status("cuda:0")
+    given = torch.zeros(2, dtype=torch.int32).cuda()
+    mok.fp8_weight_grad(*operands, device_status=given)
+    assert given.tolist() == [0, 0]
+    words = []
+    monkeypatch.setitem(X._FNS, "mok_fp8_weight_grad", lambda *a: words.append(a[-2]) or 0)
+    mok.fp8_weight_grad(*operands)
+    mok.fp8_weight_grad(*operands, device_status=given)
+    word = X._STATUS[0]
+    assert words == [word.data_ptr(), given.data_ptr()]
+    side, late = torch.cuda.Stream(), torch.tensor([5, 43], dtype=torch.int32).cuda()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):     # what a kernel would report
+        torch.cuda._sleep(40_000_000)
+        word.copy_(late)
+    assert mok.fp8_status() == (5, 43) and mok.fp8_status() == (0, 0)
+
+
 def test_two_calls_at_once():
     """The same weights on two streams: nothing is shared between calls."""
     rng = np.random.default_rng(4)
