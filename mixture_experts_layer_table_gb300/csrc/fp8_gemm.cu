@@ -32,6 +32,7 @@
 #include <type_traits>
 
 #include "fp8.cuh"
+#include "fp8_plan.h"
 #include "ptx.cuh"
 #include "tmap.cuh"
 
@@ -701,68 +702,36 @@ bool f8_wide(const void* out, int64_t ld, int64_t width, bool bf16) {
 
 uint32_t f8_magic(int64_t d) { return d == 1 ? 0 : (uint32_t)(((int64_t(1) << 32) + d - 1) / d); }
 
-// How many clusters of 2, 4 and 8 CTAs fit the device at once; asked once for each device.
+// The counts of Fp8Clusters for the current device; with the first question, each kernel is allowed its shared memory.
 template <bool WGRAD, typename OUT>
-cudaError_t f8_clusters(int (&clusters)[3]) {
-  static int known[64][3] = {};
+cudaError_t f8_clusters(int (&clusters)[2]) {
+  static Fp8Clusters known;
   int dev = 0;
-  cudaError_t err = cudaGetDevice(&dev);
+  const cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (known[dev][0] == 0) {
+  return known.get<cudaError_t>(dev, clusters, [](int (&counts)[2]) {
     auto kern = fp8_gemm_kernel<WGRAD, true, false, OUT>;
-    for (auto other : {fp8_gemm_kernel<WGRAD, false, false, OUT>, fp8_gemm_kernel<WGRAD, false, true, OUT>}) {
-      err = cudaFuncSetAttribute(other, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)f8_smem(FP8_MAX_E));
+    for (auto each : {kern, fp8_gemm_kernel<WGRAD, false, false, OUT>, fp8_gemm_kernel<WGRAD, false, true, OUT>}) {
+      const cudaError_t err = cudaFuncSetAttribute(each, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)f8_smem(FP8_MAX_E));
       if (err != cudaSuccess) return err;
     }
-    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)f8_smem(FP8_MAX_E));
-    for (int i = 2; i >= 0 && err == cudaSuccess; --i) {  // the first entry last: it says that the others are there
+    for (int i = 0; i < 2; ++i) {
       cudaLaunchConfig_t cfg{};
       cudaLaunchAttribute attr[1];
       attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = 2u << i;
+      attr[0].val.clusterDim.x = 4u << i;
       attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
       cfg.blockDim = dim3(F8_THREADS, 1, 1);
-      cfg.gridDim = dim3(64u << i, 1, 1);
+      cfg.gridDim = dim3(128u << i, 1, 1);
       cfg.dynamicSmemBytes = f8_smem(FP8_MAX_E);
       cfg.attrs = attr;
       cfg.numAttrs = 1;
-      int n = 0;
-      err = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
-      known[dev][i] = std::max(1, n);
+      const cudaError_t err = cudaOccupancyMaxActiveClusters(&counts[i], kern, &cfg);
+      if (err != cudaSuccess) return err;
     }
-    if (err != cudaSuccess) return err;
-  }
-  for (int i = 0; i < 3; ++i) clusters[i] = known[dev][i];
-  return cudaSuccess;
-}
-
-// The columns of a chunk (g.nmax) and the pairs that share a tile (g.splits), by the time of the pair that has most to do:
-// about 200 + 4 n cycles for each block of n columns (measured: 1,200 at 256, 700 at 128, 450 at 64), a tile's start and end about
-// 3,000, the joining of splits 3,000 + 20 n.  `each`: columns of each of the groups; where the groups' sizes are not known here
-// (`known` false) it is their average, and half a chunk a group is added.  Splits are taken only where every tile has its
-// own cluster and all clusters fit at once (36 of 4 CTAs, 15 of 8 on GB300), and the sums fit the first pair's stages.  Returns
-// the tiles at most.
-int64_t f8_plan(Fp8GemmArgs& g, int n_sm, int64_t nkb, int64_t groups, int64_t each, bool known, const int (&clusters)[3]) {
-  const int64_t pairs = std::max(1, n_sm / 2);
-  int64_t best = INT64_MAX, tiles = 0;
-  for (int nmax = 256; nmax >= 32; nmax /= 2)
-    for (int splits = 1; splits <= 4; splits *= 2) {
-      const int64_t whole = (each + nmax - 1) / nmax;
-      const int64_t chunks = known ? groups * whole : std::max(groups, groups * (2 * each + nmax) / (2 * nmax));
-      const int64_t most = (known ? chunks : groups * whole + g.E) * g.MT;
-      if (splits > 1 && (most > clusters[splits / 2] || nkb < 4 * splits || (splits - 1) * nmax * 512 > F8_STAGES * F8_STAGE)) continue;
-      const int64_t n = std::max<int64_t>(16, groups * each / chunks);
-      const int64_t waves = (chunks * g.MT * splits + pairs - 1) / pairs;
-      const int64_t cost = waves * ((nkb + splits - 1) / splits * (200 + 4 * n) + 3000) + (splits > 1 ? 3000 + 20 * n : 0);
-      if (cost < best) {
-        best = cost;
-        tiles = most;
-        g.nmax = nmax;
-        g.splits = splits;
-      }
-    }
-  return tiles;
+    return cudaSuccess;
+  });
 }
 
 template <bool WGRAD, typename OUT>
@@ -807,10 +776,13 @@ cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, bool bf16_out, int n_sm, c
   g.wide_out = g.mixed && f8_wide(a.out, a.out_stride, a.N, bf16_out);
   g.status = a.status;
   const int64_t groups = std::min<int64_t>(a.E, a.R);  // that can have rows
-  int clusters[3];
+  int clusters[2];
   const cudaError_t err = bf16_out ? f8_clusters<false, __nv_bfloat16>(clusters) : f8_clusters<false, float>(clusters);
   if (err != cudaSuccess) return err;
-  int64_t tiles = f8_plan(g, n_sm, g.nkb, groups, (a.R + groups - 1) / groups, a.E == 1, clusters);
+  const Fp8Plan plan = f8_plan(a.E, g.MT, n_sm, g.nkb, groups, (a.R + groups - 1) / groups, a.E == 1, clusters, F8_STAGES * F8_STAGE);
+  g.nmax = plan.nmax;
+  g.splits = plan.splits;
+  int64_t tiles = plan.tiles;
   if (a.E > 1) tiles = ((a.R + g.nmax - 1) / g.nmax + a.E) * g.MT;  // at most, whatever the groups' sizes
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
   g.magic_per = f8_magic(g.MT);
@@ -841,10 +813,13 @@ cudaError_t launch_fp8_weight_grad(const Fp8WeightGradArgs& a, bool bf16_out, in
   g.mixed = a.H % 32 == 0;
   g.wide_out = g.mixed && f8_wide(a.out, a.H, a.H, bf16_out);
   g.status = a.status;
-  int clusters[3];
+  int clusters[2];
   const cudaError_t err = bf16_out ? f8_clusters<true, __nv_bfloat16>(clusters) : f8_clusters<true, float>(clusters);
   if (err != cudaSuccess) return err;
-  const int64_t tiles = f8_plan(g, n_sm, (a.R / 128 + a.E - 1) / a.E, a.E, a.N, true, clusters);
+  const Fp8Plan plan = f8_plan(a.E, g.MT, n_sm, (a.R / 128 + a.E - 1) / a.E, a.E, a.N, true, clusters, F8_STAGES * F8_STAGE);
+  g.nmax = plan.nmax;
+  g.splits = plan.splits;
+  const int64_t tiles = plan.tiles;
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
   const int64_t nc = (a.N + g.nmax - 1) / g.nmax;
   g.magic_per = f8_magic(nc * g.MT);
