@@ -582,7 +582,8 @@ mok_status mok_fp8_quantize_weights(const mok_fp8_weights_desc* desc, const void
  * offsets[e] <= r < offsets[e+1] (as for mok_fp8_quantize; NULL with E = 1: all R rows).  x [R][K] and x_scale as q and
  * scale of mok_fp8_quantize, w [E][N][K] and w_scale as of mok_fp8_quantize_weights: q and scale for x W^T, qt and
  * qt_scale for dy W.  The sums of a block are formed by the tensor cores, the blocks are added in f32, in a fixed
- * order.  out f32 or bf16 (out_type, rounded once), out_stride elements between rows (0 = N); rows of no group are
+ * order.  The two scales' product may leave f32's range where the result does not (a block at the least scale, 2^-110 / 448, may
+ * be off by 2^-125 then).  out f32 or bf16 (out_type, rounded once), out_stride elements between rows (0 = N); rows of no group are
  * left as they were.  device_status as for mok_gather_rows; it also takes a wait that ran out (MOK_ERR_TIMEOUT). */
 typedef struct {
   int64_t R, N, K;

@@ -9,6 +9,8 @@ namespace mok {
 
 constexpr int FP8_BLOCK = 128;
 constexpr int FP8_MAX_E = 1024;
+// The least that a block's largest magnitude counts as, 2^-110, and the scale that comes of it: of a block of zeros.
+constexpr float FP8_LEAST = 7.703719777548943e-34f, FP8_LEAST_SCALE = (float)(7.703719777548943e-34 / 448);
 
 enum Fp8Source { FP8_PLAIN = 0, FP8_SWIGLU = 1, FP8_SWIGLU_GRAD = 2 };
 

@@ -18,7 +18,7 @@
 //
 // Roles of both CTAs of a pair: warp 0 TMA producer, warp 1 MMA issuer (even CTA), warp 2 the scales, warps 4 to 11 epilogue
 // (warp w reads TMEM lane quarter w % 4; the two warps of a quarter take alternate 32-column pieces).  The scales' warp
-// reads four blocks' scales at a time, multiplies the two where one is the same for a whole 128-row tile (product) and puts
+// reads four blocks' scales at a time, multiplies the two where one is the same for a whole 128-row tile (product; see f8_apart) and puts
 // them into a ring in shared memory, in the order in which the epilogue's lanes take them.  All waits and loops are a whole
 // warp's, one elected thread issues: addresses and descriptors then stay in uniform registers.  Barriers: full[s] in the even
 // CTA (one arrival with both CTAs' bytes), empty[s] and pfull[a] in both (multicast commits), pempty[a] in the even CTA (16
@@ -68,7 +68,10 @@ constexpr int F8_GROUP = 4;  // K blocks whose scales share a slot
 constexpr int F8_A_BYTES = 128 * 128;
 constexpr int F8_B_BYTES = 128 * 128;
 constexpr int F8_STAGE = F8_A_BYTES + F8_B_BYTES;
-constexpr int F8_SLOT_BLOCK = 256 + 128;  // floats of a block in a slot: the columns' scales, and (weight grad) the lanes'
+// Words of a block in a slot: the columns' scales, and the lanes' (weight grad) or (product) which columns meet the weights'
+// scale apart (a bit for each), that scale, and whether there may be any.
+constexpr int F8_SLOT_BLOCK = 256 + 128;
+constexpr int F8_APART = 256, F8_APART_SCALE = 264, F8_APART_ANY = 265;
 constexpr int F8_SLOT = F8_GROUP * F8_SLOT_BLOCK * 4;
 constexpr int F8_EPI_WARPS = 8;
 constexpr int F8_THREADS = 32 * (4 + F8_EPI_WARPS);
@@ -179,6 +182,17 @@ __device__ __forceinline__ int f8_blocks_at_once(int n) { return n <= 64 ? 4 : n
 // Where column c (of 32) has its scale: the four columns 8 g + 2 t, + 1 of two neighbouring g that a lane (t = lane % 4) holds
 // follow each other.
 __device__ __forceinline__ int f8_scale_at(int c) { return (c >> 4) * 16 + ((c >> 1) & 3) * 4 + ((c >> 3) & 1) * 2 + (c & 1); }
+
+// The two scales of a product go to the epilogue as one factor, unless that is no normal f32: it would lose bits that the block's sum
+// may still bring back, or be infinite beside a sum of 0.  Such a column keeps its row's scale, and its sums are
+// multiplied with the weights' one first ("apart"; exact to f32's rounding for scales from 2^-119 on).  Scales of 0, and the quantisers'
+// least one, which stands for zeros (masked tokens' gradients, weights that are off), are left out: what little is lost there
+// stays below 2^-125 a block.  At least F8_NORMALS for scales that meet apart.
+constexpr uint32_t F8_NORMALS = 0x7f000000u;
+__device__ __forceinline__ bool f8_zeros(float scale) { return scale == 0.0f || scale == FP8_LEAST_SCALE; }
+__device__ __forceinline__ uint32_t f8_apart(float row, float weights) {
+  return f8_zeros(row) || f8_zeros(weights) ? 0 : (__float_as_uint(row * weights) & 0x7fffffffu) - 0x00800000u;
+}
 
 __device__ __forceinline__ void f8_put4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
 __device__ __forceinline__ void f8_put4(__nv_bfloat16* p, float4 v) {
@@ -429,6 +443,13 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
       for (int g = pair; g < total && ok; g += npairs) {
         const Fp8Tile t = f8_tile<WGRAD, SPLIT>(g, split, args, at0, at0 + 4 * (args.E + 1), at0 + 8 * (args.E + 1));
         const int a_row = t.m * 256 + 128 * (int)rank;
+        auto weights_scale = [&](int64_t kb) {  // product: of the CTA's 128 rows
+          const int tiles = (args.NM + 127) >> 7;
+          return a_row < args.NM ? __ldg(args.a_scale + ((int64_t)t.e * tiles + (a_row >> 7)) * args.nkb + kb) : 0.0f;
+        };
+        auto rows_scale = [&](int64_t kb, int c) {
+          return c < t.cols ? __ldg(args.b_scale + kb * args.b_ld + t.col0 + c) : 0.0f;
+        };
         for (int kb0 = 0; kb0 < t.nkb; kb0 += F8_GROUP) {
           float b[F8_GROUP][8], a4[F8_GROUP][4];
   #pragma unroll
@@ -441,14 +462,21 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                 a4[j][i] = r < args.NM ? __ldg(args.a_scale + kb * args.NM + r) : 0.0f;
               }
             } else {
-              const int tiles = (args.NM + 127) >> 7;
-              a4[j][0] = a_row < args.NM ? __ldg(args.a_scale + ((int64_t)t.e * tiles + (a_row >> 7)) * args.nkb + kb) : 0.0f;
+              a4[j][0] = weights_scale(kb);
             }
   #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const int c = i * 32 + lane;
-              b[j][i] = c < t.cols ? __ldg(args.b_scale + kb * args.b_ld + t.col0 + c) : 0.0f;
+              b[j][i] = rows_scale(kb, i * 32 + lane);
             }
+          }
+          bool apart = false;  // of any column
+          if (!WGRAD) {
+            uint32_t worst = 0;
+  #pragma unroll
+            for (int j = 0; j < F8_GROUP; ++j)
+  #pragma unroll
+              for (int i = 0; i < 8; ++i) worst = max(worst, f8_apart(b[j][i], a4[j][0]));
+            apart = __any_sync(0xffffffffu, worst >= F8_NORMALS);
           }
             ok = __all_sync(0xffffffffu, f8_wait(sempty_bar(q), q_phase ^ 1, abort_flag, args.status, SITE_FP8_SCALES));
           if (!ok) break;
@@ -461,6 +489,27 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             if (WGRAD) {
 #pragma unroll
               for (int i = 0; i < 4; ++i) sts1(s + 4 * (256 + i * 32 + lane), a4[j][i]);
+            }
+          }
+          if (!WGRAD) {
+            const uint32_t s = slots0 + q * F8_SLOT;
+            if (lane < F8_GROUP) sts1(s + lane * (F8_SLOT_BLOCK * 4) + 4 * F8_APART_ANY, __uint_as_float(apart));
+            if (apart) {  // rare: the scales are read again, which costs no registers
+#pragma unroll 1
+              for (int j = 0; j < F8_GROUP; ++j) {
+                const int64_t kb = t.kb0 + min(kb0 + j, t.nkb - 1);
+                const float w = weights_scale(kb);
+                const uint32_t to = s + j * (F8_SLOT_BLOCK * 4);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const float r = rows_scale(kb, i * 32 + lane);
+                  const bool mine = f8_apart(r, w) >= F8_NORMALS;
+                  const uint32_t bits = __ballot_sync(0xffffffffu, mine);
+                  if (mine) sts1(to + 4 * (i * 32 + f8_scale_at(lane)), r);
+                  if (lane == 0) sts1(to + 4 * (F8_APART + i), __uint_as_float(bits));
+                }
+                if (lane == 0) sts1(to + 4 * F8_APART_SCALE, w);
+              }
             }
           }
           __syncwarp();
@@ -483,7 +532,10 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     const bool leader = elect_one();
     int acc = 0, q = 0;
     uint32_t acc_phase = 0, q_phase = 0;
-    bool ok = true, ready = false;
+    bool ok = true;
+    // ready: the next accumulator and the slot of its scales have been seen complete, without columns apart.  Where they have not,
+    // they are waited for, and `apart` is read again with the slot.
+    bool ready = false, apart = false;
     for (int g = pair; g < total && ok; g += npairs) {
       const Fp8Tile t = f8_tile<WGRAD, SPLIT>(g, split, args, at0, at0 + 4 * (args.E + 1), at0 + 8 * (args.E + 1));
       // sum[s]: piece s / 2, TMEM lanes 16 (s % 2) of the quarter: [g][row lane / 4, + 8], columns 2 t, 2 t + 1 of group g
@@ -498,15 +550,37 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
       auto run = [&](auto pieces, auto at_once) {
         constexpr int NP = decltype(pieces)::value, G = decltype(at_once)::value, S = 2 * NP;
         for (int kb = 0; kb < t.nkb; kb += G) {
-          if ((kb & (F8_GROUP - 1)) == 0)
-            ok = __all_sync(0xffffffffu, f8_wait(sfull_bar(q), q_phase, abort_flag, args.status, SITE_FP8_SCALES));
-          if (!ready)
-            ok = __all_sync(0xffffffffu,
-                            f8_wait(pfull_bar(acc), acc_phase, abort_flag, args.status, SITE_GEMM_EPI_TMEM_FULL) && ok);
-          if (!ok) break;
-          tc_fence_after();
           const uint32_t s0 = slots0 + q * F8_SLOT + (kb & (F8_GROUP - 1)) * (F8_SLOT_BLOCK * 4);
           const int blocks = min(G, t.nkb - kb);
+          if (!ready) {
+            if ((kb & (F8_GROUP - 1)) == 0) {
+              ok = __all_sync(0xffffffffu, f8_wait(sfull_bar(q), q_phase, abort_flag, args.status, SITE_FP8_SCALES));
+              if (!WGRAD) apart = __any_sync(0xffffffffu, lds1i(s0 + 4 * F8_APART_ANY));
+            }
+            ok = __all_sync(0xffffffffu,
+                            f8_wait(pfull_bar(acc), acc_phase, abort_flag, args.status, SITE_GEMM_EPI_TMEM_FULL) && ok);
+            if (!WGRAD && apart && ok) {  // the weights' scale onto the sums of columns that meet it apart, in place
+              tc_fence_after();
+#pragma unroll 1
+              for (int i = 0; i < blocks * S; ++i) {
+                const int g8 = i / S, p = i - g8 * S;
+                const uint32_t s = s0 + g8 * (F8_SLOT_BLOCK * 4);
+                const uint32_t at = tlane + acc * 256 + g8 * (256 / G) + (p >> 1) * 64 + (p & 1) * (16u << 16);
+                const uint32_t bits = (uint32_t)lds1i(s + 4 * (F8_APART + 2 * (p >> 1) + side)) >> (2 * (lane & 3));
+                const float ws = lds1(s + 4 * F8_APART_SCALE);
+                uint32_t v[16];
+                tmem_ld_16x256b_x4(at, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  if (bits >> (8 * (j >> 2) + (j & 1)) & 1) v[j] = __float_as_uint(__uint_as_float(v[j]) * ws);
+                tmem_st_16x256b_x4(at, v);
+                tmem_wait_st();
+              }
+            }
+          }
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll
           for (int g8 = 0; g8 < G; ++g8) {
             if (G == 1 || g8 < blocks) {
@@ -529,10 +603,15 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
               }
               auto done = [&]() {  // the accumulator is in registers
                 tc_fence_before();
-                const bool next = mbar_test_wait(pfull_bar(acc ^ 1), acc_phase ^ (uint32_t)acc);
+                bool next = mbar_test_wait(pfull_bar(acc ^ 1), acc_phase ^ (uint32_t)acc);
                 __syncwarp();
                 if (leader) mbar_arrive_cluster_relaxed(pempty0_cl + 8u * acc);
-                ready = __all_sync(0xffffffffu, next);
+                if ((kb & (F8_GROUP - 1)) + G >= F8_GROUP || kb + G >= t.nkb) {
+                  const int q1 = q + 1 == SLOTS ? 0 : q + 1;
+                  next = mbar_test_wait(sfull_bar(q1), q_phase ^ (uint32_t)(q1 == 0)) && next;
+                  if (!WGRAD) apart = lds1i(slots0 + q1 * F8_SLOT + 4 * F8_APART_ANY) != 0;
+                }
+                ready = __all_sync(0xffffffffu, next && (WGRAD || !apart));
               };
               if (S == 0 && final) done();
 #pragma unroll

@@ -38,7 +38,7 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) { return __ffma2_rn(a, b, c
 
 constexpr int THREADS = 256;       // rows alone
 constexpr int TILE_THREADS = 512;  // 128 x 128 tiles: 32 half-warps of 4 rows
-constexpr float LEAST = 7.703719777548943e-34f;  // 2^-110
+constexpr float LEAST = FP8_LEAST;
 constexpr float BIG = 3.4028234663852886e38f;
 
 // Off by a unit in the last place at most; 0 for what would be below 2^-126.

@@ -531,6 +531,72 @@ def test_product(counts, N, K, dtype):
     assert (torch.as_strided(out2, (R - 1, 3), (N + 3, 1), N) == 3.0).all()
 
 
+# counts, N, K: tiles of every width (16 to 256 columns, some of them with splits), f32's packed sums too
+SCALED = [([1], 130, 300), ([70, 0, 5], 264, 1111), ([129], 256, 512), ([513, 250], 260, 900), ([33] * 5, 1024, 200),
+          ([40], 130, 6000), ([1000], 384, 1500)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("counts,N,K", SCALED, ids=lambda v: str(v)[:24])
+def test_product_of_scales_out_of_range(counts, N, K, dtype):
+    """A row's scale times a weights' one beyond f32's normal range on either side, beside rows where it is not.  Where the scales
+    meet apart, two of the three roundings at the top are of numbers that may be subnormal: off by 2^-150 each and block;
+    out's own rounding by half its smallest number."""
+    rng = np.random.default_rng(sum(counts) + K)
+    E, R = len(counts), sum(counts)
+    offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    blocks = -(-K // 128)
+    x, w = random_e4m3(rng, (R, K)), random_e4m3(rng, (E, N, K))
+    kind = rng.integers(0, 5, R)       # ordinary rows, blocks of nearly nothing, small rows, rows of zeros, smallest elements
+    size = np.array([1.0, 2.0 ** -112, 2.0 ** -92, 2.0 ** 115, 2.0 ** 109])[kind]
+    kind[0], size[0] = 4, 2.0 ** 109
+    each = scales(rng, (blocks, R))
+    xs = each * cuda(size, F32)
+    zeros, least = cuda(np.nonzero(kind == 3)[0]), cuda(np.nonzero(kind == 4)[0])
+    x.view(torch.uint8)[zeros] = 0
+    x.view(torch.uint8)[least] &= 0x81  # zeros, and elements of 2^-9
+    small = rng.integers(0, 3, (E, -(-N // 128), blocks))
+    ws = scales(rng, small.shape) * cuda(np.array([1.0, 2.0 ** -32, 2.0 ** 32])[small], F32)
+    # large scales have small elements: below 2^-3
+    large = np.repeat(np.repeat(small == 2, 128, 1), 128, 2)[:, :N, :K]
+    w.view(torch.uint8)[cuda(large)] &= 0x9f
+    want, terms = O.product(f64(x), f64(xs), f64(w), f64(ws), offsets)
+    assert (np.abs(want)[kind != 4] < 3e38).all()
+    weights = mok.Fp8Weights.of(w, ws)
+    got = f64(weights.matmul(x, xs, cuda(offsets), dtype=dtype))
+    tiny = (2 * blocks + 1) * 2.0 ** -150 + (2.0 ** -134 if dtype == BF else 2.0 ** -150)
+    fits = np.abs(terms) < 3e38
+    bound = (132 + blocks) * 2 * U * terms + HALF[dtype] * np.abs(want) + tiny
+    assert fits[kind == 4].any() and (np.abs(got - want) <= bound)[fits].all()
+    assert weights.status() == (0, 0)
+    # an ordinary row has the same bits whatever its neighbours are
+    assert np.array_equal(f64(weights.matmul(x, each, cuda(offsets), dtype=dtype))[kind == 0], got[kind == 0])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("counts,N,K", SCALED, ids=lambda v: str(v)[:24])
+def test_product_of_least_scales(counts, N, K, dtype):
+    """Rows and weights at the quantisers' least scale, or at 0: their factors may be subnormal, off by 2^-150 and a block's sum by
+    that times 128 x 448^2 < 2^24.7."""
+    rng = np.random.default_rng(sum(counts) + N)
+    E, R = len(counts), sum(counts)
+    offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    blocks = -(-K // 128)
+    least = float(np.float32(2.0 ** -110 / 448))
+    pick = lambda t: torch.where(cuda(rng.random(t.shape) < 0.3), cuda(rng.choice([least, 0.0], t.shape), F32), t)  # noqa: E731
+    x, xs = random_e4m3(rng, (R, K)), pick(scales(rng, (blocks, R)))
+    w, ws = random_e4m3(rng, (E, N, K)), pick(scales(rng, (E, -(-N // 128), blocks)))
+    xs[:, -1] = least
+    want, terms = O.product(f64(x), f64(xs), f64(w), f64(ws), offsets)
+    got = f64(mok.Fp8Weights.of(w, ws).matmul(x, xs, cuda(offsets), dtype=dtype))
+    bound = (132 + blocks) * 2 * U * terms + HALF[dtype] * np.abs(want) + blocks * 2.0 ** -125
+    assert (np.abs(got - want) <= bound).all()
+    zeros = torch.zeros(R, K, device="cuda")
+    q = mok.fp8_quantize(zeros)
+    assert (q["scale"] == least).all()
+    assert (mok.Fp8Weights.of(w, ws).matmul(q["q"], q["scale"], cuda(offsets), dtype=dtype) == 0).all()
+
+
 @pytest.mark.parametrize("R,N,K", [(1, 64, 256), (5, 1000, 100), (16, 256, 2048), (100, 130, 384), (257, 700, 1300), (1, 520, 7168), (64, 260, 4100),
                                    (200, 96, 3000)])
 def test_product_without_groups(R, N, K):
