@@ -217,17 +217,23 @@ def merge_rows(o: torch.Tensor, row_of: torch.Tensor, k: int, gates: Optional[to
     return out
 
 
-def merge_rows_backward(dy: torch.Tensor, o: torch.Tensor, row_of: torch.Tensor, gates: torch.Tensor,
+def merge_rows_backward(dy: torch.Tensor, o: torch.Tensor, row_of: torch.Tensor, gates: Optional[torch.Tensor] = None,
                         out: Optional[Dict[str, torch.Tensor]] = None, device_status: Optional[torch.Tensor] = None,
                         stream=None) -> Dict[str, torch.Tensor]:
     """Gradient of ``merge_rows`` (mok_merge_rows_backward): {"do": [R][H], "dgates": f32 [T][k]}.  Rows of "do" that
-    no assignment names are left as they were (zeros where it is made here)."""
+    no assignment names are left as they were (zeros where it is made here).  ``out``: buffers, without "dgates" where
+    that is not wanted."""
     kind, dtype = _elem(dy, "dy"), dy.dtype
     device = _device(dy, "dy")
-    if not isinstance(gates, torch.Tensor) or gates.dim() != 2:
-        raise ValueError("gates: expected a float32 matrix")
     T, H = dy.shape
-    k = gates.shape[1]
+    if gates is not None and (not isinstance(gates, torch.Tensor) or gates.dim() != 2):
+        raise ValueError("gates: expected a float32 matrix")
+    if gates is not None:
+        k = gates.shape[1]
+    else:
+        if not isinstance(row_of, torch.Tensor) or row_of.dim() != 1 or (row_of.shape[0] % T if T else row_of.shape[0]):
+            raise ValueError(f"row_of: expected an int32 vector of T k = {T} k rows")
+        k = row_of.shape[0] // T if T else 1
     R = o.shape[0] if isinstance(o, torch.Tensor) and o.dim() == 2 else -1
     yp, ys = _rows(dy, (T, H), dtype, "dy", device)
     rp, rs = _rows(o, (R, H), dtype, "o", device)
@@ -235,14 +241,16 @@ def merge_rows_backward(dy: torch.Tensor, o: torch.Tensor, row_of: torch.Tensor,
         with _on(stream):
             out = {"do": torch.zeros((R, rs or H), dtype=dtype, device=dy.device)[:, :H],
                    "dgates": torch.empty((T, k), dtype=torch.float32, device=dy.device)}
+    elif "do" not in out:
+        raise ValueError('out: expected "do", and "dgates" where it is wanted')
     dp, ds = _rows(out["do"], (R, H), dtype, 'out["do"]', device)
     if ds != rs and (ds or H) != (rs or H):
         raise ValueError(f'out["do"]: rows {ds or H} elements apart, those of o {rs or H}')
     d = RowsDesc(T, R, H, ys, rs, k, kind)
     code = _fn("mok_merge_rows_backward", RowsDesc, 7)(
         d, yp, rp, _packed(row_of, (T * k,), torch.int32, "row_of", device),
-        _packed(gates, (T, k), torch.float32, "gates", device), dp,
-        _packed(out["dgates"], (T, k), torch.float32, 'out["dgates"]', device),
+        _optional(gates, (T, k), torch.float32, "gates", device), dp,
+        _optional(out.get("dgates"), (T, k), torch.float32, 'out["dgates"]', device),
         _optional(device_status, (2,), torch.int32, "device_status", device), _queue(stream, device))
     if code:
         _check("mok_merge_rows_backward", code)

@@ -988,6 +988,22 @@ def test_repeated_calls_give_the_same_bits():
         assert all(torch.equal(a, b) for a, b in zip(first, out))
 
 
+def test_merge_gradient_without_gates_and_without_their_gradient():
+    rng = np.random.default_rng(21)
+    T, k, E, H = 30, 3, 5, 72
+    _, row, _ = table(rng, T, k, E, dropped=0.2)
+    dy, dy64 = values(rng, (T, H), BF)
+    o, o64 = values(rng, (T * k, H), BF)
+    ones = torch.ones(T, k).cuda()
+    want, got = mok.merge_rows_backward(dy, o, cuda(row), ones), mok.merge_rows_backward(dy, o, cuda(row))
+    assert torch.equal(got["do"], want["do"]) and torch.equal(got["dgates"], want["dgates"])
+    only = {"do": torch.zeros_like(o)}
+    assert mok.merge_rows_backward(dy, o, cuda(row), out=only) is only and set(only) == {"do"}
+    assert torch.equal(only["do"], want["do"])
+    none = torch.empty(0, dtype=torch.int32).cuda()
+    assert mok.merge_rows_backward(dy[:0], o, none)["do"].shape == o.shape
+
+
 def test_the_binding_refuses(cuda_ok):
     c = lambda *s, dt=F32: torch.zeros(s, dtype=dt, device="cuda")  # noqa: E731
     i = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
