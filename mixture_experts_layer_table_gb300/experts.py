@@ -300,6 +300,11 @@ def fp8_quantize(x: torch.Tensor, source: str = "plain", grad: Optional[torch.Te
                 out |= {"q": empty_e4m3(max(0, R), C, device=x.device), "scale": new(_blocks(C), max(0, R))}
             if E:
                 out |= {"qt": empty_e4m3(C, fp8_columns(R, E), device=x.device), "qt_scale": new(R // 128 + E, C)}
+    for elements, scale in (("q", "scale"), ("qt", "qt_scale")):
+        if (elements in out) != (scale in out):
+            raise ValueError(f'out: "{elements}" and "{scale}" come together')
+    if "q" in out and not rows:
+        raise ValueError('out["q"] is given, but no rows are wanted')
     d = Fp8QuantizeDesc(R, C, T, 0, 0, 0, 0, 0, E, k, SOURCES[source], kind)
     xp, d.x_stride = _rows(x, (T, width), dtype, "x", device)
     gp = qp = sp = tp = tsp = None
@@ -354,6 +359,9 @@ class Fp8Weights:
             raise ValueError("q: expected [E][N][K] or [N][K]")
         if (qt is None) != (qt_scale is None):
             raise ValueError("qt and qt_scale come together")
+        for t, name in ((scale, "scale"), (qt, "qt"), (qt_scale, "qt_scale")):
+            if t is not None and not isinstance(t, torch.Tensor) or name == "scale" and t is None:
+                raise ValueError(f"{name}: expected a tensor, got {type(t).__name__}")
         if q.dim() == 2:
             q, scale = q.unsqueeze(0), scale.unsqueeze(0)
             qt, qt_scale = (None, None) if qt is None else (qt.unsqueeze(0), qt_scale.unsqueeze(0))

@@ -1004,6 +1004,22 @@ def test_merge_gradient_without_gates_and_without_their_gradient():
     assert mok.merge_rows_backward(dy[:0], o, none)["do"].shape == o.shape
 
 
+def test_the_binding_refuses_half_of_a_pair():
+    c = lambda *s, dt=F32: torch.zeros(s, dtype=dt, device="cuda")  # noqa: E731
+    i = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    x, e = c(6, 32), mok.empty_e4m3
+    for call in (lambda: mok.fp8_quantize(x, out={"q": e(6, 32)}), lambda: mok.fp8_quantize(x, out={"scale": c(1, 6)}),
+                 lambda: mok.fp8_quantize(x, offsets=i(2), out={"qt": e(32, 128)}),
+                 lambda: mok.fp8_quantize(x, offsets=i(2), out={"q": e(6, 32), "scale": c(1, 6), "qt_scale": c(1, 32)}),
+                 lambda: mok.fp8_quantize(x, out={"q": e(6, 32), "scale": c(1, 6)}, rows=False),
+                 lambda: mok.merge_rows_backward(c(4, 32), c(8, 32), i(8), c(4, 2), out={"dgates": c(4, 2)}),
+                 lambda: mok.merge_rows_backward(c(4, 32), c(8, 32), i(9)), lambda: mok.merge_rows_backward(c(0, 32), c(8, 32), i(9)),
+                 lambda: mok.merge_rows_backward(c(4, 32), c(8, 32), None),
+                 lambda: mok.Fp8Weights.of(e(48, 32), None), lambda: mok.Fp8Weights.of(e(48, 32), 1.0)):
+        with pytest.raises(ValueError):
+            call()
+
+
 def test_the_binding_refuses(cuda_ok):
     c = lambda *s, dt=F32: torch.zeros(s, dtype=dt, device="cuda")  # noqa: E731
     i = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
