@@ -653,6 +653,57 @@ def test_bad_offsets_stay_in_the_tensors():
     torch.cuda.synchronize()
 
 
+class Fenced:
+    """A [rows][width] tensor inside of a larger buffer: bytes of 0x5a in front, behind and between the rows."""
+
+    def __init__(self, shape, dtype, between=0):
+        rows, width = shape
+        item = torch.empty(0, dtype=dtype).element_size()
+        ld = -(-width * item // 16) * 16 + between if between else width * item
+        self.big = torch.full((4096 + rows * ld + 4096,), 0x5a, dtype=torch.uint8).cuda()
+        inside = torch.as_strided(self.big, (rows, width * item), (ld, 1), 4096)
+        self.t = torch.as_strided(self.big.view(dtype), (rows, width), (ld // item, 1), 4096 // item)
+        self.mask = torch.ones_like(self.big, dtype=torch.bool)
+        torch.as_strided(self.mask, inside.shape, inside.stride(), 4096).fill_(False)
+
+    def intact(self):
+        return bool((self.big[self.mask] == 0x5a).all())
+
+
+BAD_TABLES = [[0, 30, 20, 60, 2 ** 31 - 1], [-5, 10, 2 ** 30, 2 ** 30, 100], [-2 ** 31, 0, 0, 0, 500], [100, 0, 100, 0, 100],
+              [0, 400, 0, 400, 0], [300, 200, 100, 0, -100], [2 ** 31 - 1] * 5, [-1] * 5, [0, 299, 1, 299, 299]]
+
+
+@pytest.mark.parametrize("bad", BAD_TABLES, ids=str)
+def test_bad_offsets_write_nothing_beside_the_outputs(bad):
+    """As above for the outputs: what lies in front of them, behind them and between their rows stays as it was."""
+    rng = np.random.default_rng(8)
+    R, N, K, E = 300, 70, 200, 4
+    offsets = cuda(np.array(bad, np.int32))
+    x, xs = random_e4m3(rng, (R, K)), scales(rng, (2, R))
+    weights = mok.Fp8Weights.of(random_e4m3(rng, (E, N, K)), scales(rng, (E, 1, 2)))
+    P = mok.fp8_columns(R, E)
+    fences = []
+
+    def fenced(*a, **kw):
+        fences.append(Fenced(*a, **kw))
+        return fences[-1].t
+
+    for dtype in (BF, F32):
+        weights.matmul(x, xs, offsets, out=fenced((R, N), dtype, between=32))
+        for source, width in (("plain", N), ("swiglu", 2 * N), ("swiglu_grad", N), ("swiglu_grad", 512)):
+            C = width // 2 if source == "swiglu" else width
+            src, _ = values(rng, (R, width), dtype)
+            grad = values(rng, (R, C // 2), dtype)[0] if source == "swiglu_grad" else None
+            out = {"q": fenced((R, C), X.E4M3, between=16), "scale": fenced((-(-C // 128), R), F32, between=16),
+                   "qt": fenced((C, P), X.E4M3, between=16), "qt_scale": fenced((P // 128, C), F32)}
+            mok.fp8_quantize(src, source=source, grad=grad, offsets=offsets, out=out)
+        good = mok.fp8_quantize(src, offsets=cuda(np.array([0, 100, 100, 200, R], np.int32)), rows=False)
+        dw = fenced((E * 512, 512), dtype)
+        mok.fp8_weight_grad(good["qt"], good["qt_scale"], good["qt"], good["qt_scale"], offsets, out=dw.view(E, 512, 512))
+    assert all(f.intact() for f in fences) and weights.status() == (0, 0) == mok.fp8_status()
+
+
 def test_as_many_groups_as_there_may_be():
     rng = np.random.default_rng(12)
     E, N, K = 1024, 40, 150
