@@ -305,7 +305,9 @@ cudaError_t gather(const RowsArgs& a, cudaStream_t st) {
 template <typename T, int BYTES, int KMAX>
 cudaError_t merge_k(const RowsArgs& a, cudaStream_t st) {
   const int pieces = (int)(a.H * (int64_t)sizeof(T) / BYTES);
-  if (BYTES == (int)sizeof(T) && pieces >= 96 && a.T >= 512) {  // rows long enough and tokens enough to fill the SMs a block each
+  // A block a token where rows are long enough and tokens enough to fill the SMs (k = 8, f32: 4,096 tokens of 257 elements 11.8 -> 7.5
+  // us, of 65 4.6 -> 5.5; of 1,111 elements 1,024 tokens 12.6 -> 5.6, 128 3.2 -> 4.4; bf16 of 1,111: 1,024 12.8 -> 7.8, 500 7.2 both)
+  if (BYTES == (int)sizeof(T) && pieces >= 96 && a.T >= 512) {
     if (a.T > INT32_MAX) return cudaErrorInvalidValue;
     expert_merge_token_kernel<T, BYTES, KMAX><<<(unsigned)a.T, 128, 0, st>>>(a, pieces);
     return cudaGetLastError();
@@ -328,7 +330,8 @@ cudaError_t merge(const RowsArgs& a, cudaStream_t st) {
 template <typename T, int BYTES, int KMAX>
 cudaError_t merge_backward_k(const RowsArgs& a, int n_sm, cudaStream_t st) {
   const int pieces = (int)(a.H * (int64_t)sizeof(T) / BYTES);
-  // few tokens: a block of as many threads as shorten the row
+  // few tokens: a block of as many threads as shorten the row (k = 8 of 7,168 bf16: 64 tokens 8.8 us with 128 threads, 5.3 with 512;
+  // 256 11.0 and 9.9; 400 17.3 and 18.7; 1,024 48 and 53)
   const int most = a.T < 2 * n_sm ? 512 : 128;
   const int threads = std::min(most, (pieces + 31) / 32 * 32);
   if (a.T > INT32_MAX) return cudaErrorInvalidValue;

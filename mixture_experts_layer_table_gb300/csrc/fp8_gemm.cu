@@ -13,8 +13,8 @@
 // 8 k + u holds row 4 u + k) these four are neighbours in out, stored together.  Tiles of at most 128 (64) columns put two
 // (four) blocks into an accumulator and hand them over together.
 // What bounds it: few rows a group, DRAM (32 rows on 25 of 64 experts of 7,168 x 2,048 64 us, 5.7 TB/s; 16,384 rows of 128
-// experts of 4,096 x 7,168 720 us, 5.5 TB/s).  Many, the epilogue: a block of 256 columns takes its warps about 1,150 cycles
-// against 520 of MMAs (8,192^3 539 us, 2.04 PFLOP/s; the MMAs alone 246 us, with their loads 338).
+// experts of 4,096 x 7,168 705 us, 5.7 TB/s).  Many, the epilogue: a block of 256 columns takes its warps about 1,150 cycles
+// against 520 of MMAs (8,192^3 534 us, 2.06 PFLOP/s; the MMAs alone 246 us, with their loads 338).
 //
 // Roles of both CTAs of a pair: warp 0 TMA producer, warp 1 MMA issuer (even CTA), warp 2 the scales, warps 4 to 11 epilogue
 // (warp w reads TMEM lane quarter w % 4; the two warps of a quarter take alternate 32-column pieces).  The scales' warp
@@ -185,7 +185,8 @@ __device__ __forceinline__ int f8_scale_at(int c) { return (c >> 4) * 16 + ((c >
 
 // The two scales of a product go to the epilogue as one factor, unless that is no normal f32: it would lose bits that the block's sum
 // may still bring back, or be infinite beside a sum of 0.  Such a column keeps its row's scale, and its sums are
-// multiplied with the weights' one first ("apart"; exact to f32's rounding for scales from 2^-119 on).  Scales of 0, and the quantisers'
+// multiplied with the weights' one first ("apart"; to f32's precision for scales from 2^-119 on), which the epilogue does in TMEM before
+// it takes them (8,192^3 with all columns apart 1,340 us).  Scales of 0, and the quantisers'
 // least one, which stands for zeros (masked tokens' gradients, weights that are off), are left out: what little is lost there
 // stays below 2^-125 a block.  At least F8_NORMALS for scales that meet apart.
 constexpr uint32_t F8_NORMALS = 0x7f000000u;
@@ -478,7 +479,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
               for (int i = 0; i < 8; ++i) worst = max(worst, f8_apart(b[j][i], a4[j][0]));
             apart = __any_sync(0xffffffffu, worst >= F8_NORMALS);
           }
-            ok = __all_sync(0xffffffffu, f8_wait(sempty_bar(q), q_phase ^ 1, abort_flag, args.status, SITE_FP8_SCALES));
+          ok = __all_sync(0xffffffffu, f8_wait(sempty_bar(q), q_phase ^ 1, abort_flag, args.status, SITE_FP8_SCALES));
           if (!ok) break;
 #pragma unroll
           for (int j = 0; j < F8_GROUP; ++j) {
@@ -865,8 +866,7 @@ cudaError_t launch_fp8_matmul(const Fp8MatmulArgs& a, bool bf16_out, int n_sm, c
   if (a.E > 1) tiles = ((a.R + g.nmax - 1) / g.nmax + a.E) * g.MT;  // at most, whatever the groups' sizes
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
   g.magic_per = f8_magic(g.MT);
-  // 8,192 x 8,192 x 8,192 564 -> 541 us with two sums an instruction, but 16,384 rows of 128 groups 713 -> 732 (the narrower
-  // tiles' loop loses registers to the pairs)
+  // 8,192 x 8,192 x 8,192 554 -> 534 us with two sums an instruction, 256 rows a group 186 -> 182; 16,384 rows of 128 groups 711 both
   g.packed = a.R >= 192 * groups;
   CUtensorMap ta, tb[3];
   if (!tmap_a(&ta, a.w, a.K, a.N, a.E, a.w_stride, g.mixed) ||
@@ -903,8 +903,8 @@ cudaError_t launch_fp8_weight_grad(const Fp8WeightGradArgs& a, bool bf16_out, in
   const int64_t nc = (a.N + g.nmax - 1) / g.nmax;
   g.magic_per = f8_magic(nc * g.MT);
   g.magic_nc = f8_magic(nc);
-  // 1,024 rows a group 1,399 -> 1,301 us with two sums an instruction, but 128 rows (one block) 720 -> 793: the sums' pairs cost
-  // the stores moves
+  // 1,024 rows a group 1,321 -> 1,251 us with two sums an instruction, 512 1,731 -> 1,649, but 256 2,251 -> 2,281 and 128 (one block)
+  // 770 -> 858: the sums' pairs cost the stores moves
   g.packed = a.R >= 384 * (int64_t)a.E;
   CUtensorMap ta, tb[3];
   const int64_t P = 128 * g.blocks;
