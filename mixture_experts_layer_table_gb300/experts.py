@@ -476,7 +476,7 @@ def _status_of(t, device) -> Optional[int]:
             return None
         word = torch.zeros(2, dtype=torch.int32, device=t.device)
         _settle(t.device)
-        _STATUS[device] = word
+        word = _STATUS.setdefault(device, word)  # another thread's, if that was first
     return word.data_ptr()
 
 
@@ -492,7 +492,10 @@ def _read_status(word):
 def fp8_status(device=None):
     """(code, site) of the first error on the device (the current one) of ``fp8_weight_grad`` calls without a
     ``device_status``, since the last call; waits for the work of all of its streams."""
-    index = torch.device("cuda" if device is None else device).index
+    device = torch.device("cuda" if device is None else device)
+    if device.type != "cuda":
+        raise ValueError(f"device: expected a CUDA device, got {device}")
+    index = device.index
     word = _STATUS.get(_current_device() if index is None else index)
     return (0, 0) if word is None else _read_status(word)
 

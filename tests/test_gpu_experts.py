@@ -1002,6 +1002,25 @@ def test_the_weight_gradient_has_a_status_word(monkeypatch):
     assert mok.fp8_status() == (5, 43) and mok.fp8_status() == (0, 0)
 
 
+def test_threads_share_the_status_word(monkeypatch):
+    import threading
+    monkeypatch.setattr(X, "_STATUS", {})
+    x, start, got = torch.zeros(1, device="cuda"), threading.Barrier(16), []
+
+    def call():
+        start.wait()
+        got.append(X._status_of(x, 0))
+
+    threads = [threading.Thread(target=call) for _ in range(16)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert got == [X._STATUS[0].data_ptr()] * 16
+    with pytest.raises(ValueError):
+        mok.fp8_status("cpu")
+
+
 def test_two_calls_at_once():
     """The same weights on two streams: nothing is shared between calls."""
     rng = np.random.default_rng(4)
