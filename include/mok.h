@@ -594,7 +594,8 @@ mok_status mok_fp8_matmul(const mok_fp8_matmul_desc* desc, const uint8_t* x, con
                           const float* w_scale, const int32_t* offsets, void* out, int32_t* device_status,
                           void* stream);
 
-/* out[e][n][h] = sum over group e's blocks b of dy_scale[b][n] x_scale[b][h] sum_{r in b} dy[n][r] x[h][r]: the gradient
+/* out[e][n][h] = sum over group e's blocks b of dy_scale[b][n] x_scale[b][h] sum_{r in b} dy[n][r] x[h][r] (a block's sum
+ * meets dy_scale first, and that product has to lie within f32: any dy below 2^112; x may be as large as its type): the gradient
  * of the weights, with dy [N][P], x [H][P] and their scales as qt and qt_scale of mok_fp8_quantize for the same R, E and
  * offsets.  Zeros for a group without rows.  out f32 or bf16 [E][N][H], contiguous.  device_status (or NULL) takes a wait that
  * ran out (MOK_ERR_TIMEOUT); part of out is unwritten then, as of mok_fp8_matmul's. */

@@ -632,16 +632,18 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
                   for (int r = 0; r < 2; ++r) {
                     float2 x = make_float2(__uint_as_float(v[p & 1][4 * j + 2 * r]), __uint_as_float(v[p & 1][4 * j + 2 * r + 1]));
                     float (&to)[2] = sum[p][j][r];
-                    const float rs = WGRAD ? sa[2 * (p & 1) + r] : 1.0f;
+                    float2 by = make_float2(c[j][0], c[j][1]);
+                    if (WGRAD) {  // dy's scales first: x may hold a mask's lowest value, a sum of 448^2 times whose scale is infinite
+                      x = __fmul2_rn(x, by);
+                      by.x = by.y = sa[2 * (p & 1) + r];
+                    }
                     if (PACKED && G == 1) {
-                      if (WGRAD) x = __fmul2_rn(x, make_float2(rs, rs));
-                      const float2 z = __ffma2_rn(x, make_float2(c[j][0], c[j][1]), make_float2(to[0], to[1]));
+                      const float2 z = __ffma2_rn(x, by, make_float2(to[0], to[1]));
                       to[0] = z.x;
                       to[1] = z.y;
                     } else {
-                      if (WGRAD) x = make_float2(x.x * rs, x.y * rs);
-                      to[0] = fmaf(x.x, c[j][0], to[0]);
-                      to[1] = fmaf(x.y, c[j][1], to[1]);
+                      to[0] = fmaf(x.x, by.x, to[0]);
+                      to[1] = fmaf(x.y, by.y, to[1]);
                     }
                   }
                 if (p + 1 < S) tmem_wait_ld();

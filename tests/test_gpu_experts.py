@@ -653,6 +653,24 @@ def test_bad_offsets_stay_in_the_tensors():
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("counts", [[300], [1000, 40], [60, 0, 129]], ids=str)
+def test_weight_grad_of_rows_at_the_types_lowest(counts, dtype):
+    """x holds masks' lowest values, dy what gradients are: the products lie within f32."""
+    rng = np.random.default_rng(sum(counts))
+    N, H = 130, 200
+    offsets = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    R = int(offsets[-1])
+    dy, x = values(rng, (R, N), BF)[0] * 2.0 ** -20, values(rng, (R, H), BF)[0]
+    x[cuda(rng.integers(0, R, 40)), cuda(rng.integers(0, H, 40))] = float(torch.finfo(BF).min)
+    a = mok.fp8_quantize(dy, offsets=cuda(offsets), rows=False)
+    b = mok.fp8_quantize(x, offsets=cuda(offsets), rows=False)
+    want, size = O.weight_grad(f64(a["qt"]), f64(a["qt_scale"]), f64(b["qt"]), f64(b["qt_scale"]), offsets)
+    assert size.max() < 3e38
+    got = mok.fp8_weight_grad(a["qt"], a["qt_scale"], b["qt"], b["qt_scale"], cuda(offsets), dtype=dtype)
+    check_product(f64(got), want, size, max(counts), dtype)
+
+
 class Fenced:
     """A [rows][width] tensor inside of a larger buffer: bytes of 0x5a in front, behind and between the rows."""
 
