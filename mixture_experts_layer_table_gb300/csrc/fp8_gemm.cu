@@ -905,8 +905,8 @@ cudaError_t launch_fp8_weight_grad(const Fp8WeightGradArgs& a, bool bf16_out, in
   const int64_t nc = (a.N + g.nmax - 1) / g.nmax;
   g.magic_per = f8_magic(nc * g.MT);
   g.magic_nc = f8_magic(nc);
-  // 1,024 rows a group 1,321 -> 1,251 us with two sums an instruction, 512 1,731 -> 1,649, but 256 2,251 -> 2,281 and 128 (one block)
-  // 770 -> 858: the sums' pairs cost the stores moves
+  // 1,024 rows a group 1,254 -> 1,231 us with two sums an instruction, 512 1,647 -> 1,624, but 256 2,153 -> 2,266 and 128 (one block)
+  // 760 -> 853: the sums' pairs cost the stores moves
   g.packed = a.R >= 384 * (int64_t)a.E;
   CUtensorMap ta, tb[3];
   const int64_t P = 128 * g.blocks;
